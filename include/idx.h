@@ -106,6 +106,11 @@ enum {
 #define IDX_HEAD_DIM 128
 #define IDX_TOKEN_BYTES 132
 #define IDX_MXFP4_TOKEN_BYTES 68
+#define IDX_KV_LATENT 512            /* the attention cache (see below) */
+#define IDX_KV_ROPE 64
+#define IDX_KV_DIM 576
+#define IDX_KV_TOKEN_BYTES 644
+#define IDX_ATTENTION_MAX_HEADS 1024
 
 /*
  * idx_k_quant_and_cache - quantise k to e4m3 and insert it into the paged cache.
@@ -584,6 +589,164 @@ idx_status_t idx_paged_mqa_topk_decode_noalloc(const uint8_t* q, int64_t ld_q, c
                                                const int32_t* ctx_lens, int32_t B, float* logits,
                                                int64_t ld_logits, int32_t k, int32_t* out,
                                                int64_t ld_out, cudaStream_t stream);
+
+/*
+ * idx_k_norm_rope_quant_and_cache - prepare the indexer's k and insert it into
+ * the paged cache: LayerNorm, partial RoPE and idx_k_quant_and_cache in one pass.
+ *
+ * "DeepSeek V3.2 稀疏注意力 DSA 推理流程图解", "Indexer 内部六步" steps 2, 3 and 5.
+ * Per token, in binary32 (sums of 128 values in any order):
+ *   y = (x - mean(x)) / sqrt(var(x) + eps) * weight + bias   (var of the 128 values);
+ *   dims 0..63 of y rotated by the token's position, as idx_q_rope_quant rotates q;
+ *   scale and e4m3 bytes of y, and their place, as idx_k_quant_and_cache.
+ *
+ *   k, ld_k, n_tok, slot_mapping, cache, num_blocks, block_size,
+ *   block_stride_bytes, scale_fmt: as idx_k_quant_and_cache (a skipped slot
+ *                 skips the token). Inputs must be finite. Each slot at most once
+ *                 per call.
+ *   weight, bias  float [128]; bias may be NULL (0).
+ *   eps           >= 0.
+ *   positions, cos_sin, ld_cs, max_pos, rope_style: as idx_q_rope_quant (cos_sin
+ *                 with any 4-byte alignment). A position outside [0, max_pos)
+ *                 writes the token as zeros and raises the device flag.
+ * Errors: those of the two calls.
+ */
+idx_status_t idx_k_norm_rope_quant_and_cache(const void* k, int k_dtype, int64_t ld_k, int32_t n_tok,
+                                             const float* weight, const float* bias, float eps,
+                                             const int32_t* positions, const float* cos_sin,
+                                             int64_t ld_cs, int32_t max_pos, int32_t rope_style,
+                                             const int64_t* slot_mapping, uint8_t* cache,
+                                             int32_t num_blocks, int32_t block_size,
+                                             int64_t block_stride_bytes, int scale_fmt,
+                                             cudaStream_t stream);
+
+/*
+ * The attention cache
+ * -------------------
+ * The main attention of the layer keeps one latent per token, shared by every
+ * head: 512 latent dims (part of the key, and the value) and 64 rotated position
+ * dims (part of the key only), 576 dims in all ("DeepSeek V3.2 ...", the cost
+ * table). This library stores it in 644 bytes: 512 e4m3 bytes, 64 bf16 values and
+ * four E8M0 scale codes, code j for latent dims 128 j .. 128 j + 127. A latent dim
+ * stands for e4m3 * 2^(code - 127), which a bf16 holds exactly (down to 2^-126).
+ * The scale of 128 dims is the smallest power of two >= amax / 448 (binary32
+ * quotient), its code held to [0, 134]: latents beyond 448 * 2^7 = 57344 saturate.
+ * Split block layout: block b starts at b * block_stride_bytes; token i of it
+ * keeps its e4m3 bytes at 512 i, its position dims at 512 * block_size + 128 i and
+ * its four codes at 640 * block_size + 4 i. block_size is 16, 32, 64 or 128;
+ * block_stride_bytes a multiple of 16, at least block_size * 644 (41472 for 64
+ * tokens is a multiple of 512); the cache 16-byte aligned.
+ */
+
+/*
+ * idx_kv_norm_rope_quant_and_cache - prepare the attention latent and insert it
+ * into the attention cache, in one pass. Per token, in binary32 (the sum of 512
+ * squares in any order):
+ *   y = c / sqrt(mean(c^2) + eps) * weight          (weight NULL: y = c);
+ *   z = pe rotated by the token's position: pairs (i, i + 32) or (2i, 2i + 1), i < 32,
+ *       with the angles of row `position` of cos_sin   (positions NULL: z = pe);
+ *   y quantised as the attention cache defines, z rounded to bf16, both stored.
+ *
+ *   c             [n_tok, 512] of dtype (IDX_BF16 or IDX_F32), ld_c elements
+ *                 between tokens (>= 512); finite.
+ *   pe            [n_tok, 64] of dtype, ld_pe >= 64. Both may be column slices of
+ *                 one [n_tok, 576] projection.
+ *   weight        float [512] or NULL; eps >= 0.
+ *   positions, cos_sin, ld_cs, max_pos, rope_style: as
+ *                 idx_k_norm_rope_quant_and_cache, or positions and cos_sin both
+ *                 NULL. A position outside [0, max_pos) writes the token as zeros
+ *                 and raises the device flag.
+ *   slot_mapping  int64 [n_tok] (block * block_size + offset); a negative slot, or
+ *                 one >= num_blocks * block_size, skips the token. Each slot at
+ *                 most once per call.
+ * Errors: IDX_ERR_INVALID_ARG for NULL pointers with n_tok > 0, negative sizes,
+ * short strides or eps < 0; IDX_ERR_UNSUPPORTED for another dtype, rope_style or
+ * block_size, or a cache outside the layout's alignment.
+ */
+idx_status_t idx_kv_norm_rope_quant_and_cache(const void* c, int64_t ld_c, const void* pe, int64_t ld_pe,
+                                              int dtype, int32_t n_tok, const float* weight, float eps,
+                                              const int32_t* positions, const float* cos_sin,
+                                              int64_t ld_cs, int32_t max_pos, int32_t rope_style,
+                                              const int64_t* slot_mapping, uint8_t* cache,
+                                              int32_t num_blocks, int32_t block_size,
+                                              int64_t block_stride_bytes, cudaStream_t stream);
+
+/*
+ * idx_gather_kv - read tokens of a batch of requests back out of the attention
+ * cache, dequantised and packed: what a prompt's dense attention reads of an
+ * earlier context. Output row r with cu_lens[b] <= r < cu_lens[b + 1] holds token
+ * p = starts[b] + r - cu_lens[b] of request b, found in block
+ * block_table[b, p / block_size] at offset p % block_size: 512 latent dims, then
+ * 64 position dims.
+ *
+ *   block_table  int32 [B, n_pages], row stride ld_bt (>= n_pages).
+ *   starts       int32 [B] or NULL (every request from its first token).
+ *   cu_lens      int32 [B + 1], ascending: the requests' first output rows.
+ *   out          [n_out, 576] of out_dtype (IDX_BF16: exact; IDX_F32), ld_out
+ *                elements between rows (>= 576), rows 16-byte aligned. Rows outside
+ *                [cu_lens[0], cu_lens[B]) are left as they were, and rows of a
+ *                request beyond n_out are not written.
+ * A token whose page index is outside [0, n_pages), or whose block is
+ * outside [0, num_blocks), is written as zeros and raises the device flag.
+ * Errors: IDX_ERR_INVALID_ARG for NULL pointers, negative sizes or short strides;
+ * IDX_ERR_UNSUPPORTED for another out_dtype or block_size, misaligned output
+ * rows, or a cache outside the layout's alignment.
+ */
+idx_status_t idx_gather_kv(const uint8_t* cache, int32_t num_blocks, int32_t block_size,
+                           int64_t block_stride_bytes, const int32_t* block_table, int64_t ld_bt,
+                           int32_t n_pages, const int32_t* starts, const int32_t* cu_lens, int32_t B,
+                           void* out, int out_dtype, int64_t ld_out, int32_t n_out,
+                           cudaStream_t stream);
+
+/*
+ * idx_sparse_attention - attention of each query row over the tokens selected
+ * for it, read from the attention cache through their slots.
+ *
+ * The consumer of the selection ("DeepSeek V3.2 ...", data-flow items 2-3): the
+ * slots are what idx_topk_slots, idx_sparse_topk_remap_slots or
+ * idx_req_to_global_slots write. Row t attends to the tokens of its valid list
+ * entries j < min(k, n_sel[t]) with slots[t, j] >= 0, in any order; a slot listed
+ * twice counts twice. With K_j the token's 576 dims and V_j its first 512,
+ *   s[h, j] = softmax_scale * sum_d q[t, h, d] * K_j[d]
+ *   out[t, h] = sum_j exp(s[h, j]) V_j / sum_j exp(s[h, j])
+ *   lse[t, h] = ln(sum_j exp(s[h, j])).
+ * A row with no valid entry gets out = 0 and lse = -inf. Two such results over
+ * disjoint token sets combine by their lse (context-parallel decode).
+ *
+ * Products of bf16 q and the exactly dequantised token are summed in binary32;
+ * maxima, sums and the output's accumulators are binary32. The weights exp(s) enter
+ * the product with V rounded to bf16 (one rounding, the precision of the output);
+ * the sum in the denominator is of the unrounded ones.
+ *
+ *   q           bf16 [T, H, 576] (512 latent dims first), ld_q elements between rows,
+ *               ld_qh between heads (each >= 576 and a multiple of 8), 16-byte aligned.
+ *   cache       the attention cache; a slot is block * block_span + offset
+ *               (block_span >= block_size, as idx_req_to_global_slots).
+ *   slots       int32 [T, ld_slots], k entries used. An entry >= 0 outside the cache
+ *               is skipped and raises the device flag.
+ *   n_sel       int32 [T] or NULL (all k entries).
+ *   out         bf16 [T, H, 512], ld_out between rows, ld_oh between heads (each
+ *               >= 512 and a multiple of 8), 16-byte aligned.
+ *   lse         float [T, ld_lse] (ld_lse >= H) or NULL.
+ *   ws          NULL, or idx_sparse_attention_workspace_bytes(T, H, k) bytes, 16-byte
+ *               aligned: with it the lists of a few rows are split over the GPU's
+ *               SMs and joined by a second launch; without it every row is one
+ *               block's work. Its contents need no preparation and mean nothing
+ *               after the call; calls that may overlap need one each.
+ * Errors: IDX_ERR_INVALID_ARG for NULL pointers, negative sizes, short strides, a
+ * softmax_scale that is not finite or a workspace that is too small;
+ * IDX_ERR_UNSUPPORTED for more than IDX_ATTENTION_MAX_HEADS heads, misaligned rows,
+ * block_span < block_size or a cache outside the layout's alignment.
+ */
+idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache,
+                                  int32_t num_blocks, int32_t block_size, int64_t block_stride_bytes,
+                                  int32_t block_span, const int32_t* slots, int64_t ld_slots, int32_t k,
+                                  const int32_t* n_sel, int32_t T, int32_t H, float softmax_scale,
+                                  void* out, int64_t ld_out, int64_t ld_oh, float* lse, int64_t ld_lse,
+                                  void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of the optional workspace of idx_sparse_attention on the current device (host only; 0: none is used). */
+size_t idx_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t k);
 
 /*
  * idx_block_span - tokens per physical block of a pool (host only).

@@ -25,4 +25,4 @@ than itself (format definitions, closed forms, brute force, library routines on
 special cases). No function is "parity unpinned".
 """
 
-from . import codecs, indexer  # noqa: F401
+from . import attention, codecs, indexer  # noqa: F401

@@ -21,6 +21,8 @@ __all__ = [
     "idx_mqa_logits_prefill", "idx_mqa_logits_prefill_mxfp4", "idx_paged_mqa_logits_decode", "idx_paged_mqa_logits_decode_mxfp4", "idx_topk", "idx_expand_candidates", "idx_sparse_topk_remap",
     "idx_req_to_global_slots", "idx_dcp_topk_merge", "idx_q_rope_quant", "idx_block_span",
     "idx_workspace_bytes", "idx_device_error", "library",
+    "idx_k_norm_rope_quant_and_cache", "idx_kv_norm_rope_quant_and_cache", "idx_gather_kv", "idx_sparse_attention",
+    "idx_sparse_attention_workspace_bytes",
 ]
 
 
@@ -257,6 +259,173 @@ def idx_req_to_global_slots(local, row_to_req, block_table, block_size, block_sp
     _check("idx_req_to_global_slots", library().idx_req_to_global_slots(
         _ptr(local), _rows(local), local.shape[0], kk, _ptr(row_to_req), _ptr(block_table),
         _rows(block_table), block_size, block_span, _ptr(slots), _rows(slots), _stream(stream)))
+
+
+def _want(fn: str, name: str, t, dev: int, dtype, *shape) -> int:
+    """Device pointer of ``t`` after checking its device, dtype and shape (None: any extent) and that
+    its last dimension is contiguous."""
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} must be a tensor on cuda:{dev}, got one on {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    have = t.shape
+    if len(have) != len(shape):
+        raise ValueError(f"{fn}: {name} must have {len(shape)} dimensions, got {len(have)}")
+    for h, w in zip(have, shape):
+        if w is not None and h != w:
+            raise ValueError(f"{fn}: {name} has shape {tuple(have)}, expected {shape}")
+    if have[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{fn}: {name} must have a unit stride in its last dimension")
+    return t.data_ptr()
+
+
+def _ld(t, n: int) -> int:
+    """Row stride of a 2-D tensor with ``n`` columns; of one row or none, any stride serves."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), n)
+
+
+def _cuda_device(fn: str, name: str, t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+    return dev
+
+
+def _call(fn: str, dev: int, stream, *args) -> None:
+    """Call entry point ``fn`` with ``stream`` (None: torch's current one of the tensors' device) on that device."""
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        if stream.device_index != dev:
+            raise ValueError(f"{fn}: the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{dev}")
+        st = stream.cuda_stream
+    else:
+        st = int(stream)
+    f = getattr(library(), fn)
+    if dev == torch._C._cuda_getDevice():
+        status = f(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, st)
+    if status:
+        _check(fn, status)
+
+
+def _rope_args(fn: str, positions, cos_sin, n: int, dev: int):
+    if (positions is None) != (cos_sin is None):
+        raise ValueError(f"{fn}: positions and cos_sin go together")
+    if positions is None:
+        return None, None, 64, 1
+    p = _want(fn, "positions", positions, dev, torch.int32, n)
+    c = _want(fn, "cos_sin", cos_sin, dev, torch.float32, None, None)
+    if cos_sin.shape[1] < 64:
+        raise ValueError(f"{fn}: cos_sin needs 64 columns, got {cos_sin.shape[1]}")
+    return p, c, _ld(cos_sin, 64), cos_sin.shape[0]
+
+
+def _cache_args(fn: str, cache, dev: int, block_size: int, token_bytes: int):
+    p = _want(fn, "cache", cache, dev, torch.uint8, None, None)
+    if cache.shape[1] < block_size * token_bytes:
+        raise ValueError(f"{fn}: cache blocks of {cache.shape[1]} bytes hold fewer than {block_size} tokens")
+    return p, cache.shape[0], block_size, _ld(cache, cache.shape[1])
+
+
+def idx_k_norm_rope_quant_and_cache(k, weight, bias, eps, positions, cos_sin, slot_mapping, cache, block_size,
+                                    ue8m0=False, interleaved=False, stream=None):
+    """LayerNorm, partial RoPE, e4m3 quantisation and insert of the indexer's k, in one pass.
+
+    k [n, 128] bf16/fp32 (the raw projection), weight / bias fp32 [128] (bias may be None), positions int32
+    [n], cos_sin fp32 [max_pos, >= 64], slot_mapping int64 [n], cache uint8 [num_blocks, block_stride] (the
+    indexer cache of idx_k_quant_and_cache).
+    """
+    fn = "idx_k_norm_rope_quant_and_cache"
+    dev = _cuda_device(fn, "k", k)
+    code = _lib.IDX_BF16 if k.dtype is torch.bfloat16 else _lib.IDX_F32
+    kp = _want(fn, "k", k, dev, torch.bfloat16 if code else torch.float32, None, 128)
+    n = k.shape[0]
+    pos, cs, ld_cs, max_pos = _rope_args(fn, positions, cos_sin, n, dev)
+    _call(fn, dev, stream, kp, code, _ld(k, 128), n, _want(fn, "weight", weight, dev, torch.float32, 128),
+          None if bias is None else _want(fn, "bias", bias, dev, torch.float32, 128), float(eps), pos, cs, ld_cs,
+          max_pos, _lib.IDX_ROPE_INTERLEAVED if interleaved else _lib.IDX_ROPE_NEOX,
+          _want(fn, "slot_mapping", slot_mapping, dev, torch.int64, n), *_cache_args(fn, cache, dev, block_size, 132),
+          _lib.IDX_SCALE_UE8M0 if ue8m0 else _lib.IDX_SCALE_FP32)
+
+
+def idx_kv_norm_rope_quant_and_cache(c, pe, weight, eps, positions, cos_sin, slot_mapping, cache, block_size,
+                                     interleaved=False, stream=None):
+    """RMSNorm, RoPE, e4m3 quantisation and insert of the attention latent, in one pass.
+
+    c [n, 512] and pe [n, 64] bf16/fp32 (column slices of one projection will do), weight fp32 [512] or None
+    (no norm), positions int32 [n] and cos_sin fp32 [max_pos, >= 64] or both None (already rotated),
+    slot_mapping int64 [n], cache uint8 [num_blocks, block_stride] (644 bytes per token).
+    """
+    fn = "idx_kv_norm_rope_quant_and_cache"
+    dev = _cuda_device(fn, "c", c)
+    code = _lib.IDX_BF16 if c.dtype is torch.bfloat16 else _lib.IDX_F32
+    dt = torch.bfloat16 if code else torch.float32
+    cp = _want(fn, "c", c, dev, dt, None, 512)
+    n = c.shape[0]
+    pos, cs, ld_cs, max_pos = _rope_args(fn, positions, cos_sin, n, dev)
+    _call(fn, dev, stream, cp, _ld(c, 512), _want(fn, "pe", pe, dev, dt, n, 64), _ld(pe, 64), code, n,
+          None if weight is None else _want(fn, "weight", weight, dev, torch.float32, 512), float(eps), pos, cs,
+          ld_cs, max_pos, _lib.IDX_ROPE_INTERLEAVED if interleaved else _lib.IDX_ROPE_NEOX,
+          _want(fn, "slot_mapping", slot_mapping, dev, torch.int64, n), *_cache_args(fn, cache, dev, block_size, 644))
+
+
+def idx_gather_kv(cache, block_size, block_table, cu_lens, out, starts=None, stream=None):
+    """Read the tokens of a batch of requests back, dequantised and packed.
+
+    block_table int32 [B, pages], cu_lens int32 [B + 1] (first output row of each request, ascending), starts
+    int32 [B] or None (first token of each request), out [n_out, 576] bf16/fp32; rows past cu_lens[B] are left
+    as they were.
+    """
+    fn = "idx_gather_kv"
+    dev = _cuda_device(fn, "out", out)
+    code = _lib.IDX_BF16 if out.dtype is torch.bfloat16 else _lib.IDX_F32
+    op = _want(fn, "out", out, dev, torch.bfloat16 if code else torch.float32, None, 576)
+    bt = _want(fn, "block_table", block_table, dev, torch.int32, None, None)
+    B = block_table.shape[0]
+    cp, blocks, bs, stride = _cache_args(fn, cache, dev, block_size, 644)
+    if B > 1 and block_table.stride(0) < block_table.shape[1]:
+        raise ValueError(f"{fn}: block_table rows must not overlap")
+    # pages beyond the table's own columns do not exist, whatever its row stride
+    _call(fn, dev, stream, cp, blocks, bs, stride, bt, _ld(block_table, block_table.shape[1]), block_table.shape[1],
+          None if starts is None else _want(fn, "starts", starts, dev, torch.int32, B),
+          _want(fn, "cu_lens", cu_lens, dev, torch.int32, B + 1), B, op, code, _ld(out, 576), out.shape[0])
+
+
+def idx_sparse_attention_workspace_bytes(rows: int, heads: int, topk: int) -> int:
+    """Bytes of the workspace with which idx_sparse_attention splits these rows' lists (0: it would not)."""
+    return library().idx_sparse_attention_workspace_bytes(rows, heads, topk)
+
+
+def idx_sparse_attention(q, cache, block_size, slots, out, softmax_scale, lse=None, n_sel=None, block_span=None,
+                         ws=None, stream=None):
+    """Attention of each query row over the tokens selected for it.
+
+    q bf16 [T, H, 576], cache uint8 [num_blocks, block_stride] (644 bytes per token), slots int32 [T, k] (block *
+    block_span + offset, -1 = empty), out bf16 [T, H, 512], lse fp32 [T, H] or None, n_sel int32 [T] or None (the
+    list entries used), ws: a contiguous tensor of idx_sparse_attention_workspace_bytes(T, H, k) bytes, or None.
+    """
+    fn = "idx_sparse_attention"
+    dev = _cuda_device(fn, "q", q)
+    qp = _want(fn, "q", q, dev, torch.bfloat16, None, None, 576)
+    T, H = q.shape[0], q.shape[1]
+    op = _want(fn, "out", out, dev, torch.bfloat16, T, H, 512)
+    sp = _want(fn, "slots", slots, dev, torch.int32, T, None)
+    k = slots.shape[1]
+    cp, blocks, bs, stride = _cache_args(fn, cache, dev, block_size, 644)
+    wp, wb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"{fn}: ws must be a contiguous tensor on cuda:{dev}")
+        wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(fn, dev, stream, qp, q.stride(0) if T > 1 else 576, q.stride(1) if H > 1 else 576, cp, blocks, bs, stride,
+          block_size if block_span is None else block_span, sp, _ld(slots, k), k,
+          None if n_sel is None else _want(fn, "n_sel", n_sel, dev, torch.int32, T), T, H, float(softmax_scale),
+          op, out.stride(0) if T > 1 else 512, out.stride(1) if H > 1 else 512,
+          None if lse is None else _want(fn, "lse", lse, dev, torch.float32, T, H), 0 if lse is None else _ld(lse, H),
+          wp, wb)
 
 
 def idx_block_span(block_stride: int, token_stride: int) -> int:

@@ -70,6 +70,18 @@ SIGNATURES = {
     "idx_paged_mqa_topk_decode_noalloc": (c_int, [c_ptr, c_i64, c_ptr, c_int, c_i64, c_ptr, c_i32,
                                                   c_i32, c_i64, c_ptr, c_i64, c_ptr, c_i32, c_ptr,
                                                   c_i64, c_i32, c_ptr, c_i64, c_ptr]),
+    "idx_k_norm_rope_quant_and_cache": (c_int, [c_ptr, c_int, c_i64, c_i32, c_ptr, c_ptr, ctypes.c_float, c_ptr,
+                                                c_ptr, c_i64, c_i32, c_i32, c_ptr, c_ptr, c_i32, c_i32, c_i64,
+                                                c_int, c_ptr]),
+    "idx_kv_norm_rope_quant_and_cache": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_int, c_i32, c_ptr, ctypes.c_float,
+                                                 c_ptr, c_ptr, c_i64, c_i32, c_i32, c_ptr, c_ptr, c_i32, c_i32,
+                                                 c_i64, c_ptr]),
+    "idx_gather_kv": (c_int, [c_ptr, c_i32, c_i32, c_i64, c_ptr, c_i64, c_i32, c_ptr, c_ptr, c_i32, c_ptr, c_int, c_i64,
+                              c_i32, c_ptr]),
+    "idx_sparse_attention": (c_int, [c_ptr, c_i64, c_i64, c_ptr, c_i32, c_i32, c_i64, c_i32, c_ptr, c_i64, c_i32,
+                                     c_ptr, c_i32, c_i32, ctypes.c_float, c_ptr, c_i64, c_i64, c_ptr, c_i64,
+                                     c_ptr, c_size, c_ptr]),
+    "idx_sparse_attention_workspace_bytes": (c_size, [c_i32, c_i32, c_i32]),
     "idx_diag_mma_peak": (c_int, [c_int, c_i32, c_i32, ctypes.POINTER(ctypes.c_double), c_ptr]),
     "idx_diag_l2_read": (c_int, [c_ptr, c_i64, c_i32, c_i32, c_ptr]),
     "idx_block_span": (c_int, [c_i64, c_i64, ctypes.POINTER(c_i32)]),

@@ -40,6 +40,8 @@ unsigned int index_ops_read_and_clear_error(cudaStream_t stream, cudaError_t* er
 unsigned int q_rope_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
 unsigned int topk_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
 unsigned int diag_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
+unsigned int kv_cache_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
+unsigned int attention_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -175,6 +177,20 @@ __device__ __forceinline__ uint32_t e4m3x2_of_quotients(float x0, float x1, floa
 // e4m3 code of fl32(x / s) by the division itself (any positive s).
 __device__ __forceinline__ uint32_t e4m3_of_quotient_exact(float x, float s) {
   return __nv_cvt_float_to_fp8(__fdiv_rn(x, s), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The smallest power of two >= s (s a positive binary32 value), the UE8M0
+// scale format: an exact power of two keeps its value, anything else rounds up
+// to the next exponent. 0 stays 0.
+__device__ __forceinline__ float ue8m0_ceil(float s) {
+  const uint32_t b = __float_as_uint(s);
+  if (s == 0.0f) return 0.0f;
+  const uint32_t e = b >> 23;                  // biased exponent (s > 0, finite)
+  if (e == 0) {                                // subnormal: the next power of two above it
+    const int lz = __clz(b);                   // b < 2^23
+    return __uint_as_float(1u << (31 - lz + ((b & (b - 1)) != 0)));
+  }
+  return (b & 0x7FFFFFu) == 0 ? s : __uint_as_float((e + 1) << 23);
 }
 
 // --- tcgen05 -----------------------------------------------------------------

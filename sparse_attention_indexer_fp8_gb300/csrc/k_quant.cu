@@ -43,20 +43,6 @@ __device__ __forceinline__ void load4(const void* k, int64_t ld_k, int tok, int 
   }
 }
 
-// The smallest power of two >= s (s a positive binary32 value), the UE8M0
-// scale format: an exact power of two keeps its value, anything else rounds up
-// to the next exponent. 0 stays 0.
-__device__ __forceinline__ float ue8m0_ceil(float s) {
-  const uint32_t b = __float_as_uint(s);
-  if (s == 0.0f) return 0.0f;
-  const uint32_t e = b >> 23;                  // biased exponent (s > 0, finite)
-  if (e == 0) {                                // subnormal: the next power of two above it
-    const int lz = __clz(b);                   // b < 2^23
-    return __uint_as_float(1u << (31 - lz + ((b & (b - 1)) != 0)));
-  }
-  return (b & 0x7FFFFFu) == 0 ? s : __uint_as_float((e + 1) << 23);
-}
-
 template <bool kBf16>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 k_quant_and_cache_kernel(const void* __restrict__ k, int64_t ld_k, int n_tok, bool vec, bool ue8m0,

@@ -6,7 +6,9 @@ decode step (k insert of the new tokens, paged logits, top-k, slot conversion)
 ``HierarchicalStep`` those of one V4.1 consumer-layer step (candidate
 expansion, sparse logits, sparse top-k with remap, slot conversion), and
 ``DcpDecodeStep`` those of one rank of a context-parallel decode step (scoring
-of the rank's own shard, local top-k with scores, one exchange, merge). Buffers
+of the rank's own shard, local top-k with scores, one exchange, merge).
+``AttentionDecodeStep`` goes from a layer's projections to its attention output
+(both normalised inserts, q preparation, ``DecodeStep``, sparse attention). Buffers
 are allocated once at construction; ``run`` allocates nothing but the exchange's
 receive lists. ``kv="mxfp4"`` selects the MXFP4 indexer cache (the V4.1 format)
 for the cache fill and the decode and hierarchical steps.
@@ -17,9 +19,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (idx_dcp_topk_merge, idx_expand_candidates, idx_k_quant_and_cache, idx_k_quant_and_cache_mxfp4,
-               idx_paged_mqa_logits_decode, idx_paged_mqa_logits_decode_mxfp4, idx_req_to_global_slots,
-               idx_sparse_topk_remap, idx_topk, idx_workspace_bytes)
+from . import (idx_dcp_topk_merge, idx_expand_candidates, idx_k_norm_rope_quant_and_cache, idx_k_quant_and_cache,
+               idx_k_quant_and_cache_mxfp4, idx_kv_norm_rope_quant_and_cache, idx_paged_mqa_logits_decode,
+               idx_paged_mqa_logits_decode_mxfp4, idx_q_rope_quant, idx_req_to_global_slots, idx_sparse_attention,
+               idx_sparse_attention_workspace_bytes, idx_sparse_topk_remap, idx_topk, idx_workspace_bytes)
 from . import workloads as W
 
 
@@ -176,6 +179,53 @@ class HierarchicalStep:
     def run(self, q, w, cache, block_table, ctx_lens, cand, row_ke=None, stream=None):
         self.expand(cand, ctx_lens, row_ke, stream=stream)
         return self.score(q, w, cache, block_table, ctx_lens, stream=stream)
+
+
+class AttentionDecodeStep:
+    """One layer's dense decode step from its projections to the attention output, one query row per request.
+
+    [DSA] data-flow items 1-3: the new token's indexer k and attention latent are
+    normalised, rotated and inserted into their caches, the indexer's q is
+    prepared, ``DecodeStep`` scores and selects, and every head attends to the selected
+    slots. Both caches share block tables and slots. ``run`` allocates nothing.
+    """
+
+    def __init__(self, batch: int, max_ctx: int, heads: int, topk: int = W.TOPK, block_size: int = W.BLOCK_SIZE,
+                 device="cuda", softmax_scale: float = W.ATTN_DIM ** -0.5, eps: float = 1e-6,
+                 interleaved: bool = False):
+        self.block_size, self.softmax_scale, self.eps, self.interleaved = block_size, softmax_scale, eps, interleaved
+        self.indexer = DecodeStep(batch, max_ctx, topk=topk, block_size=block_size, device=device)
+        self.q8 = torch.empty((batch, 64, 128), dtype=torch.uint8, device=device)
+        self.w = torch.empty((batch, 64), dtype=torch.float32, device=device)
+        self.out = torch.empty((batch, heads, 512), dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty((batch, heads), dtype=torch.float32, device=device)
+        with torch.cuda.device(self.out.device):
+            nbytes = idx_sparse_attention_workspace_bytes(batch, heads, topk)
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+    def make_caches(self, num_blocks: int):
+        """Zeroed (indexer, attention) caches of ``num_blocks`` blocks."""
+        return tuple(torch.zeros((num_blocks, stride), dtype=torch.uint8, device=self.out.device)
+                     for stride in (W.block_stride_bytes(self.block_size), W.kv_block_stride_bytes(self.block_size)))
+
+    def insert(self, k, kv, k_weight, k_bias, kv_weight, positions, cos_sin, slots, k_cache, kv_cache, stream=None):
+        """Any number of tokens: indexer k [n, 128] and attention projection [n, 576] into both caches."""
+        idx_k_norm_rope_quant_and_cache(k, k_weight, k_bias, self.eps, positions, cos_sin, slots, k_cache,
+                                        self.block_size, interleaved=self.interleaved, stream=stream)
+        idx_kv_norm_rope_quant_and_cache(kv[:, :512], kv[:, 512:], kv_weight, self.eps, positions, cos_sin, slots,
+                                         kv_cache, self.block_size, interleaved=self.interleaved, stream=stream)
+
+    def run(self, new_k, new_kv, k_weight, k_bias, kv_weight, positions, cos_sin, new_slots, q_index, w_index, q,
+            k_cache, kv_cache, block_table, ctx_lens, stream=None):
+        """``ctx_lens`` count the new token; ``q`` [batch, heads, 576] is the absorbed and rotated query."""
+        self.insert(new_k, new_kv, k_weight, k_bias, kv_weight, positions, cos_sin, new_slots, k_cache, kv_cache,
+                    stream=stream)
+        idx_q_rope_quant(q_index, positions, cos_sin, w_index, self.q8, self.w, 128 ** -0.5, 64 ** -0.5,
+                         interleaved=self.interleaved, stream=stream)
+        slots = self.indexer.run(self.q8, self.w, k_cache, block_table, ctx_lens, stream=stream)
+        idx_sparse_attention(q, kv_cache, self.block_size, slots, self.out, self.softmax_scale, lse=self.lse,
+                             ws=self.ws, stream=stream)
+        return self.out
 
 
 def exchange_candidates(vals: torch.Tensor, idx: torch.Tensor, group=None):

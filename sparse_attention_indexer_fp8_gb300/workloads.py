@@ -45,6 +45,16 @@ def mxfp4_block_stride_bytes(block_size: int = BLOCK_SIZE, align: int = BLOCK_AL
     return (raw + align - 1) // align * align
 
 
+ATTN_DIM = 576               # key dims of the attention cache: 512 latent (the value) + 64 position dims
+KV_TOKEN_BYTES = 644         # 512 e4m3 bytes + 64 bf16 position dims + 4 E8M0 scales
+
+
+def kv_block_stride_bytes(block_size: int = BLOCK_SIZE, align: int = BLOCK_ALIGN) -> int:
+    """Bytes per attention cache block: ``block_size * 644`` rounded up to ``align`` (41472 for 64 tokens)."""
+    raw = block_size * KV_TOKEN_BYTES
+    return (raw + align - 1) // align * align
+
+
 def _gen(seed: int, *stream: int) -> torch.Generator:
     g = torch.Generator()
     s = int(seed)
