@@ -34,102 +34,567 @@ struct AttnParams {
   int64_t ld_out, ld_oh;
   float* lse;
   int64_t ld_lse;
+  int head_blocks, parts, part_tiles;  // groups of 64 heads; parts of a row's list, and the tiles of one
+  float2* ws_ml;                       // [T, head_blocks, parts, 64]: maximum (log2 units) and sum
+  float* ws_o;                         // [T, head_blocks, parts, 64, 512]: accumulators
 };
 
-constexpr int kTile = 32;
-constexpr int kHeadGroup = 8;
-constexpr int kKRow = kKvDim + 1;  // odd row length: a warp's 32 tokens fall into 32 banks
+// ---------------------------------------------------------------------------
+// The kernel
+//
+// One block per (row, group of 64 heads, part of the row's list), one block per SM.
+// Per tile of 64 tokens:
+//   S = Q K^T   64 heads x 64 tokens, 36 steps of K = 16 over the 576 dims
+//   P = exp2(S * scale - m)    the running maximum m of each head in registers
+//   O += P V    64 heads x 512 dims, 4 steps of K = 16 over the 64 tokens, two halves of N = 256
+// with tcgen05.mma.ws (M = 64) in bf16 x bf16 -> fp32. The weight-stationary form is taken
+// because its M = 64 fills all 128 tensor-memory lanes (row r, column half c / (N / 2) in lane
+// r + 64 (c / (N / 2))): O takes 256 columns, where the plain form would take all 512 and leave none
+// for S, and runs at half the rate (N = 256: 128 clocks against 80 on a GB300).
+//
+// Roles: warps 4-11 gather and dequantise the tokens, warp 12 issues the matrix
+// instructions, warps 0-3 do the softmax, the rescaling and the epilogue.
+//
+// Keys and values are one copy in shared memory: a token is a row of nine 128-byte swizzled
+// pieces (64 dims each). Read along the dims it is the K-major B operand of S, read along the
+// tokens the N-major B operand of O. Two tiles of 72 KB are in flight beside Q (72 KB) and P (8 KB).
+//
+// The loaders keep the raw e4m3 bytes of the next tile in registers: as soon as one token's
+// bytes are converted and stored, the same registers take the load of the next tile's token,
+// so HBM latency runs under the conversion and the matrix work without a staging buffer.
+// ---------------------------------------------------------------------------
+constexpr int kHeadsPerBlock = 64;
+constexpr int kTile = 64;
+constexpr int kPieces = kKvDim / 64;             // 128-byte pieces of a token's bf16 row
+constexpr int kPieceBytes = kTile * 128;         // one piece of 64 rows
+constexpr int kTileBytes = kPieces * kPieceBytes;
+constexpr int kStages = 2;
+constexpr int kLoaderWarps = 8;
+constexpr int kTokensPerWarp = kTile / kLoaderWarps;
+constexpr int kMmaWarp = 4 + kLoaderWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kOCols = 256;                      // tensor-memory columns of O; S0 and S1 (32 each) follow
+constexpr int kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kRescaleStep = 8.0f;             // log2: P may reach 2^8 before O is rescaled
 
-__global__ void __launch_bounds__(256) attention_simple_kernel(const AttnParams p) {
-  extern __shared__ float sm[];
-  float* ks = sm;                              // [kTile][kKRow]
-  float* qs = ks + kTile * kKRow;              // [kHeadGroup][kKvDim]
-  float* ps = qs + kHeadGroup * kKvDim;        // [kHeadGroup][kTile]
-  float* corr = ps + kHeadGroup * kTile;       // [kHeadGroup]
-  float* inv = corr + kHeadGroup;              // [kHeadGroup]
-  const int t = blockIdx.x, h0 = blockIdx.y * kHeadGroup;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < kHeadGroup * kKvDim; i += 256) {
-    const int h = h0 + i / kKvDim;
-    qs[i] = h < p.H ? __bfloat162float(p.q[t * p.ld_q + h * p.ld_qh + i % kKvDim]) : 0.f;
+struct Shared {
+  uint64_t q_full, p_full, pv_done, drained;
+  uint64_t k_full[kStages], k_empty[kStages], s_full[2];
+  uint32_t tmem;
+  volatile uint32_t dead;                        // a wait expired: no further wait blocks
+  uint32_t valid[kStages][2];                    // bit t: token t of the tile counts
+  float xchg[2][128];
+};
+
+constexpr int kSmemBytes = kTileBytes * (1 + kStages) + kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
+static_assert(kSmemBytes <= 232448, "shared memory of one block");
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_n_major) {
+  // D fp32 (bits 4-5), A and B bf16 (7-9, 10-12), B's major (16), N >> 3 (17-22), M >> 4 (24-28)
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// N-major operand of 64-element (128-byte) swizzled rows: rows of the K dimension
+// 128 bytes apart, the next 8 of them 1024 bytes on (stride offset), the next 64
+// elements of N a piece on (leading offset).
+__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kPieceBytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Issued by the lane with `issue` set; the whole warp passes here converged, so the
+// descriptors stay in uniform registers.
+__device__ __forceinline__ void mma_ws_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                            uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(acc), "r"(issue)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(issue)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+// Bounded wait. A wait that takes two seconds marks the block dead and raises the device
+// flag; from then on no wait blocks, every role runs its remaining iterations on whatever it
+// finds (all addresses stay in bounds), and the block ends in order.
+__device__ __forceinline__ void wait_bar(Shared& sh, uint64_t* bar, uint32_t parity) {
+  if (!mbar_try_wait(bar, parity)) {
+    const uint64_t t0 = global_timer_ns();
+    while (!sh.dead && !mbar_try_wait(bar, parity)) {
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        atomicOr(&g_attention_error, 2u);
+        sh.dead = 1;
+      }
+    }
   }
+  __syncwarp();
+}
+
+// One look at a barrier, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// A list entry: where its token's block starts, its offset in the block, whether it counts.
+struct Token {
+  int64_t block;
+  int off;
+  bool ok;
+};
+
+__device__ __forceinline__ Token locate(const AttnParams& p, int slot) {
+  Token t{0, 0, slot >= 0};
+  if (t.ok) {
+    const int blk = slot / p.block_span;
+    t.off = slot - blk * p.block_span;
+    if (blk >= p.num_blocks || t.off >= p.block_size) {
+      atomicOr(&g_attention_error, 1u);
+      t.ok = false;
+      t.off = 0;
+    } else {
+      t.block = blk * p.block_stride;
+    }
+  }
+  return t;
+}
+
+template <bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* q_s = smem;
+  uint8_t* k_s = smem + kTileBytes;
+  uint8_t* p_s = k_s + kStages * kTileBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(p_s + kPieceBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // head groups vary fastest: the blocks that read the same tokens run side by side
+  const int hb = blockIdx.x % p.head_blocks;
+  const int part = kSplit ? (blockIdx.x / p.head_blocks) % p.parts : 0;
+  const int row = blockIdx.x / (p.head_blocks * p.parts);
+  const int h0 = hb * kHeadsPerBlock;
   int n = p.k;
-  if (p.n_sel) n = min(n, max(__ldg(p.n_sel + t), 0));
-  float m = -INFINITY, l = 0.f;  // of head h0 + warp
-  float acc[kHeadGroup][2] = {};
-  for (int base = 0; base < n; base += kTile) {
-    __syncthreads();
-    for (int j = warp; j < kTile; j += 8) {
-      int slot = base + j < n ? __ldg(p.slots + t * p.ld_slots + base + j) : -1;
-      bool ok = slot >= 0;
-      int blk = 0, off = 0;
-      if (ok) {
-        blk = slot / p.block_span;
-        off = slot - blk * p.block_span;
-        if (blk >= p.num_blocks || off >= p.block_size) {
-          ok = false;
-          if (lane == 0) atomicOr(&g_attention_error, 1u);
+  if (p.n_sel) n = min(n, max(__ldg(p.n_sel + row), 0));
+  const int first = part * p.part_tiles * kTile;  // of this block's entries
+  if (kSplit) n = min(n, first + p.part_tiles * kTile);
+  const int tiles = n > first ? (n - first + kTile - 1) / kTile : 0;
+
+  const int64_t ws_row = (static_cast<int64_t>(row) * p.head_blocks + hb) * p.parts + part;
+  if (tiles == 0) {
+    if (kSplit) {
+      if (tid < kHeadsPerBlock) p.ws_ml[ws_row * kHeadsPerBlock + tid] = make_float2(-INFINITY, 0.f);
+    } else {
+      const int heads = min(kHeadsPerBlock, p.H - h0);
+      for (int i = tid; i < heads * (kKvLatent / 8); i += kThreads) {
+        const int h = h0 + i / (kKvLatent / 8);
+        *reinterpret_cast<uint4*>(p.out + row * p.ld_out + h * p.ld_oh + 8 * (i % (kKvLatent / 8))) =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (p.lse && tid < heads) p.lse[row * p.ld_lse + h0 + tid] = -INFINITY;
+    }
+    return;
+  }
+
+  if (tid == 0) {
+    mbar_init(&sh.q_full, 4);
+    mbar_init(&sh.p_full, 4);
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.drained, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.k_full[i], kLoaderWarps);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+    }
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sh.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp >= 4 && warp < kMmaWarp) {
+    // ---------------------------------------------------------------- loaders
+    const int lw = warp - 4;
+    const int32_t* list = p.slots + row * p.ld_slots + first;
+    const int count = n - first;
+    const int mine = kTokensPerWarp * lw + (lane & 7);  // entry of a tile that this lane locates
+    auto entry = [&](int tile) { return tile * kTile + mine < count ? __ldg(list + tile * kTile + mine) : -1; };
+    const int piece = lane >> 2;                        // lane l holds dims 16 l .. 16 l + 15
+    const bool odd = piece & 1;  // odd pieces store their halves in the other order: no bank conflict
+    const int rope_token = lane >> 3, rope_unit = lane & 7;
+
+    uint4 raw[kTokensPerWarp], rope[2];
+    uint32_t codes;
+    Token tok = locate(p, entry(0));
+    int next_slot = entry(1);
+    auto load_values = [&](int j) {
+      const int64_t blk = __shfl_sync(0xFFFFFFFFu, tok.block, j);
+      const int off = __shfl_sync(0xFFFFFFFFu, tok.off, j);
+      const bool ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(tok.ok), j);
+      return ok ? __ldg(reinterpret_cast<const uint4*>(p.cache + blk + off * kKvLatent + 16 * lane))
+                : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_rope = [&](int i) {
+      const int j = rope_token + 4 * i;
+      const int64_t blk = __shfl_sync(0xFFFFFFFFu, tok.block, j);
+      const int off = __shfl_sync(0xFFFFFFFFu, tok.off, j);
+      const bool ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(tok.ok), j);
+      return ok ? __ldg(reinterpret_cast<const uint4*>(p.cache + blk + p.block_size * kKvRopeAt + off * 128 +
+                                                       16 * rope_unit))
+                : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_codes = [&]() {
+      return tok.ok ? __ldg(reinterpret_cast<const uint32_t*>(p.cache + tok.block + p.block_size * kKvScaleAt +
+                                                              4 * tok.off))
+                    : 0u;
+    };
+    codes = load_codes();
+#pragma unroll
+    for (int j = 0; j < kTokensPerWarp; ++j) raw[j] = load_values(j);
+    rope[0] = load_rope(0);
+    rope[1] = load_rope(1);
+    uint32_t valid = __ballot_sync(0xFFFFFFFFu, tok.ok) & 0xFFu;
+
+    for (int i = 0; i < tiles; ++i) {
+      const int st = i & 1;
+      tok = locate(p, next_slot);  // entries past the list are -1: nothing is loaded for them
+      next_slot = entry(i + 2);
+      const uint32_t next_codes = load_codes();
+      if (i >= kStages) wait_bar(sh, &sh.k_empty[st], ((i >> 1) - 1) & 1);
+      uint8_t* tile = k_s + st * kTileBytes;
+      if (lane == 0) reinterpret_cast<uint8_t*>(sh.valid[st])[lw] = static_cast<uint8_t>(valid);
+#pragma unroll
+      for (int j = 0; j < kTokensPerWarp; ++j) {
+        const uint32_t word = __shfl_sync(0xFFFFFFFFu, codes, j);
+        const uint32_t mul = kv_dequant_multiplier((word >> (8 * (lane >> 3))) & 0xFFu);
+        const uint4 r = raw[j];
+        uint4 a, b;
+        kv_dequant4(odd ? r.z : r.x, mul, a.x, a.y);
+        kv_dequant4(odd ? r.w : r.y, mul, a.z, a.w);
+        kv_dequant4(odd ? r.x : r.z, mul, b.x, b.y);
+        kv_dequant4(odd ? r.y : r.w, mul, b.z, b.w);
+        raw[j] = load_values(j);
+        const int t = kTokensPerWarp * lw + j;  // t & 7 == j
+        uint8_t* line = tile + piece * kPieceBytes + t * 128;
+        const int u = 2 * (lane & 3) + (odd ? 1 : 0);
+        *reinterpret_cast<uint4*>(line + ((u ^ j) << 4)) = a;
+        *reinterpret_cast<uint4*>(line + (((u ^ 1) ^ j) << 4)) = b;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = kTokensPerWarp * lw + rope_token + 4 * h;
+        *reinterpret_cast<uint4*>(tile + (kPieces - 1) * kPieceBytes + t * 128 + ((rope_unit ^ (t & 7)) << 4)) = rope[h];
+        rope[h] = load_rope(h);
+      }
+      codes = next_codes;
+      valid = __ballot_sync(0xFFFFFFFFu, tok.ok) & 0xFFu;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full[st]);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- matrix instructions
+    // Whichever of the next S and the next O product has its operands goes first, O before S:
+    // O's completion is what frees a tile.
+    const uint32_t lead = lane == 0;
+    const uint64_t q_desc = sw128_kmajor_desc(smem_u32(q_s));
+    const uint64_t p_desc = sw128_kmajor_desc(smem_u32(p_s));
+    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(k_s));
+    const uint64_t v_desc = sw128_nmajor_desc(smem_u32(k_s));
+    wait_bar(sh, &sh.q_full, 0);
+    const int total = __shfl_sync(0xFFFFFFFFu, tiles, 0);
+    int s_next = 0, o_next = 0;
+    uint64_t t0 = global_timer_ns();
+    int idle = 0;
+    while (o_next < total) {
+      const bool can_o = o_next < s_next && mbar_test(&sh.p_full, o_next & 1);
+      if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(can_o), 0)) {
+        tc_fence_after();
+        const int st = o_next & 1;
+        const uint64_t v = v_desc + st * (kTileBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            mma_ws_bf16(tmem + half * (kOCols / 2), p_desc + 2 * ks, v + ((4 * half * kPieceBytes + 2048 * ks) >> 4),
+                        idesc_bf16(64, 256, true), o_next > 0 || ks > 0, lead);
+          }
+        }
+        commit_if(&sh.k_empty[st], lead);
+        commit_if(&sh.pv_done, lead);
+        ++o_next;
+        idle = 0;
+        continue;
+      }
+      const bool can_s = s_next < total && s_next - o_next < kStages &&
+                         mbar_test(&sh.k_full[s_next & 1], (s_next >> 1) & 1);
+      if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(can_s), 0)) {
+        tc_fence_after();
+        const int st = s_next & 1;
+        const uint64_t k = k_desc + st * (kTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            mma_ws_bf16(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks,
+                        k + ((c * kPieceBytes) >> 4) + 2 * ks, idesc_bf16(64, 64, false), c > 0 || ks > 0, lead);
+          }
+        }
+        commit_if(&sh.s_full[st], lead);
+        ++s_next;
+        idle = 0;
+        continue;
+      }
+      // nothing was ready: the limit of two seconds runs from the first such pass
+      if (idle++ == 0) t0 = global_timer_ns();
+      bool expired = sh.dead != 0;
+      if (!expired && (idle & 63) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
+        expired = true;
+        atomicOr(&g_attention_error, 2u);
+        sh.dead = 1;
+      }
+      if (__any_sync(0xFFFFFFFFu, expired)) break;
+    }
+    if (o_next < total) {  // given up: whatever was issued finishes before the tensor memory is freed
+      commit_if(&sh.drained, lead);
+      t0 = global_timer_ns();
+      while (!mbar_test(&sh.drained, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax and epilogue
+    // Q: rows of heads past the last one are zero
+    for (int i = tid; i < kHeadsPerBlock * (kKvDim / 8); i += 128) {
+      const int r = i / (kKvDim / 8), u = i % (kKvDim / 8);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (h0 + r < p.H) v = __ldg(reinterpret_cast<const uint4*>(p.q + row * p.ld_q + (h0 + r) * p.ld_qh + 8 * u));
+      *reinterpret_cast<uint4*>(q_s + (u >> 3) * kPieceBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_full);
+
+    const int r = tid & 63, half = tid >> 6;          // head of the group, and half of the tile's tokens
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    float m = -INFINITY, l = 0.f;                     // maximum (log2 units) that P and O refer to; this half's sum
+    for (int i = 0; i < tiles; ++i) {
+      const int st = i & 1;
+      wait_bar(sh, &sh.s_full[st], (i >> 1) & 1);
+      wait_bar(sh, &sh.k_full[st], (i >> 1) & 1);     // long complete; orders this read of `valid` after the loaders
+      tc_fence_after();
+      uint32_t v[32];
+      tmem_ld_x32(lanes + kOCols + st * 32, v);
+      const uint32_t valid = sh.valid[st][half];
+      tmem_wait_ld(v);
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float s = (valid >> c) & 1u ? __uint_as_float(v[c]) * p.scale_log2 : -INFINITY;
+        v[c] = __float_as_uint(s);
+        top = fmaxf(top, s);
+      }
+      sh.xchg[st][tid] = top;
+      softmax_bar();
+      top = fmaxf(top, sh.xchg[st][tid ^ 64]);
+      // P and O keep an old reference until the maximum has risen by 2^8: P stays finite and
+      // its relative precision is the same, and most tiles leave O alone
+      const bool rise = top > m + kRescaleStep || (m == -INFINITY && top > -INFINITY);
+      const float m_new = rise ? top : m;
+      if (i > 0) {
+        wait_bar(sh, &sh.pv_done, (i - 1) & 1);       // P is free, and O complete up to the last tile
+        if (__any_sync(0xFFFFFFFFu, rise)) {
+          tc_fence_after();
+          const float f = rise ? exp2_approx(m - m_new) : 1.0f;  // m = -inf: 0, and O is 0
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < kOCols; c += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(lanes + c, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st_x32(lanes + c, o);
+          }
+          tmem_wait_st();
         }
       }
-      if (lane == 0) ps[j] = ok ? 1.f : 0.f;
-      const uint8_t* b = p.cache + blk * p.block_stride;
-      uint32_t codes = ok ? __ldg(reinterpret_cast<const uint32_t*>(b + p.block_size * kKvScaleAt + 4 * off)) : 0u;
-      for (int d = 4 * lane; d < kKvLatent; d += 128) {
-        uint32_t w = ok ? __ldg(reinterpret_cast<const uint32_t*>(b + off * kKvLatent + d)) : 0u, lo, hi;
-        kv_dequant4(w, kv_dequant_multiplier((codes >> (8 * (d / 128))) & 0xFFu), lo, hi);
-        ks[j * kKRow + d] = __uint_as_float(lo << 16);
-        ks[j * kKRow + d + 1] = __uint_as_float(lo & 0xFFFF0000u);
-        ks[j * kKRow + d + 2] = __uint_as_float(hi << 16);
-        ks[j * kKRow + d + 3] = __uint_as_float(hi & 0xFFFF0000u);
+      m = m_new;
+      const float ref = m == -INFINITY ? 0.f : m;
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const float e0 = exp2_approx(__uint_as_float(v[c]) - ref), e1 = exp2_approx(__uint_as_float(v[c + 1]) - ref);
+        l += e0 + e1;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+        w[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
-      uint32_t w = ok ? __ldg(reinterpret_cast<const uint32_t*>(b + p.block_size * kKvRopeAt + off * 128 + 4 * lane)) : 0u;
-      ks[j * kKRow + kKvLatent + 2 * lane] = __uint_as_float(w << 16);
-      ks[j * kKRow + kKvLatent + 2 * lane + 1] = __uint_as_float(w & 0xFFFF0000u);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        *reinterpret_cast<uint4*>(p_s + r * 128 + (((4 * half + c) ^ (r & 7)) << 4)) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full);
     }
-    __syncthreads();
-    const bool ok = ps[lane] != 0.f;
-    float s = 0.f;
-    for (int d = 0; d < kKvDim; ++d) s = fmaf(qs[warp * kKvDim + d], ks[lane * kKRow + d], s);
-    s = ok ? s * p.scale_log2 : -INFINITY;
-    float top = s;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float m2 = fmaxf(m, top);
-    const float e = ok ? exp2f(s - m2) : 0.f;
-    float sum = e;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const float c = m == -INFINITY ? 0.f : exp2f(m - m2);
-    l = l * c + sum;
-    m = m2;
-    __syncthreads();
-    ps[warp * kTile + lane] = e;
-    if (lane == 0) corr[warp] = c;
-    __syncthreads();
-    for (int h = 0; h < kHeadGroup; ++h) {
-      acc[h][0] *= corr[h];
-      acc[h][1] *= corr[h];
-      for (int j = 0; j < kTile; ++j) {
-        const float w = ps[h * kTile + j];
-        acc[h][0] = fmaf(w, ks[j * kKRow + 2 * tid], acc[h][0]);
-        acc[h][1] = fmaf(w, ks[j * kKRow + 2 * tid + 1], acc[h][1]);
+    wait_bar(sh, &sh.pv_done, (tiles - 1) & 1);
+    tc_fence_after();
+    softmax_bar();
+    sh.xchg[0][tid] = l;
+    softmax_bar();
+    l += sh.xchg[0][tid ^ 64];
+    const int h = h0 + r;
+    if (kSplit) {
+      if (half == 0) p.ws_ml[ws_row * kHeadsPerBlock + r] = make_float2(m, l);
+    } else if (p.lse && half == 0 && h < p.H) {
+      p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll 1
+    for (int c = 0; c < kOCols; c += 32) {
+      uint32_t o[32];
+      tmem_ld_x32(lanes + c, o);
+      tmem_wait_ld(o);
+      // columns 0..127 are dims 128 half .. of the first 256, columns 128..255 of the second
+      const int dim = (c / 128) * 256 + half * 128 + (c % 128);
+      if (h >= p.H) {
+        // no head: nothing to store
+      } else if (kSplit) {
+        float4* dst = reinterpret_cast<float4*>(p.ws_o + (ws_row * kHeadsPerBlock + r) * kKvLatent + dim);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+                               __uint_as_float(o[4 * j + 3]));
+        }
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.ld_out + h * p.ld_oh + dim);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * x]) * inv,
+                                                           __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
+            w[x] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
+      __syncwarp();
     }
   }
+  tc_fence_before();
   __syncthreads();
-  if (lane == 0) {
-    inv[warp] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-    if (p.lse && h0 + warp < p.H) {
-      p.lse[t * p.ld_lse + h0 + warp] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-    }
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the parts of each (row, head): weights 2^(m_i - max m), a part without a valid token
+// skipped (its accumulators were never written). One block per head, one float4 per thread and part.
+__global__ void __launch_bounds__(kKvLatent / 4) attention_join_kernel(const AttnParams p) {
+  const int row = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  const int64_t base = (static_cast<int64_t>(row) * p.head_blocks + h / kHeadsPerBlock) * p.parts;
+  const int r = h % kHeadsPerBlock;
+  float m = -INFINITY;
+  for (int i = 0; i < p.parts; ++i) m = fmaxf(m, __ldg(&p.ws_ml[(base + i) * kHeadsPerBlock + r].x));
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < p.parts; ++i) {
+    const float2 ml = __ldg(&p.ws_ml[(base + i) * kHeadsPerBlock + r]);
+    if (ml.y == 0.f) continue;
+    const float w = exp2f(ml.x - m);
+    const float4 o = __ldg(reinterpret_cast<const float4*>(p.ws_o + ((base + i) * kHeadsPerBlock + r) * kKvLatent) +
+                           threadIdx.x);
+    l = fmaf(w, ml.y, l);
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
   }
-  __syncthreads();
-  for (int h = 0; h < kHeadGroup && h0 + h < p.H; ++h) {
-    __nv_bfloat16* o = p.out + t * p.ld_out + (h0 + h) * p.ld_oh + 2 * tid;
-    o[0] = __float2bfloat16_rn(acc[h][0] * inv[h]);
-    o[1] = __float2bfloat16_rn(acc[h][1] * inv[h]);
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.out + row * p.ld_out + h * p.ld_oh + 4 * threadIdx.x) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (p.lse && threadIdx.x == 0) {
+    p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
-constexpr int kSimpleSmem = (kTile * kKRow + kHeadGroup * kKvDim + kHeadGroup * kTile + 2 * kHeadGroup) * 4;
+// Parts that a list of k entries is split into: the number that minimises the waves of
+// blocks times the tiles of one (a block's start and end cost about three tiles), the join
+// counted as three more tiles. One part when the rows alone fill the GPU.
+int attention_parts(int64_t blocks, int k, int sms) {
+  const int tiles = (k + kTile - 1) / kTile;
+  if (sms <= 0 || tiles <= 1 || blocks >= sms) return 1;
+  int best = 1;
+  int64_t best_cost = (blocks + sms - 1) / sms * (tiles + 3);
+  for (int parts = 2; parts <= tiles && blocks * parts <= 2 * sms; ++parts) {
+    const int per = (tiles + parts - 1) / parts;
+    if ((tiles + per - 1) / per != parts) continue;  // no part without tiles
+    const int64_t cost = (blocks * parts + sms - 1) / sms * (per + 3) + 3;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = parts;
+    }
+  }
+  return best;
+}
+
+int64_t part_bytes() { return kHeadsPerBlock * (static_cast<int64_t>(kKvLatent) * 4 + 8); }
 
 }  // namespace
 
@@ -149,10 +614,10 @@ unsigned int attention_read_and_clear_error(cudaStream_t stream, cudaError_t* er
 using namespace idx;
 
 extern "C" size_t idx_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t k) {
-  (void)T;
-  (void)H;
-  (void)k;
-  return 0;
+  if (T <= 0 || H <= 0 || k <= 0 || k > (1 << 30)) return 0;
+  const int64_t blocks = static_cast<int64_t>(T) * ((H + kHeadsPerBlock - 1) / kHeadsPerBlock);
+  const int parts = attention_parts(blocks, k, device_sm_count());
+  return parts == 1 ? 0 : static_cast<size_t>(blocks * parts * part_bytes());
 }
 
 extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache,
@@ -162,9 +627,8 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
                                              void* out, int64_t ld_out, int64_t ld_oh, float* lse, int64_t ld_lse,
                                              void* ws, size_t ws_bytes, cudaStream_t stream) {
   const char* fn = "idx_sparse_attention";
-  (void)ws;
-  (void)ws_bytes;
   if (T < 0 || H < 0 || k < 0) return fail(IDX_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (k > (1 << 30)) return fail(IDX_ERR_UNSUPPORTED, "%s: lists of %d entries", fn, k);
   if (H > IDX_ATTENTION_MAX_HEADS) return fail(IDX_ERR_UNSUPPORTED, "%s: %d heads", fn, H);
   if (ld_slots < k || ld_q < kKvDim || ld_qh < kKvDim || ld_out < kKvLatent || ld_oh < kKvLatent || (lse && ld_lse < H)) {
     return fail(IDX_ERR_INVALID_ARG, "%s: a stride is smaller than its row", fn);
@@ -179,11 +643,52 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
     return fail(IDX_ERR_UNSUPPORTED, "%s: q and out rows must be 16-byte aligned", fn);
   }
   if (ws && !aligned(ws, 16)) return fail(IDX_ERR_UNSUPPORTED, "%s: the workspace is not 16-byte aligned", fn);
-  AttnParams p{static_cast<const __nv_bfloat16*>(q), ld_q, ld_qh, cache, num_blocks, block_size, block_span,
-               block_stride_bytes, slots, ld_slots, k, n_sel, T, H, softmax_scale * 1.4426950408889634f,
-               static_cast<__nv_bfloat16*>(out), ld_out, ld_oh, lse, ld_lse};
-  cudaError_t e = cudaFuncSetAttribute(attention_simple_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSimpleSmem);
+  const int sms = device_sm_count();
+  if (sms <= 0) return fail(IDX_ERR_CUDA, "%s: cannot query the SM count", fn);
+  AttnParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.ld_q = ld_q;
+  p.ld_qh = ld_qh;
+  p.cache = cache;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.block_span = block_span;
+  p.block_stride = block_stride_bytes;
+  p.slots = slots;
+  p.ld_slots = ld_slots;
+  p.k = k;
+  p.n_sel = n_sel;
+  p.T = T;
+  p.H = H;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ld_out = ld_out;
+  p.ld_oh = ld_oh;
+  p.lse = lse;
+  p.ld_lse = ld_lse;
+  p.head_blocks = (H + kHeadsPerBlock - 1) / kHeadsPerBlock;
+  const int64_t blocks = static_cast<int64_t>(T) * p.head_blocks;
+  p.parts = ws ? attention_parts(blocks, k, sms) : 1;
+  const int tiles = (k + kTile - 1) / kTile;
+  p.part_tiles = (tiles + p.parts - 1) / p.parts;
+  if (blocks * p.parts > INT32_MAX || static_cast<int64_t>(T) * H > INT32_MAX) {
+    return fail(IDX_ERR_UNSUPPORTED, "%s: %d rows of %d heads", fn, T, H);
+  }
+  const unsigned grid = static_cast<unsigned>(blocks * p.parts);
+  if (p.parts > 1) {
+    if (ws_bytes < static_cast<size_t>(blocks * p.parts * part_bytes())) {
+      return fail(IDX_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %lld are needed", fn, ws_bytes,
+                  static_cast<long long>(blocks * p.parts * part_bytes()));
+    }
+    p.ws_o = static_cast<float*>(ws);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + blocks * p.parts * kHeadsPerBlock * kKvLatent);
+  }
+  auto* kernel = p.parts > 1 ? attention_kernel<true> : attention_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-  attention_simple_kernel<<<dim3(T, (H + kHeadGroup - 1) / kHeadGroup), 256, kSimpleSmem, stream>>>(p);
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
+  st = check_launch(fn);
+  if (st != IDX_OK || p.parts == 1) return st;
+  attention_join_kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * H), kKvLatent / 4, 0, stream>>>(p);
   return check_launch(fn);
 }

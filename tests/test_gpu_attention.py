@@ -296,6 +296,8 @@ def test_attention(T, H, K, bs, amp, ws):
     out = torch.full((T, H, 512), 9.0, dtype=torch.bfloat16, device=DEV)
     lse = torch.full((T, H), 9.0, device=DEV)
     w = workspace(T, H, K) if ws else None
+    if ws and K >= 512 and T == 1:
+        assert w is not None                                       # a single long row is split
     idx.idx_sparse_attention(dev(q.view(np.int16)).view(torch.bfloat16), dev(cache), bs, dev(slots), out, 576 ** -0.5,
                              lse=lse, ws=w)
     idx.idx_device_error()
@@ -423,11 +425,15 @@ def test_attention_repeats_bit_for_bit_on_streams_and_in_graphs():
     idx.idx_device_error()
 
 
-def test_wrong_tensors_are_refused():
+def test_small_workspace_and_wrong_tensors_are_refused():
     T, H, K = 1, 64, 2048
     cache, slots, q = attention_case(31, T, H, K, 64)
     qd, cd, sd = dev(q.view(np.int16)).view(torch.bfloat16), dev(cache), dev(slots)
     out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=DEV)
+    n = idx.idx_sparse_attention_workspace_bytes(T, H, K)
+    assert n > 0
+    with pytest.raises(idx.IdxError, match="workspace"):
+        idx.idx_sparse_attention(qd, cd, 64, sd, out, 0.05, ws=torch.empty(n - 16, dtype=torch.uint8, device=DEV))
     for bad in (dict(out=out.float()), dict(out=out[:, :32]), dict(slots=sd.long()), dict(q=qd.float()),
                 dict(lse=torch.empty((T, H + 1), device=DEV)), dict(n_sel=torch.zeros(T + 1, dtype=torch.int32, device=DEV)),
                 dict(cache=cd.cpu())):
