@@ -59,9 +59,11 @@ struct AttnParams {
 // pieces (64 dims each). Read along the dims it is the K-major B operand of S, read along the
 // tokens the N-major B operand of O. Two tiles of 72 KB are in flight beside Q (72 KB) and P (8 KB).
 //
-// The loaders keep the raw e4m3 bytes of the next tile in registers: as soon as one token's
-// bytes are converted and stored, the same registers take the load of the next tile's token,
-// so HBM latency runs under the conversion and the matrix work without a staging buffer.
+// Two groups of four loader warps own a stage each. A group converts and stores its tile, then
+// issues every load of its next one at once, into registers: HBM latency runs under the other
+// group's conversion and the matrix work, with no staging buffer. (One group that refilled each
+// register right after its conversion measured 7000 clocks a tile: loads of two tiles shared
+// scoreboards, so every conversion waited for the newest load.)
 // ---------------------------------------------------------------------------
 constexpr int kHeadsPerBlock = 64;
 constexpr int kTile = 64;
@@ -70,7 +72,8 @@ constexpr int kPieceBytes = kTile * 128;         // one piece of 64 rows
 constexpr int kTileBytes = kPieces * kPieceBytes;
 constexpr int kStages = 2;
 constexpr int kLoaderWarps = 8;
-constexpr int kTokensPerWarp = kTile / kLoaderWarps;
+constexpr int kGroupWarps = kLoaderWarps / kStages;  // each stage has its own group of loader warps
+constexpr int kTokensPerWarp = kTile / kGroupWarps;
 constexpr int kMmaWarp = 4 + kLoaderWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kOCols = 256;                      // tensor-memory columns of O; S0 and S1 (32 each) follow
@@ -180,26 +183,56 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// A list entry: where its token's block starts, its offset in the block, whether it counts.
+// 16 bytes of the cache, or zeros. Volatile: the load is issued where it stands, a tile ahead of its use.
+__device__ __forceinline__ uint4 load16_if(const uint8_t* ptr, bool ok) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(ptr), "r"(static_cast<int>(ok)));
+  return v;
+}
+
+__device__ __forceinline__ uint2 load8_if(const uint8_t* ptr, bool ok) {
+  uint2 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y)
+      : "l"(ptr), "r"(static_cast<int>(ok)));
+  return v;
+}
+
+__device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* ptr, int lane) {
+  return reinterpret_cast<const uint8_t*>(
+      __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(ptr), lane));
+}
+
+// Where the token of a list entry lies; all null for an entry that does not count.
 struct Token {
-  int64_t block;
-  int off;
-  bool ok;
+  const uint8_t* latent;
+  const uint8_t* rope;
+  const uint32_t* codes;
 };
 
 __device__ __forceinline__ Token locate(const AttnParams& p, int slot) {
-  Token t{0, 0, slot >= 0};
-  if (t.ok) {
-    const int blk = slot / p.block_span;
-    t.off = slot - blk * p.block_span;
-    if (blk >= p.num_blocks || t.off >= p.block_size) {
-      atomicOr(&g_attention_error, 1u);
-      t.ok = false;
-      t.off = 0;
-    } else {
-      t.block = blk * p.block_stride;
-    }
+  Token t{nullptr, nullptr, nullptr};
+  if (slot < 0) return t;
+  const int blk = slot / p.block_span;
+  const int off = slot - blk * p.block_span;
+  if (blk >= p.num_blocks || off >= p.block_size) {
+    atomicOr(&g_attention_error, 1u);
+    return t;
   }
+  const uint8_t* base = p.cache + blk * p.block_stride;
+  t.latent = base + off * kKvLatent;
+  t.rope = base + p.block_size * kKvRopeAt + off * (2 * kKvRope);
+  t.codes = reinterpret_cast<const uint32_t*>(base + p.block_size * kKvScaleAt + 4 * off);
   return t;
 }
 
@@ -246,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.drained, 1);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.k_full[i], kLoaderWarps);
+      mbar_init(&sh.k_full[i], kGroupWarps);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
     }
@@ -264,89 +297,75 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 
   if (warp >= 4 && warp < kMmaWarp) {
     // ---------------------------------------------------------------- loaders
-    const int lw = warp - 4;
+    const int group = (warp - 4) / kGroupWarps, lw = (warp - 4) % kGroupWarps;  // this group's tiles: group, group + 2, ...
     const int32_t* list = p.slots + row * p.ld_slots + first;
     const int count = n - first;
-    const int mine = kTokensPerWarp * lw + (lane & 7);  // entry of a tile that this lane locates
+    const int mine = kTokensPerWarp * lw + (lane % kTokensPerWarp);  // entry of a tile that this lane locates
     auto entry = [&](int tile) { return tile * kTile + mine < count ? __ldg(list + tile * kTile + mine) : -1; };
-    const int piece = lane >> 2;                        // lane l holds dims 16 l .. 16 l + 15
-    const bool odd = piece & 1;  // odd pieces store their halves in the other order: no bank conflict
     const int rope_token = lane >> 3, rope_unit = lane & 7;
 
-    uint4 raw[kTokensPerWarp], rope[2];
-    uint32_t codes;
-    Token tok = locate(p, entry(0));
-    int next_slot = entry(1);
-    auto load_values = [&](int j) {
-      const int64_t blk = __shfl_sync(0xFFFFFFFFu, tok.block, j);
-      const int off = __shfl_sync(0xFFFFFFFFu, tok.off, j);
-      const bool ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(tok.ok), j);
-      return ok ? __ldg(reinterpret_cast<const uint4*>(p.cache + blk + off * kKvLatent + 16 * lane))
-                : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_rope = [&](int i) {
-      const int j = rope_token + 4 * i;
-      const int64_t blk = __shfl_sync(0xFFFFFFFFu, tok.block, j);
-      const int off = __shfl_sync(0xFFFFFFFFu, tok.off, j);
-      const bool ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(tok.ok), j);
-      return ok ? __ldg(reinterpret_cast<const uint4*>(p.cache + blk + p.block_size * kKvRopeAt + off * 128 +
-                                                       16 * rope_unit))
-                : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_codes = [&]() {
-      return tok.ok ? __ldg(reinterpret_cast<const uint32_t*>(p.cache + tok.block + p.block_size * kKvScaleAt +
-                                                              4 * tok.off))
-                    : 0u;
-    };
-    codes = load_codes();
+    uint2 raw[kTokensPerWarp][2];  // dims 8 lane .. + 7 and 256 + 8 lane .. + 7 of each token
+    uint4 rope[kTokensPerWarp / 4];
+    uint32_t codes, valid;
+    int next_slot = -1;
+    auto load_tile = [&](int tile) {
+      const Token tok = locate(p, next_slot);
+      next_slot = entry(tile + kStages);
+      valid = __ballot_sync(0xFFFFFFFFu, tok.latent != nullptr);
+      codes = 0;
+      if (tok.latent) codes = __ldg(tok.codes);
 #pragma unroll
-    for (int j = 0; j < kTokensPerWarp; ++j) raw[j] = load_values(j);
-    rope[0] = load_rope(0);
-    rope[1] = load_rope(1);
-    uint32_t valid = __ballot_sync(0xFFFFFFFFu, tok.ok) & 0xFFu;
-
-    for (int i = 0; i < tiles; ++i) {
-      const int st = i & 1;
-      tok = locate(p, next_slot);  // entries past the list are -1: nothing is loaded for them
-      next_slot = entry(i + 2);
-      const uint32_t next_codes = load_codes();
-      if (i >= kStages) wait_bar(sh, &sh.k_empty[st], ((i >> 1) - 1) & 1);
-      uint8_t* tile = k_s + st * kTileBytes;
-      if (lane == 0) reinterpret_cast<uint8_t*>(sh.valid[st])[lw] = static_cast<uint8_t>(valid);
+      for (int j = 0; j < kTokensPerWarp; ++j) {
+        const uint8_t* src = shfl_ptr(tok.latent, j);
+        raw[j][0] = load8_if(src + 8 * lane, src != nullptr);
+        raw[j][1] = load8_if(src + 256 + 8 * lane, src != nullptr);
+      }
+#pragma unroll
+      for (int h = 0; h < kTokensPerWarp / 4; ++h) {
+        const uint8_t* src = shfl_ptr(tok.rope, rope_token + 4 * h);
+        rope[h] = load16_if(src + 16 * rope_unit, src != nullptr);
+      }
+      codes = __vminu4(codes, kKvMaxScaleCode * 0x01010101u);
+    };
+    if (group < tiles) {
+      next_slot = entry(group);
+      load_tile(group);
+    }
+    for (int i = group; i < tiles; i += kStages) {
+      if (i >= kStages) wait_bar(sh, &sh.k_empty[group], ((i >> 1) - 1) & 1);
+      uint8_t* tile = k_s + group * kTileBytes;
+      if (lane == 0) reinterpret_cast<uint16_t*>(sh.valid[group])[lw] = static_cast<uint16_t>(valid);
+      // the lane's 16-byte unit of piece lane / 8 (and of piece 4 + lane / 8), in the first row of the swizzle
+      uint8_t* line = tile + (lane >> 3) * kPieceBytes + kTokensPerWarp * lw * 128;
 #pragma unroll
       for (int j = 0; j < kTokensPerWarp; ++j) {
         const uint32_t word = __shfl_sync(0xFFFFFFFFu, codes, j);
-        const uint32_t mul = kv_dequant_multiplier((word >> (8 * (lane >> 3))) & 0xFFu);
-        const uint4 r = raw[j];
-        uint4 a, b;
-        kv_dequant4(odd ? r.z : r.x, mul, a.x, a.y);
-        kv_dequant4(odd ? r.w : r.y, mul, a.z, a.w);
-        kv_dequant4(odd ? r.x : r.z, mul, b.x, b.y);
-        kv_dequant4(odd ? r.y : r.w, mul, b.z, b.w);
-        raw[j] = load_values(j);
-        const int t = kTokensPerWarp * lw + j;  // t & 7 == j
-        uint8_t* line = tile + piece * kPieceBytes + t * 128;
-        const int u = 2 * (lane & 3) + (odd ? 1 : 0);
-        *reinterpret_cast<uint4*>(line + ((u ^ j) << 4)) = a;
-        *reinterpret_cast<uint4*>(line + (((u ^ 1) ^ j) << 4)) = b;
+        const int at = j * 128 + (((lane & 7) ^ (j & 7)) << 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t mul = kv_multiplier_of(__byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)));
+          uint4 w;
+          kv_dequant4_even_odd(raw[j][h].x, mul, w.x, w.y);
+          kv_dequant4_even_odd(raw[j][h].y, mul, w.z, w.w);
+          *reinterpret_cast<uint4*>(line + 4 * h * kPieceBytes + at) = w;
+        }
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kTokensPerWarp / 4; ++h) {
         const int t = kTokensPerWarp * lw + rope_token + 4 * h;
         *reinterpret_cast<uint4*>(tile + (kPieces - 1) * kPieceBytes + t * 128 + ((rope_unit ^ (t & 7)) << 4)) = rope[h];
-        rope[h] = load_rope(h);
       }
-      codes = next_codes;
-      valid = __ballot_sync(0xFFFFFFFFu, tok.ok) & 0xFFu;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full[st]);
+      if (lane == 0) mbar_arrive(&sh.k_full[group]);
+      if (i + kStages < tiles) load_tile(i + kStages);
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- matrix instructions
     // Whichever of the next S and the next O product has its operands goes first, O before S:
     // O's completion is what frees a tile.
-    const uint32_t lead = lane == 0;
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(lead));
     const uint64_t q_desc = sw128_kmajor_desc(smem_u32(q_s));
     const uint64_t p_desc = sw128_kmajor_desc(smem_u32(p_s));
     const uint64_t k_desc = sw128_kmajor_desc(smem_u32(k_s));
@@ -358,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     int idle = 0;
     while (o_next < total) {
       const bool can_o = o_next < s_next && mbar_test(&sh.p_full, o_next & 1);
-      if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(can_o), 0)) {
+      if (__all_sync(0xFFFFFFFFu, can_o)) {
         tc_fence_after();
         const int st = o_next & 1;
         const uint64_t v = v_desc + st * (kTileBytes >> 4);
@@ -378,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       }
       const bool can_s = s_next < total && s_next - o_next < kStages &&
                          mbar_test(&sh.k_full[s_next & 1], (s_next >> 1) & 1);
-      if (__shfl_sync(0xFFFFFFFFu, static_cast<int>(can_s), 0)) {
+      if (__all_sync(0xFFFFFFFFu, can_s)) {
         tc_fence_after();
         const int st = s_next & 1;
         const uint64_t k = k_desc + st * (kTileBytes >> 4);
@@ -419,6 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       const int r = i / (kKvDim / 8), u = i % (kKvDim / 8);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (h0 + r < p.H) v = __ldg(reinterpret_cast<const uint4*>(p.q + row * p.ld_q + (h0 + r) * p.ld_qh + 8 * u));
+      if (u < kKvLatent / 8) {  // the loaders' order of the latent dims: 0, 2, 1, 3 of every four
+        v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                       __byte_perm(v.z, v.w, 0x7632));
+      }
       *reinterpret_cast<uint4*>(q_s + (u >> 3) * kPieceBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v;
     }
     fence_proxy_async_smem();
@@ -515,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         float4* dst = reinterpret_cast<float4*>(p.ws_o + (ws_row * kHeadsPerBlock + r) * kKvLatent + dim);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+          dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 1]),
                                __uint_as_float(o[4 * j + 3]));
         }
       } else {
@@ -525,8 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
           uint32_t w[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * x]) * inv,
-                                                           __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
+            const int e = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
+            const __nv_bfloat162 b =
+                __floats2bfloat162_rn(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 2]) * inv);
             w[x] = *reinterpret_cast<const uint32_t*>(&b);
           }
           dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
