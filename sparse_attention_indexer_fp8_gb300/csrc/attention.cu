@@ -52,18 +52,20 @@ struct AttnParams {
 // r + 64 (c / (N / 2))): O takes 256 columns, where the plain form would take all 512 and leave none
 // for S, and runs at half the rate (N = 256: 128 clocks against 80 on a GB300).
 //
-// Roles: warps 4-11 gather and dequantise the tokens, warp 12 issues the matrix
+// Roles: warps 4-19 gather and dequantise the tokens, warp 20 issues the matrix
 // instructions, warps 0-3 do the softmax, the rescaling and the epilogue.
 //
 // Keys and values are one copy in shared memory: a token is a row of nine 128-byte swizzled
 // pieces (64 dims each). Read along the dims it is the K-major B operand of S, read along the
 // tokens the N-major B operand of O. Two tiles of 72 KB are in flight beside Q (72 KB) and P (8 KB).
 //
-// Two groups of four loader warps own a stage each. A group converts and stores its tile, then
+// Two groups of eight loader warps own a stage each. A group converts and stores its tile, then
 // issues every load of its next one at once, into registers: HBM latency runs under the other
 // group's conversion and the matrix work, with no staging buffer. (One group that refilled each
 // register right after its conversion measured 7000 clocks a tile: loads of two tiles shared
-// scoreboards, so every conversion waited for the newest load.)
+// scoreboards, so every conversion waited for the newest load.) What a warp keeps in flight is
+// limited whatever it asks for: random 512-byte rows read by 8 warps an SM came at 3.2 TB/s, by
+// 16 at 5.4 TB/s, by 32 at 6.4 TB/s, with 8 or 16 rows asked for by each; hence sixteen.
 // ---------------------------------------------------------------------------
 constexpr int kHeadsPerBlock = 64;
 constexpr int kTile = 64;
@@ -71,7 +73,7 @@ constexpr int kPieces = kKvDim / 64;             // 128-byte pieces of a token's
 constexpr int kPieceBytes = kTile * 128;         // one piece of 64 rows
 constexpr int kTileBytes = kPieces * kPieceBytes;
 constexpr int kStages = 2;
-constexpr int kLoaderWarps = 8;
+constexpr int kLoaderWarps = 16;
 constexpr int kGroupWarps = kLoaderWarps / kStages;  // each stage has its own group of loader warps
 constexpr int kTokensPerWarp = kTile / kGroupWarps;
 constexpr int kMmaWarp = 4 + kLoaderWarps;
@@ -134,15 +136,24 @@ __device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t issue) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[32]) {
+// Sixteen columns of the thread's lane, read (valid after the wait inside) or written.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     for (int i = group; i < tiles; i += kStages) {
       if (i >= kStages) wait_bar(sh, &sh.k_empty[group], ((i >> 1) - 1) & 1);
       uint8_t* tile = k_s + group * kTileBytes;
-      if (lane == 0) reinterpret_cast<uint16_t*>(sh.valid[group])[lw] = static_cast<uint16_t>(valid);
+      if (lane == 0) reinterpret_cast<uint8_t*>(sh.valid[group])[lw] = static_cast<uint8_t>(valid);
       // the lane's 16-byte unit of piece lane / 8 (and of piece 4 + lane / 8), in the first row of the swizzle
       uint8_t* line = tile + (lane >> 3) * kPieceBytes + kTokensPerWarp * lw * 128;
 #pragma unroll
@@ -481,13 +492,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
           const float f = rise ? exp2_approx(m - m_new) : 1.0f;  // m = -inf: 0, and O is 0
           l *= f;
 #pragma unroll 1
-          for (int c = 0; c < kOCols; c += 32) {
-            uint32_t o[32];
-            tmem_ld_x32(lanes + c, o);
-            tmem_wait_ld(o);
+          for (int c = 0; c < kOCols; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(lanes + c, o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st_x32(lanes + c, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(lanes + c, o);
           }
           tmem_wait_st();
         }
