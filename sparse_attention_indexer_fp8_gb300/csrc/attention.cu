@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv_layout.cuh"
@@ -23,6 +24,7 @@ struct AttnParams {
   int64_t ld_q, ld_qh;  // elements between rows, between heads
   const uint8_t* cache;
   int num_blocks, block_size, block_span;
+  uint32_t span_magic, span_shift;  // slot / block_span = (slot * span_magic >> 32) >> span_shift
   int64_t block_stride;
   const int32_t* slots;
   int64_t ld_slots;
@@ -52,8 +54,9 @@ struct AttnParams {
 // r + 64 (c / (N / 2))): O takes 256 columns, where the plain form would take all 512 and leave none
 // for S, and runs at half the rate (N = 256: 128 clocks against 80 on a GB300).
 //
-// Roles: warps 4-19 gather and dequantise the tokens, warp 20 issues the matrix
-// instructions, warps 0-3 do the softmax, the rescaling and the epilogue.
+// Roles: warps 4-19 gather and dequantise the tokens' latents, warps 21-22 copy their position
+// dims, warp 20 issues the matrix instructions, warps 0-3 do the softmax, the rescaling and the
+// epilogue.
 //
 // Keys and values are one copy in shared memory: a token is a row of nine 128-byte swizzled
 // pieces (64 dims each). Read along the dims it is the K-major B operand of S, read along the
@@ -70,30 +73,49 @@ struct AttnParams {
 constexpr int kHeadsPerBlock = 64;
 constexpr int kTile = 64;
 constexpr int kPieces = kKvDim / 64;             // 128-byte pieces of a token's bf16 row
-constexpr int kPieceBytes = kTile * 128;         // one piece of 64 rows
-constexpr int kTileBytes = kPieces * kPieceBytes;
+constexpr int kPieceBytes = 64 * 128;            // one piece of 64 rows
+constexpr int kQBytes = kPieces * kPieceBytes;
 constexpr int kStages = 2;
 constexpr int kLoaderWarps = 16;
 constexpr int kGroupWarps = kLoaderWarps / kStages;  // each stage has its own group of loader warps
-constexpr int kTokensPerWarp = kTile / kGroupWarps;
 constexpr int kMmaWarp = 4 + kLoaderWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kRopeWarp = kMmaWarp + 1;          // one per stage
+constexpr int kThreads = (kRopeWarp + kStages) * 32;
+constexpr int kValidRing = 4;
+constexpr int kAhead = 4;                        // tiles between the L2 prefetch and the loads
 constexpr int kOCols = 256;                      // tensor-memory columns of O; S0 and S1 (32 each) follow
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescaleStep = 8.0f;             // log2: P may reach 2^8 before O is rescaled
 
 struct Shared {
-  uint64_t q_full, p_full, pv_done, drained;
-  uint64_t k_full[kStages], k_empty[kStages], s_full[2];
+  uint64_t q_full, drained;
+  uint64_t k_full[kStages];                      // a stage's keys are stored (a pair: the leader's, for both blocks)
+  uint64_t v_full[kStages];                      // a pair's values likewise
+  uint64_t s_full[kStages];                      // S of the tile is complete: a pair's keys are free
+  uint64_t p_full[kStages];                      // P is stored (a pair: the leader's, for both blocks)
+  uint64_t o_done[kStages];                      // the tile's share of O is complete: P and the values are free
+  uint64_t flags[kValidRing];                    // `valid` is written
   uint32_t tmem;
   volatile uint32_t dead;                        // a wait expired: no further wait blocks
-  uint32_t valid[kStages][2];                    // bit t: token t of the tile counts
+  uint32_t valid[kValidRing][2];                 // bit t: token t of the tile counts
   float xchg[2][128];
 };
 
-constexpr int kSmemBytes = kTileBytes * (1 + kStages) + kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
-static_assert(kSmemBytes <= 232448, "shared memory of one block");
+// A stage's keys (all 576 dims of this block's tokens of a tile) and, of a pair, its values (256
+// dims of all 64 tokens; a block alone reads them out of its keys). Keys of a pair are free once S is
+// complete, values once O is, so the next tile's S does not wait for this one's softmax.
+template <bool kPair>
+struct Stage {
+  static constexpr int kTokens = kPair ? kTile / 2 : kTile;  // in the block's keys
+  static constexpr int kKeyPiece = kTokens * 128;
+  static constexpr int kKeys = kPieces * kKeyPiece;
+  static constexpr int kValues = kPair ? kKvLatent / 2 / 64 * kPieceBytes : 0;
+  static constexpr int kPBufs = kPair ? 2 : 1;
+  static constexpr int kSmem =
+      kQBytes + kStages * (kKeys + kValues) + kPBufs * kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
+  static_assert(kSmem <= 232448, "shared memory of one block");
+};
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_n_major) {
   // D fp32 (bits 4-5), A and B bf16 (7-9, 10-12), B's major (16), N >> 3 (17-22), M >> 4 (24-28)
@@ -114,26 +136,71 @@ __device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr) {
   return d;
 }
 
-// Issued by the lane with `issue` set; the whole warp passes here converged, so the
-// descriptors stay in uniform registers.
-__device__ __forceinline__ void mma_ws_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
-                                            uint32_t issue) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(acc), "r"(issue)
-      : "memory");
+// Issued by the lane with `issue` set; the whole warp passes here converged, so the descriptors stay in
+// uniform registers (N = 64 products then go out every 32 clocks; issued from a branch of one
+// lane, every 45 to 56). A pair's leader issues for both blocks.
+template <bool kPair>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                         uint32_t issue) {
+  if constexpr (kPair) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(acc), "r"(issue)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(acc), "r"(issue)
+        : "memory");
+  }
 }
 
-__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t issue) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(issue)
-      : "memory");
+// Arrives on the barrier, of a pair on that of both blocks, once everything issued so far is complete.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t issue) {
+  if constexpr (kPair) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "mov.b16 m, 3;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+        ::"r"(smem_u32(bar)), "r"(issue)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(issue)
+        : "memory");
+  }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_get(uint32_t* dst) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+                 "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)), "r"(kTmemCols)
+                 : "memory");
+  } else {
+    tmem_alloc(dst, kTmemCols);
+    tmem_relinquish();
+  }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_put(uint32_t taddr) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+  } else {
+    tmem_dealloc(taddr, kTmemCols);
+  }
 }
 
 // Sixteen columns of the thread's lane, read (valid after the wait inside) or written.
@@ -157,6 +224,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
+// One look at a barrier, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Bounded wait. A wait that takes two seconds marks the block dead and raises the device
 // flag; from then on no wait blocks, every role runs its remaining iterations on whatever it
 // finds (all addresses stay in bounds), and the block ends in order.
@@ -173,17 +253,28 @@ __device__ __forceinline__ void wait_bar(Shared& sh, uint64_t* bar, uint32_t par
   __syncwarp();
 }
 
-// One look at a barrier, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
+// --- the other block of a pair (a cluster of two) -------------------------------
+__device__ __forceinline__ uint32_t peer_addr(const void* ptr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(ptr)), "r"(rank));
+  return a;
+}
+
+// Arrives on a barrier of either block. What it announces was written to this block's own shared memory
+// for the tensor core of this SM, and fence.proxy.async has made it visible there, so no release at
+// cluster scope is needed (it measured a thousand clocks a hop).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Arrives on this barrier, of a pair on the leader's.
+template <bool kPair>
+__device__ __forceinline__ void arrive_lead(uint64_t* bar) {
+  if constexpr (kPair) mbar_arrive_cluster(peer_addr(bar, 0)); else mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -194,19 +285,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// 16 bytes of the cache, or zeros. Volatile: the load is issued where it stands, a tile ahead of its use.
-__device__ __forceinline__ uint4 load16_if(const uint8_t* ptr, bool ok) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(ptr), "r"(static_cast<int>(ok)));
-  return v;
+// 16 bytes of global memory into shared memory, asynchronously; zeros where `ok` is false.
+__device__ __forceinline__ void copy16_if(uint8_t* dst, const uint8_t* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
 }
 
+// 8 bytes of the cache, or zeros. Volatile: the load is issued where it stands, a tile ahead of its use.
 __device__ __forceinline__ uint2 load8_if(const uint8_t* ptr, bool ok) {
   uint2 v;
   asm volatile(
@@ -218,6 +303,12 @@ __device__ __forceinline__ uint2 load8_if(const uint8_t* ptr, bool ok) {
       : "l"(ptr), "r"(static_cast<int>(ok)));
   return v;
 }
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 
 __device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* ptr, int lane) {
   return reinterpret_cast<const uint8_t*>(
@@ -234,7 +325,7 @@ struct Token {
 __device__ __forceinline__ Token locate(const AttnParams& p, int slot) {
   Token t{nullptr, nullptr, nullptr};
   if (slot < 0) return t;
-  const int blk = slot / p.block_span;
+  const int blk = static_cast<int>(__umulhi(static_cast<uint32_t>(slot), p.span_magic) >> p.span_shift);
   const int off = slot - blk * p.block_span;
   if (blk >= p.num_blocks || off >= p.block_size) {
     atomicOr(&g_attention_error, 1u);
@@ -247,14 +338,16 @@ __device__ __forceinline__ Token locate(const AttnParams& p, int slot) {
   return t;
 }
 
-template <bool kSplit>
+template <bool kSplit, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  using St = Stage<kPair>;
   uint8_t* q_s = smem;
-  uint8_t* k_s = smem + kTileBytes;
-  uint8_t* p_s = k_s + kStages * kTileBytes;
-  Shared& sh = *reinterpret_cast<Shared*>(p_s + kPieceBytes);
+  uint8_t* k_s = q_s + kQBytes;
+  uint8_t* v_s = k_s + kStages * St::kKeys;
+  uint8_t* p_s = v_s + kStages * St::kValues;
+  Shared& sh = *reinterpret_cast<Shared*>(p_s + St::kPBufs * kPieceBytes);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // head groups vary fastest: the blocks that read the same tokens run side by side
@@ -262,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   const int part = kSplit ? (blockIdx.x / p.head_blocks) % p.parts : 0;
   const int row = blockIdx.x / (p.head_blocks * p.parts);
   const int h0 = hb * kHeadsPerBlock;
+  const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;  // 0: the pair's leader
   int n = p.k;
   if (p.n_sel) n = min(n, max(__ldg(p.n_sel + row), 0));
   const int first = part * p.part_tiles * kTile;  // of this block's entries
@@ -285,123 +379,255 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   }
 
   if (tid == 0) {
-    mbar_init(&sh.q_full, 4);
-    mbar_init(&sh.p_full, 4);
-    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.q_full, kPair ? 8 : 4);  // of a pair: the leader's, with the other block's warps
     mbar_init(&sh.drained, 1);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.k_full[i], kGroupWarps);
-      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.k_full[i], (kPair ? 2 : 1) * (kGroupWarps + 1));
+      mbar_init(&sh.v_full[i], 2 * kGroupWarps);
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], kPair ? 8 : 4);
+      mbar_init(&sh.o_done[i], 1);
     }
+    for (int i = 0; i < kValidRing; ++i) mbar_init(&sh.flags[i], 1);
     sh.dead = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(&sh.tmem, kTmemCols);
-    tmem_relinquish();
+    tmem_get<kPair>(&sh.tmem);
   }
   tc_fence_before();
+  __syncwarp();
+  if (kPair) cluster_sync();  // the other block's barriers exist too
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp >= 4 && warp < kMmaWarp) {
+  // The loaders' role, compiled for either rank of a pair: addresses that depend on it stay immediates.
+  auto loader = [&](auto rank_of) {
+    constexpr uint32_t rank = decltype(rank_of)::value;
     // ---------------------------------------------------------------- loaders
+    // Of a pair, a block gathers half of a tile's tokens whole, as keys, and of the others the 256 dims
+    // that it keeps as values. (Values fetched from the other block's shared memory instead came at some
+    // 10 bytes a clock, by stores as by bulk copies, and bounded the tile.)
+    constexpr int kOwn = St::kTokens / kGroupWarps;     // a warp's whole tokens
+    constexpr int kOther = kPair ? kOwn : 0;            // and the others
+    constexpr int kLocated = kOwn + kOther;
+    constexpr int kEarly = 2;  // tokens converted while the stage is still in use; the registers hold no more
     const int group = (warp - 4) / kGroupWarps, lw = (warp - 4) % kGroupWarps;  // this group's tiles: group, group + 2, ...
+    const int r0 = kOwn * lw;                                     // the warp's first row of the stage's keys
+    const int own_at = static_cast<int>(rank) * St::kTokens + r0;  // and its token of the tile
+    const int other_at = static_cast<int>(rank ^ 1u) * St::kTokens + r0;
     const int32_t* list = p.slots + row * p.ld_slots + first;
     const int count = n - first;
-    const int mine = kTokensPerWarp * lw + (lane % kTokensPerWarp);  // entry of a tile that this lane locates
-    auto entry = [&](int tile) { return tile * kTile + mine < count ? __ldg(list + tile * kTile + mine) : -1; };
-    const int rope_token = lane >> 3, rope_unit = lane & 7;
+    const int which = lane % kLocated;  // of the warp's tokens, the one that this lane locates
+    const int mine = kPair && which >= kOwn ? other_at + which - kOwn : own_at + which;
+    const int left = count - mine;      // entries from its first one on
+    const int32_t* my_list = list + mine;
+    auto entry = [&](int tile) { return tile * kTile < left ? __ldg(my_list + tile * kTile) : -1; };
 
-    uint2 raw[kTokensPerWarp][2];  // dims 8 lane .. + 7 and 256 + 8 lane .. + 7 of each token
-    uint4 rope[kTokensPerWarp / 4];
-    uint32_t codes, valid;
+    // Lane l stores unit l % 8 of piece l / 8 (of the first half of the dims, of a pair the block's own,
+    // and of the other): it holds the eight dims that the swizzle puts there. So the loads' addresses
+    // depend on the row, and the stores', which would take registers, do not.
+    auto chunk = [&](int j) { return 8u * (static_cast<uint32_t>(lane) ^ (static_cast<uint32_t>(r0 + j) & 7u)); };
+    uint2 raw[kOwn][2];                // eight dims in either half of each token
+    uint2 half_raw[kPair ? kOwn : 1];  // and in the block's own half of the others
+    // Tokens are located two tiles of the group ahead of their conversion, and their slots read one more
+    // ahead: nothing between two tiles' loads waits for an address.
+    uint32_t codes = 0, next_codes = 0, found_codes = 0;
     int next_slot = -1;
-    auto load_tile = [&](int tile) {
+    const uint8_t* latent = nullptr;
+    auto find = [&](int tile) {
       const Token tok = locate(p, next_slot);
+      latent = tok.latent;
       next_slot = entry(tile + kStages);
-      valid = __ballot_sync(0xFFFFFFFFu, tok.latent != nullptr);
-      codes = 0;
-      if (tok.latent) codes = __ldg(tok.codes);
-#pragma unroll
-      for (int j = 0; j < kTokensPerWarp; ++j) {
-        const uint8_t* src = shfl_ptr(tok.latent, j);
-        raw[j][0] = load8_if(src + 8 * lane, src != nullptr);
-        raw[j][1] = load8_if(src + 256 + 8 * lane, src != nullptr);
-      }
-#pragma unroll
-      for (int h = 0; h < kTokensPerWarp / 4; ++h) {
-        const uint8_t* src = shfl_ptr(tok.rope, rope_token + 4 * h);
-        rope[h] = load16_if(src + 16 * rope_unit, src != nullptr);
-      }
-      codes = __vminu4(codes, kKvMaxScaleCode * 0x01010101u);
+      found_codes = 0;
+      if (latent) found_codes = __ldg(tok.codes);
     };
+    auto load_own = [&]() {
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+        const uint8_t* src = shfl_ptr(latent, j);
+        raw[j][0] = load8_if(src + 256 * rank + chunk(j), src != nullptr);
+        raw[j][1] = load8_if(src + 256 * (rank ^ 1u) + chunk(j), src != nullptr);
+      }
+    };
+    auto load_other = [&]() {
+#pragma unroll
+      for (int j = 0; j < kOther; ++j) {
+        const uint8_t* src = shfl_ptr(latent, kOwn + j);
+        half_raw[j] = load8_if(src + 256 * rank + chunk(j), src != nullptr);
+      }
+    };
+    // eight dims in half h of the token with these scale codes
+    auto word_of = [&](int j) { return __shfl_sync(0xFFFFFFFFu, codes, j); };
+    auto convert = [&](const uint2& x, uint32_t word, uint32_t h) {
+      const uint32_t mul = kv_multiplier_of(__byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)));
+      uint4 w;
+      kv_dequant4_even_odd(x.x, mul, w.x, w.y);
+      kv_dequant4_even_odd(x.y, mul, w.z, w.w);
+      return w;
+    };
+    // shared addresses in 32 bits: the registers are all taken
+    const uint32_t keys = smem_u32(k_s) + group * St::kKeys + (lane >> 3) * St::kKeyPiece + r0 * 128 + 16 * (lane & 7);
+    const uint32_t keys_of[2] = {keys + 4 * rank * St::kKeyPiece, keys + 4 * (rank ^ 1u) * St::kKeyPiece};
+    const uint32_t values = smem_u32(v_s) + group * St::kValues + (lane >> 3) * kPieceBytes + 16 * (lane & 7);
+
     if (group < tiles) {
       next_slot = entry(group);
-      load_tile(group);
+      find(group);
+      load_own();
+      load_other();
+      next_codes = found_codes;
+      find(group + kStages);
     }
     for (int i = group; i < tiles; i += kStages) {
-      if (i >= kStages) wait_bar(sh, &sh.k_empty[group], ((i >> 1) - 1) & 1);
-      uint8_t* tile = k_s + group * kTileBytes;
-      if (lane == 0) reinterpret_cast<uint8_t*>(sh.valid[group])[lw] = static_cast<uint8_t>(valid);
-      // the lane's 16-byte unit of piece lane / 8 (and of piece 4 + lane / 8), in the first row of the swizzle
-      uint8_t* line = tile + (lane >> 3) * kPieceBytes + kTokensPerWarp * lw * 128;
+      codes = __vminu4(next_codes, kKvMaxScaleCode * 0x01010101u);
+      uint4 first_half[kOwn], second_half[kOwn];
 #pragma unroll
-      for (int j = 0; j < kTokensPerWarp; ++j) {
-        const uint32_t word = __shfl_sync(0xFFFFFFFFu, codes, j);
-        const int at = j * 128 + (((lane & 7) ^ (j & 7)) << 4);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t mul = kv_multiplier_of(__byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)));
-          uint4 w;
-          kv_dequant4_even_odd(raw[j][h].x, mul, w.x, w.y);
-          kv_dequant4_even_odd(raw[j][h].y, mul, w.z, w.w);
-          *reinterpret_cast<uint4*>(line + 4 * h * kPieceBytes + at) = w;
-        }
+      for (int j = 0; j < kEarly; ++j) {
+        const uint32_t word = word_of(j);
+        first_half[j] = convert(raw[j][0], word, rank);
+        second_half[j] = convert(raw[j][1], word, rank ^ 1u);
       }
+      if (i >= kStages) wait_bar(sh, kPair ? &sh.s_full[group] : &sh.o_done[group], ((i >> 1) - 1) & 1);
 #pragma unroll
-      for (int h = 0; h < kTokensPerWarp / 4; ++h) {
-        const int t = kTokensPerWarp * lw + rope_token + 4 * h;
-        *reinterpret_cast<uint4*>(tile + (kPieces - 1) * kPieceBytes + t * 128 + ((rope_unit ^ (t & 7)) << 4)) = rope[h];
+      for (int j = 0; j < kOwn; ++j) {
+        if (j >= kEarly) {
+          const uint32_t word = word_of(j);
+          first_half[j] = convert(raw[j][0], word, rank);
+          second_half[j] = convert(raw[j][1], word, rank ^ 1u);
+        }
+        st_shared16(keys_of[0] + j * 128, first_half[j]);
+        st_shared16(keys_of[1] + j * 128, second_half[j]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full[group]);
-      if (i + kStages < tiles) load_tile(i + kStages);
+      if (lane == 0) arrive_lead<kPair>(&sh.k_full[group]);
+      // before the next loads: a conversion behind them would wait for them too
+#pragma unroll
+      for (int j = 0; j < kOther; ++j) second_half[j] = convert(half_raw[j], word_of(kOwn + j), rank);
+      if (i + kStages < tiles) load_own();
+      if (kPair) {
+        if (i >= kStages) wait_bar(sh, &sh.o_done[group], ((i >> 1) - 1) & 1);
+#pragma unroll
+        for (int j = 0; j < kOther; ++j) {
+          st_shared16(values + own_at * 128 + j * 128, first_half[j]);
+          st_shared16(values + other_at * 128 + j * 128, second_half[j]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_lead<kPair>(&sh.v_full[group]);
+        if (i + kStages < tiles) load_other();
+      }
+      next_codes = found_codes;
+      find(i + 2 * kStages);
     }
-  } else if (warp == kMmaWarp) {
+  };
+  if (warp >= 4 && warp < kMmaWarp) {
+    if (kPair && rank == 1) {
+      loader(std::integral_constant<uint32_t, 1>{});
+    } else {
+      loader(std::integral_constant<uint32_t, 0>{});
+    }
+  } else if (warp >= kRopeWarp) {
+    // ---------------------------------------------------------------- position dims, and L2 prefetch
+    // Position dims are bf16 in the cache as in the tile: copied asynchronously, once the stage is free.
+    // Lane l locates tokens l and 32 + l. The same warp brings the records of the tile kAhead further
+    // on into L2: a random token comes out of HBM in some 2900 clocks, out of L2 in 1200, and the
+    // loaders' registers hold one tile.
+    const int group = warp - kRopeWarp;
+    const int32_t* list = p.slots + row * p.ld_slots + first;
+    const int count = n - first;
+    auto entry = [&](int tile, int h) {
+      const int e = tile * kTile + 32 * h + lane;
+      return e < count ? __ldg(list + e) : -1;
+    };
+    // 32 tokens: each lane's own position dims and codes, and 8 x 4 lines of latents an instruction
+    auto prefetch = [&](int slot) {
+      const Token t = locate(p, slot);
+      if (t.latent) {
+        prefetch_l2(t.rope);
+        prefetch_l2(t.codes);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t* src = shfl_ptr(t.latent, 8 * k + (lane >> 2));
+        if (src) prefetch_l2(src + 128 * (lane & 3));
+      }
+      __syncwarp();
+    };
+    // a pair's block looks after its own half
+    const int h0p = kPair ? static_cast<int>(rank) : 0, h1p = kPair ? static_cast<int>(rank) : 1;
+    for (int i = group; i < kAhead && i < tiles; i += kStages) {
+      for (int h = h0p; h <= h1p; ++h) prefetch(entry(i, h));
+    }
+    int s0 = entry(group, 0), s1 = entry(group, 1);
+    int a0 = entry(group + kAhead, h0p), a1 = entry(group + kAhead, h1p);
+    uint8_t* piece = k_s + group * St::kKeys + (kPieces - 1) * St::kKeyPiece;
+    for (int i = group; i < tiles; i += kStages) {
+      const uint8_t* src[2] = {locate(p, s0).rope, locate(p, s1).rope};
+      s0 = entry(i + kStages, 0);
+      s1 = entry(i + kStages, 1);
+      if (i >= kStages) wait_bar(sh, kPair ? &sh.s_full[group] : &sh.o_done[group], ((i >> 1) - 1) & 1);
+#pragma unroll
+      for (int c = 0; c < St::kTokens / 4; ++c) {
+        const int t = 4 * c + (lane >> 3), u = lane & 7;  // row of the stage's keys
+        const uint8_t* from = shfl_ptr(kPair ? (rank ? src[1] : src[0]) : src[c / 8], t & 31);
+        copy16_if(piece + t * 128 + ((u ^ (t & 7)) << 4), from ? from + 16 * u : p.cache, from != nullptr);
+      }
+      const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, src[0] != nullptr);
+      const uint32_t v1 = __ballot_sync(0xFFFFFFFFu, src[1] != nullptr);
+      if (lane == 0) {
+        // S of this tile is issued after O of tile i - 2, so entry i - 4 has been read
+        sh.valid[i % kValidRing][0] = v0;
+        sh.valid[i % kValidRing][1] = v1;
+        mbar_arrive(&sh.flags[i % kValidRing]);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_lead<kPair>(&sh.k_full[group]);
+      if (i + kAhead < tiles) {
+        prefetch(a0);
+        if (!kPair) prefetch(a1);
+        a0 = entry(i + kStages + kAhead, h0p);
+        a1 = entry(i + kStages + kAhead, h1p);
+      }
+    }
+  } else if (warp == kMmaWarp && rank == 0) {
     // ---------------------------------------------------------------- matrix instructions
-    // Whichever of the next S and the next O product has its operands goes first, O before S:
-    // O's completion is what frees a tile.
+    // Whichever of the next S and the next O product has its operands goes first, O before S.
     uint32_t lead;
     asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(lead));
     const uint64_t q_desc = sw128_kmajor_desc(smem_u32(q_s));
     const uint64_t p_desc = sw128_kmajor_desc(smem_u32(p_s));
     const uint64_t k_desc = sw128_kmajor_desc(smem_u32(k_s));
-    const uint64_t v_desc = sw128_nmajor_desc(smem_u32(k_s));
+    // values: the pieces of a block's 128 (pair: the other 128 are the other block's) or 256 dims of a product
+    const uint64_t v_desc = sw128_nmajor_desc(smem_u32(kPair ? v_s : k_s));
+    constexpr int kValueStage = kPair ? St::kValues : St::kKeys;
+    constexpr int kValuePieces = kPair ? 2 : 4;
     wait_bar(sh, &sh.q_full, 0);
     const int total = __shfl_sync(0xFFFFFFFFu, tiles, 0);
     int s_next = 0, o_next = 0;
     uint64_t t0 = global_timer_ns();
     int idle = 0;
     while (o_next < total) {
-      const bool can_o = o_next < s_next && mbar_test(&sh.p_full, o_next & 1);
+      const bool can_o = o_next < s_next && mbar_test(&sh.p_full[o_next & 1], (o_next >> 1) & 1) &&
+                         (!kPair || mbar_test(&sh.v_full[o_next & 1], (o_next >> 1) & 1));
       if (__all_sync(0xFFFFFFFFu, can_o)) {
         tc_fence_after();
         const int st = o_next & 1;
-        const uint64_t v = v_desc + st * (kTileBytes >> 4);
+        const uint64_t v = v_desc + st * (kValueStage >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            mma_ws_bf16(tmem + half * (kOCols / 2), p_desc + 2 * ks, v + ((4 * half * kPieceBytes + 2048 * ks) >> 4),
-                        idesc_bf16(64, 256, true), o_next > 0 || ks > 0, lead);
+            mma_bf16<kPair>(tmem + half * (kOCols / 2), p_desc + (kPair ? st * (kPieceBytes >> 4) : 0) + 2 * ks,
+                            v + ((kValuePieces * half * kPieceBytes + 2048 * ks) >> 4),
+                            idesc_bf16(kPair ? 128 : 64, 256, true), o_next > 0 || ks > 0, lead);
           }
         }
-        commit_if(&sh.k_empty[st], lead);
-        commit_if(&sh.pv_done, lead);
+        commit<kPair>(&sh.o_done[st], lead);
         ++o_next;
         idle = 0;
         continue;
@@ -411,16 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       if (__all_sync(0xFFFFFFFFu, can_s)) {
         tc_fence_after();
         const int st = s_next & 1;
-        const uint64_t k = k_desc + st * (kTileBytes >> 4);
+        const uint64_t k = k_desc + st * (St::kKeys >> 4);
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            mma_ws_bf16(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks,
-                        k + ((c * kPieceBytes) >> 4) + 2 * ks, idesc_bf16(64, 64, false), c > 0 || ks > 0, lead);
+            mma_bf16<kPair>(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks,
+                            k + ((c * St::kKeyPiece) >> 4) + 2 * ks, idesc_bf16(kPair ? 128 : 64, 64, false),
+                            c > 0 || ks > 0, lead);
           }
         }
-        commit_if(&sh.s_full[st], lead);
+        commit<kPair>(&sh.s_full[st], lead);
         ++s_next;
         idle = 0;
         continue;
@@ -436,13 +663,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       if (__any_sync(0xFFFFFFFFu, expired)) break;
     }
     if (o_next < total) {  // given up: whatever was issued finishes before the tensor memory is freed
-      commit_if(&sh.drained, lead);
+      commit<kPair>(&sh.drained, lead);
       t0 = global_timer_ns();
       while (!mbar_test(&sh.drained, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
       }
       __syncwarp();
     }
-  } else {
+  } else if (warp < 4) {
     // ---------------------------------------------------------------- softmax and epilogue
     // Q: rows of heads past the last one are zero
     for (int i = tid; i < kHeadsPerBlock * (kKvDim / 8); i += 128) {
@@ -455,9 +682,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       }
       *reinterpret_cast<uint4*>(q_s + (u >> 3) * kPieceBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v;
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_full);
+    auto arrive = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_lead<kPair>(bar);
+    };
+    arrive(&sh.q_full);
 
     const int r = tid & 63, half = tid >> 6;          // head of the group, and half of the tile's tokens
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -465,19 +696,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     for (int i = 0; i < tiles; ++i) {
       const int st = i & 1;
       wait_bar(sh, &sh.s_full[st], (i >> 1) & 1);
-      wait_bar(sh, &sh.k_full[st], (i >> 1) & 1);     // long complete; orders this read of `valid` after the loaders
+      wait_bar(sh, &sh.flags[i % kValidRing], (i / kValidRing) & 1);  // long complete
       tc_fence_after();
       uint32_t v[32];
       tmem_ld_x32(lanes + kOCols + st * 32, v);
-      const uint32_t valid = sh.valid[st][half];
+      const uint32_t valid = sh.valid[i % kValidRing][half];
       tmem_wait_ld(v);
+      // v * unit is the logit in log2 units: the raw products as they are where every token counts, or
+      // scaled here with -inf for the others
+      float unit = p.scale_log2;
       float top = -INFINITY;
+      if (valid != 0xFFFFFFFFu) {
+        unit = 1.0f;
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float s = (valid >> c) & 1u ? __uint_as_float(v[c]) * p.scale_log2 : -INFINITY;
-        v[c] = __float_as_uint(s);
-        top = fmaxf(top, s);
+        for (int c = 0; c < 32; ++c) {
+          v[c] = (valid >> c) & 1u ? __float_as_uint(__uint_as_float(v[c]) * p.scale_log2) : 0xFF800000u;
+        }
       }
+      if (unit >= 0.f) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+      } else {
+        top = INFINITY;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) top = fminf(top, fminf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+      }
+      top *= unit;
       sh.xchg[st][tid] = top;
       softmax_bar();
       top = fmaxf(top, sh.xchg[st][tid ^ 64]);
@@ -486,8 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       const bool rise = top > m + kRescaleStep || (m == -INFINITY && top > -INFINITY);
       const float m_new = rise ? top : m;
       if (i > 0) {
-        wait_bar(sh, &sh.pv_done, (i - 1) & 1);       // P is free, and O complete up to the last tile
-        if (__any_sync(0xFFFFFFFFu, rise)) {
+        // O is complete up to the last tile (for a rescaling), and with it the only P is free
+        const bool scale_o = __any_sync(0xFFFFFFFFu, rise);
+        if (!kPair || scale_o) wait_bar(sh, &sh.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
+        if (scale_o) {
           tc_fence_after();
           const float f = rise ? exp2_approx(m - m_new) : 1.0f;  // m = -inf: 0, and O is 0
           l *= f;
@@ -507,22 +753,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       uint32_t w[16];
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
-        const float e0 = exp2_approx(__uint_as_float(v[c]) - ref), e1 = exp2_approx(__uint_as_float(v[c + 1]) - ref);
+        const float e0 = exp2_approx(fmaf(__uint_as_float(v[c]), unit, -ref));
+        const float e1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), unit, -ref));
         l += e0 + e1;
         const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
         w[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
+      // of two P, the one that tile i - 2 used
+      if (kPair && i >= 2) wait_bar(sh, &sh.o_done[st], ((i >> 1) - 1) & 1);
+      const uint32_t p_row = smem_u32(p_s) + (kPair ? st * kPieceBytes : 0) + r * 128;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        *reinterpret_cast<uint4*>(p_s + r * 128 + (((4 * half + c) ^ (r & 7)) << 4)) =
-            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        st_shared16(p_row + (((4 * half + c) ^ (r & 7)) << 4), make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full);
+      arrive(&sh.p_full[st]);
     }
-    wait_bar(sh, &sh.pv_done, (tiles - 1) & 1);
+    wait_bar(sh, &sh.o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
     tc_fence_after();
     softmax_bar();
     sh.xchg[0][tid] = l;
@@ -540,8 +786,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       uint32_t o[32];
       tmem_ld_x32(lanes + c, o);
       tmem_wait_ld(o);
-      // columns 0..127 are dims 128 half .. of the first 256, columns 128..255 of the second
-      const int dim = (c / 128) * 256 + half * 128 + (c % 128);
+      // A product has 256 dims, 128 to each lane half: of a block alone consecutive ones, of a pair 128
+      // of each block's 256.
+      const int dim = kPair ? 256 * half + c : (c / 128) * 256 + half * 128 + (c % 128);
       if (h >= p.H) {
         // no head: nothing to store
       } else if (kSplit) {
@@ -570,9 +817,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
   }
   tc_fence_before();
+  __syncwarp();
+  if (kPair) {
+    // neither block ends while the other may still arrive in it or read its operands
+    __syncwarp();
+    cluster_sync();
+  }
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_put<kPair>(tmem);
 }
 
 // Joins the parts of each (row, head): weights 2^(m_i - max m), a part without a valid token
@@ -687,6 +940,12 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
   p.num_blocks = num_blocks;
   p.block_size = block_size;
   p.block_span = block_span;
+  // Division of n < 2^31 by d by one multiplication: with 2^(s - 1) < d <= 2^s and m = floor(2^(31 + s) / d) + 1,
+  // m d exceeds 2^(31 + s) by at most d <= 2^s, so n m / 2^(31 + s) exceeds n / d by less than 1 / d.
+  uint32_t log = 1;
+  while ((int64_t{1} << log) < block_span) ++log;
+  p.span_magic = static_cast<uint32_t>((uint64_t{1} << (31 + log)) / static_cast<uint32_t>(block_span) + 1);
+  p.span_shift = log - 1;
   p.block_stride = block_stride_bytes;
   p.slots = slots;
   p.ld_slots = ld_slots;
@@ -717,10 +976,29 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
     p.ws_o = static_cast<float*>(ws);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + blocks * p.parts * kHeadsPerBlock * kKvLatent);
   }
-  auto* kernel = p.parts > 1 ? attention_kernel<true> : attention_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  // Rows of an even number of head groups run as pairs of blocks.
+  const bool pair = p.head_blocks % 2 == 0;
+  auto* kernel = p.parts > 1 ? (pair ? attention_kernel<true, true> : attention_kernel<true, false>)
+                             : (pair ? attention_kernel<false, true> : attention_kernel<false, false>);
+  const int smem = pair ? Stage<true>::kSmem : Stage<false>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(IDX_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  }
   st = check_launch(fn);
   if (st != IDX_OK || p.parts == 1) return st;
   attention_join_kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * H), kKvLatent / 4, 0, stream>>>(p);
