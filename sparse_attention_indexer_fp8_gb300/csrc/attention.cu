@@ -100,6 +100,7 @@ struct Shared {
   volatile uint32_t dead;                        // a wait expired: no further wait blocks
   uint32_t valid[kValidRing][2];                 // bit t: token t of the tile counts
   float xchg[2][128];
+  float inv[kHeadsPerBlock];                     // 1 / sum of each head
 };
 
 // A stage's keys (all 576 dims of this block's tokens of a tile) and, of a pair, its values (256
@@ -283,12 +284,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 2, %0;" ::"n"(kMmaWarp * 32) : "memory"); }
+
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // 16 bytes of global memory into shared memory, asynchronously; zeros where `ok` is false.
-__device__ __forceinline__ void copy16_if(uint8_t* dst, const uint8_t* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void copy16_if(uint32_t dst, const uint8_t* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 
 // 8 bytes of the cache, or zeros. Volatile: the load is issued where it stands, a tile ahead of its use.
@@ -306,6 +308,12 @@ __device__ __forceinline__ uint2 load8_if(const uint8_t* ptr, bool ok) {
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
@@ -378,29 +386,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     return;
   }
 
-  if (tid == 0) {
-    mbar_init(&sh.q_full, kPair ? 8 : 4);  // of a pair: the leader's, with the other block's warps
-    mbar_init(&sh.drained, 1);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.k_full[i], (kPair ? 2 : 1) * (kGroupWarps + 1));
-      mbar_init(&sh.v_full[i], 2 * kGroupWarps);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], kPair ? 8 : 4);
-      mbar_init(&sh.o_done[i], 1);
-    }
-    for (int i = 0; i < kValidRing; ++i) mbar_init(&sh.flags[i], 1);
-    sh.dead = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMmaWarp) {
-    tmem_get<kPair>(&sh.tmem);
-  }
-  tc_fence_before();
-  __syncwarp();
-  if (kPair) cluster_sync();  // the other block's barriers exist too
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  // Barriers and tensor memory are set up by the matrix warp; every role first does what needs neither.
+  uint32_t tmem = 0;
+  auto setup = [&]() {
+    tc_fence_before();
+    __syncwarp();
+    if (kPair) cluster_sync();  // the other block's barriers exist too
+    asm volatile("bar.sync 0;" ::: "memory");
+    tc_fence_after();
+    tmem = sh.tmem;
+  };
 
   // The loaders' role, compiled for either rank of a pair: addresses that depend on it stay immediates.
   auto loader = [&](auto rank_of) {
@@ -480,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       next_codes = found_codes;
       find(group + kStages);
     }
+    setup();
     for (int i = group; i < tiles; i += kStages) {
       codes = __vminu4(next_codes, kKvMaxScaleCode * 0x01010101u);
       uint4 first_half[kOwn], second_half[kOwn];
@@ -563,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
     int s0 = entry(group, 0), s1 = entry(group, 1);
     int a0 = entry(group + kAhead, h0p), a1 = entry(group + kAhead, h1p);
-    uint8_t* piece = k_s + group * St::kKeys + (kPieces - 1) * St::kKeyPiece;
+    const uint32_t piece = smem_u32(k_s) + group * St::kKeys + (kPieces - 1) * St::kKeyPiece;
+    setup();
     for (int i = group; i < tiles; i += kStages) {
       const uint8_t* src[2] = {locate(p, s0).rope, locate(p, s1).rope};
       s0 = entry(i + kStages, 0);
@@ -594,7 +591,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         a1 = entry(i + kStages + kAhead, h1p);
       }
     }
-  } else if (warp == kMmaWarp && rank == 0) {
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      mbar_init(&sh.q_full, kPair ? 8 : 4);  // of a pair: the leader's, with the other block's warps
+      mbar_init(&sh.drained, 1);
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&sh.k_full[i], (kPair ? 2 : 1) * (kGroupWarps + 1));
+        mbar_init(&sh.v_full[i], 2 * kGroupWarps);
+        mbar_init(&sh.s_full[i], 1);
+        mbar_init(&sh.p_full[i], kPair ? 8 : 4);
+        mbar_init(&sh.o_done[i], 1);
+      }
+      for (int i = 0; i < kValidRing; ++i) mbar_init(&sh.flags[i], 1);
+      sh.dead = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_get<kPair>(&sh.tmem);
+    setup();
+  }
+  if (warp == kMmaWarp && rank == 0) {
     // ---------------------------------------------------------------- matrix instructions
     // Whichever of the next S and the next O product has its operands goes first, O before S.
     uint32_t lead;
@@ -670,18 +686,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       __syncwarp();
     }
   } else if (warp < 4) {
-    // ---------------------------------------------------------------- softmax and epilogue
-    // Q: rows of heads past the last one are zero
-    for (int i = tid; i < kHeadsPerBlock * (kKvDim / 8); i += 128) {
-      const int r = i / (kKvDim / 8), u = i % (kKvDim / 8);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (h0 + r < p.H) v = __ldg(reinterpret_cast<const uint4*>(p.q + row * p.ld_q + (h0 + r) * p.ld_qh + 8 * u));
-      if (u < kKvLatent / 8) {  // the loaders' order of the latent dims: 0, 2, 1, 3 of every four
-        v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
-                       __byte_perm(v.z, v.w, 0x7632));
-      }
-      *reinterpret_cast<uint4*>(q_s + (u >> 3) * kPieceBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v;
+    // ---------------------------------------------------------------- softmax
+    // Q, sixteen rows a warp, rows of heads past the last one zero. All copies go out at once; what a thread
+    // copied it then puts into the loaders' order of the latent dims: 0, 2, 1, 3 of every four.
+    const uint32_t q_row = smem_u32(q_s) + 16 * warp * 128;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const int qh = h0 + 16 * warp + i;
+      const bool have = qh < p.H;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q + row * p.ld_q + (have ? qh * p.ld_qh : 0));
+      const uint32_t at = q_row + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
+      copy16_if(at + (lane >> 3) * kPieceBytes, src + 16 * lane, have);
+      copy16_if(at + (4 + (lane >> 3)) * kPieceBytes, src + 512 + 16 * lane, have);
+      if (lane < 8) copy16_if(at + 8 * kPieceBytes, src + 1024 + 16 * lane, have);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+    for (int i = 0; i < 16; i += 4) {
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = ld_shared16(q_row + (i + j / 2) * 128 + (((lane & 7) ^ ((i + j / 2) & 7)) << 4) +
+                           (4 * (j & 1) + (lane >> 3)) * kPieceBytes);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        st_shared16(q_row + (i + j / 2) * 128 + (((lane & 7) ^ ((i + j / 2) & 7)) << 4) +
+                        (4 * (j & 1) + (lane >> 3)) * kPieceBytes,
+                    make_uint4(__byte_perm(v[j].x, v[j].y, 0x5410), __byte_perm(v[j].x, v[j].y, 0x7632),
+                               __byte_perm(v[j].z, v[j].w, 0x5410), __byte_perm(v[j].z, v[j].w, 0x7632)));
+      }
+    }
+    setup();
     auto arrive = [&](uint64_t* bar) {
       fence_proxy_async_smem();
       tc_fence_before();
@@ -768,52 +804,72 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       }
       arrive(&sh.p_full[st]);
     }
-    wait_bar(sh, &sh.o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
-    tc_fence_after();
     softmax_bar();
     sh.xchg[0][tid] = l;
     softmax_bar();
     l += sh.xchg[0][tid ^ 64];
     const int h = h0 + r;
-    if (kSplit) {
-      if (half == 0) p.ws_ml[ws_row * kHeadsPerBlock + r] = make_float2(m, l);
-    } else if (p.lse && half == 0 && h < p.H) {
-      p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    if (half == 0) {
+      sh.inv[r] = l == 0.f ? 0.f : 1.0f / l;
+      if (kSplit) {
+        p.ws_ml[ws_row * kHeadsPerBlock + r] = make_float2(m, l);
+      } else if (p.lse && h < p.H) {
+        p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      }
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
+  }
+  if (warp < kMmaWarp) {
+    // ---------------------------------------------------------------- epilogue
+    // The loaders, four to a lane quarter and 64 columns each, write O (bf16, or the sums of a part) into the
+    // stages' memory, a row of it per head, and whole rows leave as bulk copies. (Stored from the
+    // registers, 16 bytes of a row each, the rows of 64 heads took 5500 clocks, 10500 in fp32.)
+    constexpr int kRowBytes = kKvLatent * (kSplit ? 4 : 2);
+    constexpr int kPitch = kRowBytes + 16;  // eight rows' stores fall into different banks
+    static_assert(kHeadsPerBlock * kPitch <= kStages * (St::kKeys + St::kValues), "the rows fit the stages");
+    wait_bar(sh, &sh.o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
+    tc_fence_after();
+    epilogue_bar();
+    if (warp >= 4) {
+      const int quarter = warp & 3, r = (32 * quarter + lane) & 63, half = quarter >> 1;
+      const float inv = sh.inv[r];
 #pragma unroll 1
-    for (int c = 0; c < kOCols; c += 32) {
-      uint32_t o[32];
-      tmem_ld_x32(lanes + c, o);
-      tmem_wait_ld(o);
-      // A product has 256 dims, 128 to each lane half: of a block alone consecutive ones, of a pair 128
-      // of each block's 256.
-      const int dim = kPair ? 256 * half + c : (c / 128) * 256 + half * 128 + (c % 128);
-      if (h >= p.H) {
-        // no head: nothing to store
-      } else if (kSplit) {
-        float4* dst = reinterpret_cast<float4*>(p.ws_o + (ws_row * kHeadsPerBlock + r) * kKvLatent + dim);
+      for (int c = 64 * ((warp - 4) >> 2); c < 64 * ((warp - 4) >> 2) + 64; c += 32) {
+        uint32_t o[32];
+        tmem_ld_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c, o);
+        tmem_wait_ld(o);
+        // A product has 256 dims, 128 to each lane half: of a block alone consecutive ones, of a pair 128
+        // of each block's 256. Dims 1 and 2 of every four have changed places.
+        const int dim = kPair ? 256 * half + c : (c / 128) * 256 + half * 128 + (c % 128);
+        const uint32_t at = smem_u32(k_s) + r * kPitch + dim * (kSplit ? 4 : 2);
+        if (kSplit) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 1]),
-                               __uint_as_float(o[4 * j + 3]));
-        }
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.ld_out + h * p.ld_oh + dim);
+          for (int j = 0; j < 8; ++j) st_shared16(at + 16 * j, make_uint4(o[4 * j], o[4 * j + 2], o[4 * j + 1], o[4 * j + 3]));
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t w[4];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int e = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
-            const __nv_bfloat162 b =
-                __floats2bfloat162_rn(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 2]) * inv);
-            w[x] = *reinterpret_cast<const uint32_t*>(&b);
+            for (int x = 0; x < 4; ++x) {
+              const int e = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
+              const __nv_bfloat162 b =
+                  __floats2bfloat162_rn(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 2]) * inv);
+              w[x] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            st_shared16(at + 16 * j, make_uint4(w[0], w[1], w[2], w[3]));
           }
-          dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      __syncwarp();
+      fence_proxy_async_smem();
+    }
+    epilogue_bar();
+    if (tid < kHeadsPerBlock && h0 + tid < p.H) {
+      void* dst = kSplit ? static_cast<void*>(p.ws_o + (ws_row * kHeadsPerBlock + tid) * kKvLatent)
+                         : static_cast<void*>(p.out + row * p.ld_out + (h0 + tid) * p.ld_oh);
+      asm volatile(
+          "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+          "cp.async.bulk.commit_group;\n\t"
+          "cp.async.bulk.wait_group.read 0;" ::"l"(dst), "r"(smem_u32(k_s) + tid * kPitch), "n"(kRowBytes)
+          : "memory");
     }
   }
   tc_fence_before();
@@ -828,35 +884,69 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   if (warp == kMmaWarp) tmem_put<kPair>(tmem);
 }
 
-// Joins the parts of each (row, head): weights 2^(m_i - max m), a part without a valid token
-// skipped (its accumulators were never written). One block per head, one float4 per thread and part.
-__global__ void __launch_bounds__(kKvLatent / 4) attention_join_kernel(const AttnParams p) {
+// Joins the parts of each (row, head): weights 2^(m_i - max m), a part without a valid token skipped (its
+// accumulators were never written). One block per head: four groups of 128 threads, each a float4 of the
+// row and every fourth part, so that a few rounds of loads cover the parts of one row.
+constexpr int kJoinGroups = 4;
+constexpr int kMaxParts = 256;
+
+__global__ void __launch_bounds__(kJoinGroups * kKvLatent / 4) attention_join_kernel(const AttnParams p) {
+  __shared__ float weight[kMaxParts];
+  __shared__ float4 sums[kJoinGroups - 1][kKvLatent / 4];
+  __shared__ float warp_max[kJoinGroups * 4], warp_sum[kJoinGroups * 4];
   const int row = blockIdx.x / p.H, h = blockIdx.x % p.H;
   const int64_t base = (static_cast<int64_t>(row) * p.head_blocks + h / kHeadsPerBlock) * p.parts;
-  const int r = h % kHeadsPerBlock;
-  float m = -INFINITY;
-  for (int i = 0; i < p.parts; ++i) m = fmaxf(m, __ldg(&p.ws_ml[(base + i) * kHeadsPerBlock + r].x));
-  float l = 0.f;
+  const int r = h % kHeadsPerBlock, tid = threadIdx.x;
+  const float2 ml = tid < p.parts ? __ldg(&p.ws_ml[(base + tid) * kHeadsPerBlock + r]) : make_float2(-INFINITY, 0.f);
+  float m = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if ((tid & 31) == 0) warp_max[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinGroups * 4; ++i) m = fmaxf(m, warp_max[i]);
+  const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
+  if (tid < p.parts) weight[tid] = w;
+  float l = w * ml.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+  if ((tid & 31) == 0) warp_sum[tid >> 5] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinGroups * 4; ++i) l += warp_sum[i];
+
+  const int group = tid / (kKvLatent / 4), at = tid % (kKvLatent / 4);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < p.parts; ++i) {
-    const float2 ml = __ldg(&p.ws_ml[(base + i) * kHeadsPerBlock + r]);
-    if (ml.y == 0.f) continue;
-    const float w = exp2f(ml.x - m);
-    const float4 o = __ldg(reinterpret_cast<const float4*>(p.ws_o + ((base + i) * kHeadsPerBlock + r) * kKvLatent) +
-                           threadIdx.x);
-    l = fmaf(w, ml.y, l);
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+#pragma unroll 8
+  for (int i = group; i < p.parts; i += kJoinGroups) {
+    const float f = weight[i];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (f != 0.f) {
+      o = __ldg(reinterpret_cast<const float4*>(p.ws_o + ((base + i) * kHeadsPerBlock + r) * kKvLatent) + at);
+    }
+    acc.x = fmaf(f, o.x, acc.x);
+    acc.y = fmaf(f, o.y, acc.y);
+    acc.z = fmaf(f, o.z, acc.z);
+    acc.w = fmaf(f, o.w, acc.w);
+  }
+  if (group > 0) sums[group - 1][at] = acc;
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int g = 0; g < kJoinGroups - 1; ++g) {
+    const float4 o = sums[g][at];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.out + row * p.ld_out + h * p.ld_oh + 4 * threadIdx.x) =
+  *reinterpret_cast<uint2*>(p.out + row * p.ld_out + h * p.ld_oh + 4 * at) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (p.lse && threadIdx.x == 0) {
+  if (p.lse && tid == 0) {
     p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
 }
@@ -869,7 +959,7 @@ int attention_parts(int64_t blocks, int k, int sms) {
   if (sms <= 0 || tiles <= 1 || blocks >= sms) return 1;
   int best = 1;
   int64_t best_cost = (blocks + sms - 1) / sms * (tiles + 3);
-  for (int parts = 2; parts <= tiles && blocks * parts <= 2 * sms; ++parts) {
+  for (int parts = 2; parts <= tiles && parts <= kMaxParts && blocks * parts <= 2 * sms; ++parts) {
     const int per = (tiles + parts - 1) / parts;
     if ((tiles + per - 1) / per != parts) continue;  // no part without tiles
     const int64_t cost = (blocks * parts + sms - 1) / sms * (per + 3) + 3;
@@ -1001,6 +1091,7 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
   }
   st = check_launch(fn);
   if (st != IDX_OK || p.parts == 1) return st;
-  attention_join_kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * H), kKvLatent / 4, 0, stream>>>(p);
+  attention_join_kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * H), kJoinGroups * kKvLatent / 4, 0,
+                          stream>>>(p);
   return check_launch(fn);
 }
