@@ -261,27 +261,49 @@ def idx_req_to_global_slots(local, row_to_req, block_table, block_size, block_sp
         _rows(block_table), block_size, block_span, _ptr(slots), _rows(slots), _stream(stream)))
 
 
-def _want(fn: str, name: str, t, dev: int, dtype, *shape) -> int:
-    """Device pointer of ``t`` after checking its device, dtype and shape (None: any extent) and that
-    its last dimension is contiguous."""
+def _refuse(fn: str, name: str, t, dev: int, dtype, shape) -> None:
+    """Say what is wrong with ``t`` as argument ``name`` (shape entries None: any extent)."""
     if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} must be a tensor on cuda:{dev}, got one on {t.device}")
     if t.dtype is not dtype:
         raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
-    have = t.shape
+    have = tuple(t.shape)
     if len(have) != len(shape):
         raise ValueError(f"{fn}: {name} must have {len(shape)} dimensions, got {len(have)}")
-    for h, w in zip(have, shape):
-        if w is not None and h != w:
-            raise ValueError(f"{fn}: {name} has shape {tuple(have)}, expected {shape}")
-    if have[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{fn}: {name} must have a unit stride in its last dimension")
-    return t.data_ptr()
+    if any(w is not None and h != w for h, w in zip(have, shape)):
+        raise ValueError(f"{fn}: {name} has shape {have}, expected {shape}")
+    raise ValueError(f"{fn}: {name} must have a unit stride in its last dimension")
 
 
-def _ld(t, n: int) -> int:
-    """Row stride of a 2-D tensor with ``n`` columns; of one row or none, any stride serves."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), n)
+def _vec(fn: str, name: str, t, dev: int, dtype, n: int) -> int:
+    """Device pointer of the contiguous vector ``t`` [n]. These checks run on every call of a decode step, so the
+    common case is one expression."""
+    if t.get_device() == dev and t.dtype is dtype and t.shape == (n,) and (n < 2 or t.stride(0) == 1):
+        return t.data_ptr()
+    _refuse(fn, name, t, dev, dtype, (n,))
+
+
+def _mat(fn: str, name: str, t, dev: int, dtype, rows, cols):
+    """(device pointer, row stride) of ``t`` [rows, cols] with contiguous rows (None: any extent). Of one row or
+    none, any stride serves."""
+    if t.get_device() == dev and t.dtype is dtype and t.dim() == 2:
+        r, c = t.shape
+        if (rows is None or r == rows) and (cols is None or c == cols):
+            ld, step = t.stride()
+            if step == 1 or c < 2:
+                return t.data_ptr(), ld if r > 1 or ld > c else c
+    _refuse(fn, name, t, dev, dtype, (rows, cols))
+
+
+def _heads(fn: str, name: str, t, dev: int, rows, heads, dims: int):
+    """(device pointer, row stride, head stride) of the bf16 ``t`` [rows, heads, dims]."""
+    if t.get_device() == dev and t.dtype is torch.bfloat16 and t.dim() == 3:
+        r, h, d = t.shape
+        if d == dims and (rows is None or r == rows) and (heads is None or h == heads):
+            ld, ldh, step = t.stride()
+            if step == 1:
+                return t.data_ptr(), ld if r > 1 else dims, ldh if h > 1 else dims
+    _refuse(fn, name, t, dev, torch.bfloat16, (rows, heads, dims))
 
 
 def _cuda_device(fn: str, name: str, t) -> int:
@@ -289,6 +311,9 @@ def _cuda_device(fn: str, name: str, t) -> int:
     if dev < 0:
         raise ValueError(f"{fn}: {name} must be a CUDA tensor")
     return dev
+
+
+_ENTRY = {}  # entry points by name
 
 
 def _call(fn: str, dev: int, stream, *args) -> None:
@@ -301,7 +326,9 @@ def _call(fn: str, dev: int, stream, *args) -> None:
         st = stream.cuda_stream
     else:
         st = int(stream)
-    f = getattr(library(), fn)
+    f = _ENTRY.get(fn)
+    if f is None:
+        f = _ENTRY[fn] = getattr(library(), fn)
     if dev == torch._C._cuda_getDevice():
         status = f(*args, st)
     else:
@@ -312,22 +339,23 @@ def _call(fn: str, dev: int, stream, *args) -> None:
 
 
 def _rope_args(fn: str, positions, cos_sin, n: int, dev: int):
-    if (positions is None) != (cos_sin is None):
-        raise ValueError(f"{fn}: positions and cos_sin go together")
-    if positions is None:
+    if positions is None or cos_sin is None:
+        if positions is not cos_sin:
+            raise ValueError(f"{fn}: positions and cos_sin go together")
         return None, None, 64, 1
-    p = _want(fn, "positions", positions, dev, torch.int32, n)
-    c = _want(fn, "cos_sin", cos_sin, dev, torch.float32, None, None)
-    if cos_sin.shape[1] < 64:
-        raise ValueError(f"{fn}: cos_sin needs 64 columns, got {cos_sin.shape[1]}")
-    return p, c, _ld(cos_sin, 64), cos_sin.shape[0]
+    c, ld = _mat(fn, "cos_sin", cos_sin, dev, torch.float32, None, None)
+    max_pos, cols = cos_sin.shape
+    if cols < 64:
+        raise ValueError(f"{fn}: cos_sin needs 64 columns, got {cols}")
+    return _vec(fn, "positions", positions, dev, torch.int32, n), c, ld, max_pos
 
 
 def _cache_args(fn: str, cache, dev: int, block_size: int, token_bytes: int):
-    p = _want(fn, "cache", cache, dev, torch.uint8, None, None)
-    if cache.shape[1] < block_size * token_bytes:
-        raise ValueError(f"{fn}: cache blocks of {cache.shape[1]} bytes hold fewer than {block_size} tokens")
-    return p, cache.shape[0], block_size, _ld(cache, cache.shape[1])
+    p, ld = _mat(fn, "cache", cache, dev, torch.uint8, None, None)
+    blocks, size = cache.shape
+    if size < block_size * token_bytes:
+        raise ValueError(f"{fn}: cache blocks of {size} bytes hold fewer than {block_size} tokens")
+    return p, blocks, block_size, ld
 
 
 def idx_k_norm_rope_quant_and_cache(k, weight, bias, eps, positions, cos_sin, slot_mapping, cache, block_size,
@@ -340,14 +368,17 @@ def idx_k_norm_rope_quant_and_cache(k, weight, bias, eps, positions, cos_sin, sl
     """
     fn = "idx_k_norm_rope_quant_and_cache"
     dev = _cuda_device(fn, "k", k)
-    code = _lib.IDX_BF16 if k.dtype is torch.bfloat16 else _lib.IDX_F32
-    kp = _want(fn, "k", k, dev, torch.bfloat16 if code else torch.float32, None, 128)
+    bf16 = k.dtype is torch.bfloat16
+    kp, ld_k = _mat(fn, "k", k, dev, torch.bfloat16 if bf16 else torch.float32, None, 128)
     n = k.shape[0]
-    pos, cs, ld_cs, max_pos = _rope_args(fn, positions, cos_sin, n, dev)
-    _call(fn, dev, stream, kp, code, _ld(k, 128), n, _want(fn, "weight", weight, dev, torch.float32, 128),
-          None if bias is None else _want(fn, "bias", bias, dev, torch.float32, 128), float(eps), pos, cs, ld_cs,
-          max_pos, _lib.IDX_ROPE_INTERLEAVED if interleaved else _lib.IDX_ROPE_NEOX,
-          _want(fn, "slot_mapping", slot_mapping, dev, torch.int64, n), *_cache_args(fn, cache, dev, block_size, 132),
+    if positions is None:
+        raise ValueError(f"{fn}: positions and cos_sin are required")
+    _call(fn, dev, stream, kp, _lib.IDX_BF16 if bf16 else _lib.IDX_F32, ld_k, n,
+          _vec(fn, "weight", weight, dev, torch.float32, 128),
+          None if bias is None else _vec(fn, "bias", bias, dev, torch.float32, 128), eps,
+          *_rope_args(fn, positions, cos_sin, n, dev),
+          _lib.IDX_ROPE_INTERLEAVED if interleaved else _lib.IDX_ROPE_NEOX,
+          _vec(fn, "slot_mapping", slot_mapping, dev, torch.int64, n), *_cache_args(fn, cache, dev, block_size, 132),
           _lib.IDX_SCALE_UE8M0 if ue8m0 else _lib.IDX_SCALE_FP32)
 
 
@@ -361,15 +392,15 @@ def idx_kv_norm_rope_quant_and_cache(c, pe, weight, eps, positions, cos_sin, slo
     """
     fn = "idx_kv_norm_rope_quant_and_cache"
     dev = _cuda_device(fn, "c", c)
-    code = _lib.IDX_BF16 if c.dtype is torch.bfloat16 else _lib.IDX_F32
-    dt = torch.bfloat16 if code else torch.float32
-    cp = _want(fn, "c", c, dev, dt, None, 512)
+    bf16 = c.dtype is torch.bfloat16
+    dt = torch.bfloat16 if bf16 else torch.float32
+    cp, ld_c = _mat(fn, "c", c, dev, dt, None, 512)
     n = c.shape[0]
-    pos, cs, ld_cs, max_pos = _rope_args(fn, positions, cos_sin, n, dev)
-    _call(fn, dev, stream, cp, _ld(c, 512), _want(fn, "pe", pe, dev, dt, n, 64), _ld(pe, 64), code, n,
-          None if weight is None else _want(fn, "weight", weight, dev, torch.float32, 512), float(eps), pos, cs,
-          ld_cs, max_pos, _lib.IDX_ROPE_INTERLEAVED if interleaved else _lib.IDX_ROPE_NEOX,
-          _want(fn, "slot_mapping", slot_mapping, dev, torch.int64, n), *_cache_args(fn, cache, dev, block_size, 644))
+    _call(fn, dev, stream, cp, ld_c, *_mat(fn, "pe", pe, dev, dt, n, 64), _lib.IDX_BF16 if bf16 else _lib.IDX_F32, n,
+          None if weight is None else _vec(fn, "weight", weight, dev, torch.float32, 512), eps,
+          *_rope_args(fn, positions, cos_sin, n, dev),
+          _lib.IDX_ROPE_INTERLEAVED if interleaved else _lib.IDX_ROPE_NEOX,
+          _vec(fn, "slot_mapping", slot_mapping, dev, torch.int64, n), *_cache_args(fn, cache, dev, block_size, 644))
 
 
 def idx_gather_kv(cache, block_size, block_table, cu_lens, out, starts=None, stream=None):
@@ -381,17 +412,15 @@ def idx_gather_kv(cache, block_size, block_table, cu_lens, out, starts=None, str
     """
     fn = "idx_gather_kv"
     dev = _cuda_device(fn, "out", out)
-    code = _lib.IDX_BF16 if out.dtype is torch.bfloat16 else _lib.IDX_F32
-    op = _want(fn, "out", out, dev, torch.bfloat16 if code else torch.float32, None, 576)
-    bt = _want(fn, "block_table", block_table, dev, torch.int32, None, None)
-    B = block_table.shape[0]
-    cp, blocks, bs, stride = _cache_args(fn, cache, dev, block_size, 644)
-    if B > 1 and block_table.stride(0) < block_table.shape[1]:
-        raise ValueError(f"{fn}: block_table rows must not overlap")
+    bf16 = out.dtype is torch.bfloat16
+    op, ld_out = _mat(fn, "out", out, dev, torch.bfloat16 if bf16 else torch.float32, None, 576)
+    bt, ld_bt = _mat(fn, "block_table", block_table, dev, torch.int32, None, None)
+    B, pages = block_table.shape
     # pages beyond the table's own columns do not exist, whatever its row stride
-    _call(fn, dev, stream, cp, blocks, bs, stride, bt, _ld(block_table, block_table.shape[1]), block_table.shape[1],
-          None if starts is None else _want(fn, "starts", starts, dev, torch.int32, B),
-          _want(fn, "cu_lens", cu_lens, dev, torch.int32, B + 1), B, op, code, _ld(out, 576), out.shape[0])
+    _call(fn, dev, stream, *_cache_args(fn, cache, dev, block_size, 644), bt, ld_bt, pages,
+          None if starts is None else _vec(fn, "starts", starts, dev, torch.int32, B),
+          _vec(fn, "cu_lens", cu_lens, dev, torch.int32, B + 1), B, op, _lib.IDX_BF16 if bf16 else _lib.IDX_F32,
+          ld_out, out.shape[0])
 
 
 def idx_sparse_attention_workspace_bytes(rows: int, heads: int, topk: int) -> int:
@@ -409,23 +438,20 @@ def idx_sparse_attention(q, cache, block_size, slots, out, softmax_scale, lse=No
     """
     fn = "idx_sparse_attention"
     dev = _cuda_device(fn, "q", q)
-    qp = _want(fn, "q", q, dev, torch.bfloat16, None, None, 576)
-    T, H = q.shape[0], q.shape[1]
-    op = _want(fn, "out", out, dev, torch.bfloat16, T, H, 512)
-    sp = _want(fn, "slots", slots, dev, torch.int32, T, None)
-    k = slots.shape[1]
-    cp, blocks, bs, stride = _cache_args(fn, cache, dev, block_size, 644)
+    qp, ld_q, ld_qh = _heads(fn, "q", q, dev, None, None, 576)
+    T, H, _ = q.shape
+    op, ld_out, ld_oh = _heads(fn, "out", out, dev, T, H, 512)
+    sp, ld_slots = _mat(fn, "slots", slots, dev, torch.int32, T, None)
     wp, wb = None, 0
     if ws is not None:
         if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"{fn}: ws must be a contiguous tensor on cuda:{dev}")
         wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
-    _call(fn, dev, stream, qp, q.stride(0) if T > 1 else 576, q.stride(1) if H > 1 else 576, cp, blocks, bs, stride,
-          block_size if block_span is None else block_span, sp, _ld(slots, k), k,
-          None if n_sel is None else _want(fn, "n_sel", n_sel, dev, torch.int32, T), T, H, float(softmax_scale),
-          op, out.stride(0) if T > 1 else 512, out.stride(1) if H > 1 else 512,
-          None if lse is None else _want(fn, "lse", lse, dev, torch.float32, T, H), 0 if lse is None else _ld(lse, H),
-          wp, wb)
+    lp, ld_lse = (None, 0) if lse is None else _mat(fn, "lse", lse, dev, torch.float32, T, H)
+    cp, blocks, bs, stride = _cache_args(fn, cache, dev, block_size, 644)
+    _call(fn, dev, stream, qp, ld_q, ld_qh, cp, blocks, bs, stride, bs if block_span is None else block_span, sp,
+          ld_slots, slots.shape[1], None if n_sel is None else _vec(fn, "n_sel", n_sel, dev, torch.int32, T), T, H,
+          softmax_scale, op, ld_out, ld_oh, lp, ld_lse, wp, wb)
 
 
 def idx_block_span(block_stride: int, token_stride: int) -> int:

@@ -8,7 +8,6 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
-#include <type_traits>
 
 #include "common.cuh"
 #include "kv_layout.cuh"
@@ -75,9 +74,13 @@ constexpr int kTile = 64;
 constexpr int kPieces = kKvDim / 64;             // 128-byte pieces of a token's bf16 row
 constexpr int kPieceBytes = 64 * 128;            // one piece of 64 rows
 constexpr int kQBytes = kPieces * kPieceBytes;
+constexpr int kStageBytes = kPieces * kPieceBytes;
 constexpr int kStages = 2;
 constexpr int kLoaderWarps = 16;
 constexpr int kGroupWarps = kLoaderWarps / kStages;  // each stage has its own group of loader warps
+constexpr int kTokensPerWarp = kTile / kGroupWarps;
+static_assert(kTokensPerWarp == 8, "a loader warp's tokens are eight rows of the swizzle");
+constexpr int kEarly = 2;  // of a warp's tokens, those converted while the stage is still in use
 constexpr int kMmaWarp = 4 + kLoaderWarps;
 constexpr int kRopeWarp = kMmaWarp + 1;          // one per stage
 constexpr int kThreads = (kRopeWarp + kStages) * 32;
@@ -90,11 +93,10 @@ constexpr float kRescaleStep = 8.0f;             // log2: P may reach 2^8 before
 
 struct Shared {
   uint64_t q_full, drained;
-  uint64_t k_full[kStages];                      // a stage's keys are stored (a pair: the leader's, for both blocks)
-  uint64_t v_full[kStages];                      // a pair's values likewise
-  uint64_t s_full[kStages];                      // S of the tile is complete: a pair's keys are free
-  uint64_t p_full[kStages];                      // P is stored (a pair: the leader's, for both blocks)
-  uint64_t o_done[kStages];                      // the tile's share of O is complete: P and the values are free
+  uint64_t k_full[kStages];                      // a stage's tokens are stored
+  uint64_t s_full[kStages];                      // S of the tile is complete
+  uint64_t p_full[kStages];                      // P is stored
+  uint64_t o_done[kStages];                      // the tile's share of O is complete: P and the stage are free
   uint64_t flags[kValidRing];                    // `valid` is written
   uint32_t tmem;
   volatile uint32_t dead;                        // a wait expired: no further wait blocks
@@ -103,20 +105,8 @@ struct Shared {
   float inv[kHeadsPerBlock];                     // 1 / sum of each head
 };
 
-// A stage's keys (all 576 dims of this block's tokens of a tile) and, of a pair, its values (256
-// dims of all 64 tokens; a block alone reads them out of its keys). Keys of a pair are free once S is
-// complete, values once O is, so the next tile's S does not wait for this one's softmax.
-template <bool kPair>
-struct Stage {
-  static constexpr int kTokens = kPair ? kTile / 2 : kTile;  // in the block's keys
-  static constexpr int kKeyPiece = kTokens * 128;
-  static constexpr int kKeys = kPieces * kKeyPiece;
-  static constexpr int kValues = kPair ? kKvLatent / 2 / 64 * kPieceBytes : 0;
-  static constexpr int kPBufs = kPair ? 2 : 1;
-  static constexpr int kSmem =
-      kQBytes + kStages * (kKeys + kValues) + kPBufs * kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
-  static_assert(kSmem <= 232448, "shared memory of one block");
-};
+constexpr int kSmemBytes = kQBytes + kStages * kStageBytes + kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
+static_assert(kSmemBytes <= 232448, "shared memory of one block");
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_n_major) {
   // D fp32 (bits 4-5), A and B bf16 (7-9, 10-12), B's major (16), N >> 3 (17-22), M >> 4 (24-28)
@@ -139,69 +129,26 @@ __device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr) {
 
 // Issued by the lane with `issue` set; the whole warp passes here converged, so the descriptors stay in
 // uniform registers (N = 64 products then go out every 32 clocks; issued from a branch of one
-// lane, every 45 to 56). A pair's leader issues for both blocks.
-template <bool kPair>
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
-                                         uint32_t issue) {
-  if constexpr (kPair) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-        "r"(acc), "r"(issue)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-        "r"(acc), "r"(issue)
-        : "memory");
-  }
+// lane, every 45 to 56).
+__device__ __forceinline__ void mma_ws_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                            uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(acc), "r"(issue)
+      : "memory");
 }
 
-// Arrives on the barrier, of a pair on that of both blocks, once everything issued so far is complete.
-template <bool kPair>
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t issue) {
-  if constexpr (kPair) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
-        "setp.ne.b32 e, %1, 0;\n\t"
-        "mov.b16 m, 3;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
-        ::"r"(smem_u32(bar)), "r"(issue)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "setp.ne.b32 e, %1, 0;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(issue)
-        : "memory");
-  }
-}
-
-template <bool kPair>
-__device__ __forceinline__ void tmem_get(uint32_t* dst) {
-  if constexpr (kPair) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
-                 "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)), "r"(kTmemCols)
-                 : "memory");
-  } else {
-    tmem_alloc(dst, kTmemCols);
-    tmem_relinquish();
-  }
-}
-
-template <bool kPair>
-__device__ __forceinline__ void tmem_put(uint32_t taddr) {
-  if constexpr (kPair) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
-  } else {
-    tmem_dealloc(taddr, kTmemCols);
-  }
+// Arrives on the barrier once everything issued so far is complete.
+__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(issue)
+      : "memory");
 }
 
 // Sixteen columns of the thread's lane, read (valid after the wait inside) or written.
@@ -252,30 +199,6 @@ __device__ __forceinline__ void wait_bar(Shared& sh, uint64_t* bar, uint32_t par
     }
   }
   __syncwarp();
-}
-
-// --- the other block of a pair (a cluster of two) -------------------------------
-__device__ __forceinline__ uint32_t peer_addr(const void* ptr, uint32_t rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(ptr)), "r"(rank));
-  return a;
-}
-
-// Arrives on a barrier of either block. What it announces was written to this block's own shared memory
-// for the tensor core of this SM, and fence.proxy.async has made it visible there, so no release at
-// cluster scope is needed (it measured a thousand clocks a hop).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-// Arrives on this barrier, of a pair on the leader's.
-template <bool kPair>
-__device__ __forceinline__ void arrive_lead(uint64_t* bar) {
-  if constexpr (kPair) mbar_arrive_cluster(peer_addr(bar, 0)); else mbar_arrive(bar);
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -346,16 +269,14 @@ __device__ __forceinline__ Token locate(const AttnParams& p, int slot) {
   return t;
 }
 
-template <bool kSplit, bool kPair>
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  using St = Stage<kPair>;
   uint8_t* q_s = smem;
   uint8_t* k_s = q_s + kQBytes;
-  uint8_t* v_s = k_s + kStages * St::kKeys;
-  uint8_t* p_s = v_s + kStages * St::kValues;
-  Shared& sh = *reinterpret_cast<Shared*>(p_s + St::kPBufs * kPieceBytes);
+  uint8_t* p_s = k_s + kStages * kStageBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(p_s + kPieceBytes);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // head groups vary fastest: the blocks that read the same tokens run side by side
@@ -363,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   const int part = kSplit ? (blockIdx.x / p.head_blocks) % p.parts : 0;
   const int row = blockIdx.x / (p.head_blocks * p.parts);
   const int h0 = hb * kHeadsPerBlock;
-  const uint32_t rank = kPair ? blockIdx.x & 1u : 0u;  // 0: the pair's leader
   int n = p.k;
   if (p.n_sel) n = min(n, max(__ldg(p.n_sel + row), 0));
   const int first = part * p.part_tiles * kTile;  // of this block's entries
@@ -391,41 +311,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   auto setup = [&]() {
     tc_fence_before();
     __syncwarp();
-    if (kPair) cluster_sync();  // the other block's barriers exist too
     asm volatile("bar.sync 0;" ::: "memory");
     tc_fence_after();
     tmem = sh.tmem;
   };
 
-  // The loaders' role, compiled for either rank of a pair: addresses that depend on it stay immediates.
-  auto loader = [&](auto rank_of) {
-    constexpr uint32_t rank = decltype(rank_of)::value;
+  if (warp >= 4 && warp < kMmaWarp) {
     // ---------------------------------------------------------------- loaders
-    // Of a pair, a block gathers half of a tile's tokens whole, as keys, and of the others the 256 dims
-    // that it keeps as values. (Values fetched from the other block's shared memory instead came at some
-    // 10 bytes a clock, by stores as by bulk copies, and bounded the tile.)
-    constexpr int kOwn = St::kTokens / kGroupWarps;     // a warp's whole tokens
-    constexpr int kOther = kPair ? kOwn : 0;            // and the others
-    constexpr int kLocated = kOwn + kOther;
-    constexpr int kEarly = 2;  // tokens converted while the stage is still in use; the registers hold no more
     const int group = (warp - 4) / kGroupWarps, lw = (warp - 4) % kGroupWarps;  // this group's tiles: group, group + 2, ...
-    const int r0 = kOwn * lw;                                     // the warp's first row of the stage's keys
-    const int own_at = static_cast<int>(rank) * St::kTokens + r0;  // and its token of the tile
-    const int other_at = static_cast<int>(rank ^ 1u) * St::kTokens + r0;
+    const int r0 = kTokensPerWarp * lw;  // the warp's first token of a tile
     const int32_t* list = p.slots + row * p.ld_slots + first;
     const int count = n - first;
-    const int which = lane % kLocated;  // of the warp's tokens, the one that this lane locates
-    const int mine = kPair && which >= kOwn ? other_at + which - kOwn : own_at + which;
+    const int mine = r0 + lane % kTokensPerWarp;  // entry of a tile that this lane locates
     const int left = count - mine;      // entries from its first one on
     const int32_t* my_list = list + mine;
     auto entry = [&](int tile) { return tile * kTile < left ? __ldg(my_list + tile * kTile) : -1; };
 
-    // Lane l stores unit l % 8 of piece l / 8 (of the first half of the dims, of a pair the block's own,
-    // and of the other): it holds the eight dims that the swizzle puts there. So the loads' addresses
-    // depend on the row, and the stores', which would take registers, do not.
-    auto chunk = [&](int j) { return 8u * (static_cast<uint32_t>(lane) ^ (static_cast<uint32_t>(r0 + j) & 7u)); };
-    uint2 raw[kOwn][2];                // eight dims in either half of each token
-    uint2 half_raw[kPair ? kOwn : 1];  // and in the block's own half of the others
+    // Lane l stores unit l % 8 of piece l / 8 and of piece 4 + l / 8: it holds the eight dims of either half
+    // that the swizzle puts there. So the loads' addresses depend on the row, and the stores', which
+    // would take registers, do not.
+    uint2 raw[kTokensPerWarp][2];
     // Tokens are located two tiles of the group ahead of their conversion, and their slots read one more
     // ahead: nothing between two tiles' loads waits for an address.
     uint32_t codes = 0, next_codes = 0, found_codes = 0;
@@ -438,19 +343,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       found_codes = 0;
       if (latent) found_codes = __ldg(tok.codes);
     };
-    auto load_own = [&]() {
+    auto load = [&]() {
 #pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
+      for (int j = 0; j < kTokensPerWarp; ++j) {
         const uint8_t* src = shfl_ptr(latent, j);
-        raw[j][0] = load8_if(src + 256 * rank + chunk(j), src != nullptr);
-        raw[j][1] = load8_if(src + 256 * (rank ^ 1u) + chunk(j), src != nullptr);
-      }
-    };
-    auto load_other = [&]() {
-#pragma unroll
-      for (int j = 0; j < kOther; ++j) {
-        const uint8_t* src = shfl_ptr(latent, kOwn + j);
-        half_raw[j] = load8_if(src + 256 * rank + chunk(j), src != nullptr);
+        raw[j][0] = load8_if(src + 8 * (lane ^ j), src != nullptr);  // r0 is a multiple of eight: row j of the swizzle
+        raw[j][1] = load8_if(src + 256 + 8 * (lane ^ j), src != nullptr);
       }
     };
     // eight dims in half h of the token with these scale codes
@@ -462,68 +360,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       kv_dequant4_even_odd(x.y, mul, w.z, w.w);
       return w;
     };
-    // shared addresses in 32 bits: the registers are all taken
-    const uint32_t keys = smem_u32(k_s) + group * St::kKeys + (lane >> 3) * St::kKeyPiece + r0 * 128 + 16 * (lane & 7);
-    const uint32_t keys_of[2] = {keys + 4 * rank * St::kKeyPiece, keys + 4 * (rank ^ 1u) * St::kKeyPiece};
-    const uint32_t values = smem_u32(v_s) + group * St::kValues + (lane >> 3) * kPieceBytes + 16 * (lane & 7);
+    const uint32_t unit = smem_u32(k_s) + group * kStageBytes + (lane >> 3) * kPieceBytes + r0 * 128 + 16 * (lane & 7);
 
     if (group < tiles) {
       next_slot = entry(group);
       find(group);
-      load_own();
-      load_other();
+      load();
       next_codes = found_codes;
       find(group + kStages);
     }
     setup();
     for (int i = group; i < tiles; i += kStages) {
       codes = __vminu4(next_codes, kKvMaxScaleCode * 0x01010101u);
-      uint4 first_half[kOwn], second_half[kOwn];
+      uint4 early[kEarly][2];
 #pragma unroll
       for (int j = 0; j < kEarly; ++j) {
         const uint32_t word = word_of(j);
-        first_half[j] = convert(raw[j][0], word, rank);
-        second_half[j] = convert(raw[j][1], word, rank ^ 1u);
+        early[j][0] = convert(raw[j][0], word, 0);
+        early[j][1] = convert(raw[j][1], word, 1);
       }
-      if (i >= kStages) wait_bar(sh, kPair ? &sh.s_full[group] : &sh.o_done[group], ((i >> 1) - 1) & 1);
+      if (i >= kStages) wait_bar(sh, &sh.o_done[group], ((i >> 1) - 1) & 1);
 #pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        if (j >= kEarly) {
-          const uint32_t word = word_of(j);
-          first_half[j] = convert(raw[j][0], word, rank);
-          second_half[j] = convert(raw[j][1], word, rank ^ 1u);
+      for (int j = 0; j < kTokensPerWarp; ++j) {
+        const uint32_t word = j < kEarly ? 0u : word_of(j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          st_shared16(unit + 4 * h * kPieceBytes + j * 128, j < kEarly ? early[j % kEarly][h] : convert(raw[j][h], word, h));
         }
-        st_shared16(keys_of[0] + j * 128, first_half[j]);
-        st_shared16(keys_of[1] + j * 128, second_half[j]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_lead<kPair>(&sh.k_full[group]);
-      // before the next loads: a conversion behind them would wait for them too
-#pragma unroll
-      for (int j = 0; j < kOther; ++j) second_half[j] = convert(half_raw[j], word_of(kOwn + j), rank);
-      if (i + kStages < tiles) load_own();
-      if (kPair) {
-        if (i >= kStages) wait_bar(sh, &sh.o_done[group], ((i >> 1) - 1) & 1);
-#pragma unroll
-        for (int j = 0; j < kOther; ++j) {
-          st_shared16(values + own_at * 128 + j * 128, first_half[j]);
-          st_shared16(values + other_at * 128 + j * 128, second_half[j]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_lead<kPair>(&sh.v_full[group]);
-        if (i + kStages < tiles) load_other();
-      }
+      if (lane == 0) mbar_arrive(&sh.k_full[group]);
+      if (i + kStages < tiles) load();
       next_codes = found_codes;
       find(i + 2 * kStages);
-    }
-  };
-  if (warp >= 4 && warp < kMmaWarp) {
-    if (kPair && rank == 1) {
-      loader(std::integral_constant<uint32_t, 1>{});
-    } else {
-      loader(std::integral_constant<uint32_t, 0>{});
     }
   } else if (warp >= kRopeWarp) {
     // ---------------------------------------------------------------- position dims, and L2 prefetch
@@ -552,24 +422,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       }
       __syncwarp();
     };
-    // a pair's block looks after its own half
-    const int h0p = kPair ? static_cast<int>(rank) : 0, h1p = kPair ? static_cast<int>(rank) : 1;
     for (int i = group; i < kAhead && i < tiles; i += kStages) {
-      for (int h = h0p; h <= h1p; ++h) prefetch(entry(i, h));
+      prefetch(entry(i, 0));
+      prefetch(entry(i, 1));
     }
     int s0 = entry(group, 0), s1 = entry(group, 1);
-    int a0 = entry(group + kAhead, h0p), a1 = entry(group + kAhead, h1p);
-    const uint32_t piece = smem_u32(k_s) + group * St::kKeys + (kPieces - 1) * St::kKeyPiece;
+    int a0 = entry(group + kAhead, 0), a1 = entry(group + kAhead, 1);
+    const uint32_t piece = smem_u32(k_s) + group * kStageBytes + (kPieces - 1) * kPieceBytes;
     setup();
     for (int i = group; i < tiles; i += kStages) {
       const uint8_t* src[2] = {locate(p, s0).rope, locate(p, s1).rope};
       s0 = entry(i + kStages, 0);
       s1 = entry(i + kStages, 1);
-      if (i >= kStages) wait_bar(sh, kPair ? &sh.s_full[group] : &sh.o_done[group], ((i >> 1) - 1) & 1);
+      // only S reads position dims, so their piece is free long before the stage is
+      if (i >= kStages) wait_bar(sh, &sh.s_full[group], ((i >> 1) - 1) & 1);
 #pragma unroll
-      for (int c = 0; c < St::kTokens / 4; ++c) {
-        const int t = 4 * c + (lane >> 3), u = lane & 7;  // row of the stage's keys
-        const uint8_t* from = shfl_ptr(kPair ? (rank ? src[1] : src[0]) : src[c / 8], t & 31);
+      for (int c = 0; c < kTile / 4; ++c) {
+        const int t = 4 * c + (lane >> 3), u = lane & 7;
+        const uint8_t* from = shfl_ptr(src[c / 8], t & 31);
         copy16_if(piece + t * 128 + ((u ^ (t & 7)) << 4), from ? from + 16 * u : p.cache, from != nullptr);
       }
       const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, src[0] != nullptr);
@@ -583,23 +453,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_lead<kPair>(&sh.k_full[group]);
+      if (lane == 0) mbar_arrive(&sh.k_full[group]);
       if (i + kAhead < tiles) {
         prefetch(a0);
-        if (!kPair) prefetch(a1);
-        a0 = entry(i + kStages + kAhead, h0p);
-        a1 = entry(i + kStages + kAhead, h1p);
+        prefetch(a1);
+        a0 = entry(i + kStages + kAhead, 0);
+        a1 = entry(i + kStages + kAhead, 1);
       }
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
-      mbar_init(&sh.q_full, kPair ? 8 : 4);  // of a pair: the leader's, with the other block's warps
+      mbar_init(&sh.q_full, 4);
       mbar_init(&sh.drained, 1);
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(&sh.k_full[i], (kPair ? 2 : 1) * (kGroupWarps + 1));
-        mbar_init(&sh.v_full[i], 2 * kGroupWarps);
+        mbar_init(&sh.k_full[i], kGroupWarps + 1);
         mbar_init(&sh.s_full[i], 1);
-        mbar_init(&sh.p_full[i], kPair ? 8 : 4);
+        mbar_init(&sh.p_full[i], 4);
         mbar_init(&sh.o_done[i], 1);
       }
       for (int i = 0; i < kValidRing; ++i) mbar_init(&sh.flags[i], 1);
@@ -607,10 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       fence_mbar_init();
     }
     __syncwarp();
-    tmem_get<kPair>(&sh.tmem);
+    tmem_alloc(&sh.tmem, kTmemCols);
+    tmem_relinquish();
     setup();
-  }
-  if (warp == kMmaWarp && rank == 0) {
     // ---------------------------------------------------------------- matrix instructions
     // Whichever of the next S and the next O product has its operands goes first, O before S.
     uint32_t lead;
@@ -618,32 +486,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     const uint64_t q_desc = sw128_kmajor_desc(smem_u32(q_s));
     const uint64_t p_desc = sw128_kmajor_desc(smem_u32(p_s));
     const uint64_t k_desc = sw128_kmajor_desc(smem_u32(k_s));
-    // values: the pieces of a block's 128 (pair: the other 128 are the other block's) or 256 dims of a product
-    const uint64_t v_desc = sw128_nmajor_desc(smem_u32(kPair ? v_s : k_s));
-    constexpr int kValueStage = kPair ? St::kValues : St::kKeys;
-    constexpr int kValuePieces = kPair ? 2 : 4;
+    const uint64_t v_desc = sw128_nmajor_desc(smem_u32(k_s));
     wait_bar(sh, &sh.q_full, 0);
     const int total = __shfl_sync(0xFFFFFFFFu, tiles, 0);
     int s_next = 0, o_next = 0;
     uint64_t t0 = global_timer_ns();
     int idle = 0;
     while (o_next < total) {
-      const bool can_o = o_next < s_next && mbar_test(&sh.p_full[o_next & 1], (o_next >> 1) & 1) &&
-                         (!kPair || mbar_test(&sh.v_full[o_next & 1], (o_next >> 1) & 1));
+      const bool can_o = o_next < s_next && mbar_test(&sh.p_full[o_next & 1], (o_next >> 1) & 1);
       if (__all_sync(0xFFFFFFFFu, can_o)) {
         tc_fence_after();
         const int st = o_next & 1;
-        const uint64_t v = v_desc + st * (kValueStage >> 4);
+        const uint64_t v = v_desc + st * (kStageBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            mma_bf16<kPair>(tmem + half * (kOCols / 2), p_desc + (kPair ? st * (kPieceBytes >> 4) : 0) + 2 * ks,
-                            v + ((kValuePieces * half * kPieceBytes + 2048 * ks) >> 4),
-                            idesc_bf16(kPair ? 128 : 64, 256, true), o_next > 0 || ks > 0, lead);
+            mma_ws_bf16(tmem + half * (kOCols / 2), p_desc + 2 * ks, v + ((4 * half * kPieceBytes + 2048 * ks) >> 4),
+                        idesc_bf16(64, 256, true), o_next > 0 || ks > 0, lead);
           }
         }
-        commit<kPair>(&sh.o_done[st], lead);
+        commit_if(&sh.o_done[st], lead);
         ++o_next;
         idle = 0;
         continue;
@@ -653,17 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       if (__all_sync(0xFFFFFFFFu, can_s)) {
         tc_fence_after();
         const int st = s_next & 1;
-        const uint64_t k = k_desc + st * (St::kKeys >> 4);
+        const uint64_t k = k_desc + st * (kStageBytes >> 4);
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            mma_bf16<kPair>(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks,
-                            k + ((c * St::kKeyPiece) >> 4) + 2 * ks, idesc_bf16(kPair ? 128 : 64, 64, false),
-                            c > 0 || ks > 0, lead);
+            mma_ws_bf16(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks,
+                        k + ((c * kPieceBytes) >> 4) + 2 * ks, idesc_bf16(64, 64, false), c > 0 || ks > 0, lead);
           }
         }
-        commit<kPair>(&sh.s_full[st], lead);
+        commit_if(&sh.s_full[st], lead);
         ++s_next;
         idle = 0;
         continue;
@@ -679,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       if (__any_sync(0xFFFFFFFFu, expired)) break;
     }
     if (o_next < total) {  // given up: whatever was issued finishes before the tensor memory is freed
-      commit<kPair>(&sh.drained, lead);
+      commit_if(&sh.drained, lead);
       t0 = global_timer_ns();
       while (!mbar_test(&sh.drained, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
       }
@@ -722,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_lead<kPair>(bar);
+      if (lane == 0) mbar_arrive(bar);
     };
     arrive(&sh.q_full);
 
@@ -768,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       if (i > 0) {
         // O is complete up to the last tile (for a rescaling), and with it the only P is free
         const bool scale_o = __any_sync(0xFFFFFFFFu, rise);
-        if (!kPair || scale_o) wait_bar(sh, &sh.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
+        wait_bar(sh, &sh.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
         if (scale_o) {
           tc_fence_after();
           const float f = rise ? exp2_approx(m - m_new) : 1.0f;  // m = -inf: 0, and O is 0
@@ -795,9 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
         w[c / 2] = *reinterpret_cast<const uint32_t*>(&h);
       }
-      // of two P, the one that tile i - 2 used
-      if (kPair && i >= 2) wait_bar(sh, &sh.o_done[st], ((i >> 1) - 1) & 1);
-      const uint32_t p_row = smem_u32(p_s) + (kPair ? st * kPieceBytes : 0) + r * 128;
+      const uint32_t p_row = smem_u32(p_s) + r * 128;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         st_shared16(p_row + (((4 * half + c) ^ (r & 7)) << 4), make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
@@ -825,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     // registers, 16 bytes of a row each, the rows of 64 heads took 5500 clocks, 10500 in fp32.)
     constexpr int kRowBytes = kKvLatent * (kSplit ? 4 : 2);
     constexpr int kPitch = kRowBytes + 16;  // eight rows' stores fall into different banks
-    static_assert(kHeadsPerBlock * kPitch <= kStages * (St::kKeys + St::kValues), "the rows fit the stages");
+    static_assert(kHeadsPerBlock * kPitch <= kStages * kStageBytes, "the rows fit the stages");
     wait_bar(sh, &sh.o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
     tc_fence_after();
     epilogue_bar();
@@ -837,9 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         uint32_t o[32];
         tmem_ld_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c, o);
         tmem_wait_ld(o);
-        // A product has 256 dims, 128 to each lane half: of a block alone consecutive ones, of a pair 128
-        // of each block's 256. Dims 1 and 2 of every four have changed places.
-        const int dim = kPair ? 256 * half + c : (c / 128) * 256 + half * 128 + (c % 128);
+        // A product has 256 dims, 128 to each lane half. Dims 1 and 2 of every four have changed places.
+        const int dim = (c / 128) * 256 + half * 128 + (c % 128);
         const uint32_t at = smem_u32(k_s) + r * kPitch + dim * (kSplit ? 4 : 2);
         if (kSplit) {
 #pragma unroll
@@ -874,14 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   }
   tc_fence_before();
   __syncwarp();
-  if (kPair) {
-    // neither block ends while the other may still arrive in it or read its operands
-    __syncwarp();
-    cluster_sync();
-  }
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_put<kPair>(tmem);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the parts of each (row, head): weights 2^(m_i - max m), a part without a valid token skipped (its
@@ -1066,29 +920,10 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
     p.ws_o = static_cast<float*>(ws);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + blocks * p.parts * kHeadsPerBlock * kKvLatent);
   }
-  // Rows of an even number of head groups run as pairs of blocks.
-  const bool pair = p.head_blocks % 2 == 0;
-  auto* kernel = p.parts > 1 ? (pair ? attention_kernel<true, true> : attention_kernel<true, false>)
-                             : (pair ? attention_kernel<false, true> : attention_kernel<false, false>);
-  const int smem = pair ? Stage<true>::kSmem : Stage<false>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto* kernel = p.parts > 1 ? attention_kernel<true> : attention_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = pair ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(IDX_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
-  }
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
   st = check_launch(fn);
   if (st != IDX_OK || p.parts == 1) return st;
   attention_join_kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * H), kJoinGroups * kKvLatent / 4, 0,

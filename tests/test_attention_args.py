@@ -109,16 +109,29 @@ def test_bindings_refuse_host_tensors_and_wrong_shapes():
                                  f(4, 8, 512, dtype=bf), 0.04)
     # the checks behind the device check, on what they see of a tensor
     with pytest.raises(ValueError, match="must be torch.int32"):
-        idx._want("f", "x", f(4), -1, i32, 4)
+        idx._vec("f", "x", f(4), -1, i32, 4)
     with pytest.raises(ValueError, match="dimensions"):
-        idx._want("f", "x", f(4), -1, torch.float32, 4, 1)
+        idx._mat("f", "x", f(4), -1, torch.float32, 4, 1)
     with pytest.raises(ValueError, match="shape"):
-        idx._want("f", "x", f(4, 3), -1, torch.float32, None, 4)
+        idx._mat("f", "x", f(4, 3), -1, torch.float32, None, 4)
+    with pytest.raises(ValueError, match="shape"):
+        idx._vec("f", "x", f(5), -1, torch.float32, 4)
     with pytest.raises(ValueError, match="unit stride"):
-        idx._want("f", "x", f(4, 6)[:, ::2], -1, torch.float32, 4, 3)
+        idx._mat("f", "x", f(4, 6)[:, ::2], -1, torch.float32, 4, 3)
+    with pytest.raises(ValueError, match="unit stride"):
+        idx._vec("f", "x", f(8)[::2], -1, torch.float32, 4)
+    with pytest.raises(ValueError, match="unit stride"):
+        idx._heads("f", "x", f(2, 3, 1152, dtype=bf)[:, :, ::2], -1, 2, 3, 576)
+    with pytest.raises(ValueError, match="shape"):
+        idx._heads("f", "x", f(2, 3, 576, dtype=bf), -1, 2, 4, 576)
     with pytest.raises(ValueError, match="go together"):
         idx._rope_args("f", None, f(8, 64), 4, -1)
+    with pytest.raises(ValueError, match="go together"):
+        idx._rope_args("f", f(4, dtype=i32), None, 4, -1)
     with pytest.raises(ValueError, match="64 columns"):
         idx._rope_args("f", f(4, dtype=i32), f(8, 63), 4, -1)
     with pytest.raises(ValueError, match="fewer than"):
         idx._cache_args("f", f(8, 41215, dtype=u8), -1, 64, 644)
+    # strides of what has one row or one head only do not matter
+    assert idx._mat("f", "x", f(1, 576)[:, :512], -1, torch.float32, 1, 512)[1] >= 512
+    assert idx._heads("f", "x", f(1, 1, 576, dtype=bf), -1, 1, 1, 576)[1:] == (576, 576)
