@@ -80,7 +80,7 @@ constexpr int kLoaderWarps = 16;
 constexpr int kGroupWarps = kLoaderWarps / kStages;  // each stage has its own group of loader warps
 constexpr int kTokensPerWarp = kTile / kGroupWarps;
 static_assert(kTokensPerWarp == 8, "a loader warp's tokens are eight rows of the swizzle");
-constexpr int kEarly = 2;  // of a warp's tokens, those converted while the stage is still in use
+constexpr int kEarly = 3;  // of a warp's tokens, those converted while the stage is still in use
 constexpr int kMmaWarp = 4 + kLoaderWarps;
 constexpr int kRopeWarp = kMmaWarp + 1;          // one per stage
 constexpr int kThreads = (kRopeWarp + kStages) * 32;
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   Shared& sh = *reinterpret_cast<Shared*>(p_s + kPieceBytes);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (kSplit) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
   // head groups vary fastest: the blocks that read the same tokens run side by side
   const int hb = blockIdx.x % p.head_blocks;
   const int part = kSplit ? (blockIdx.x / p.head_blocks) % p.parts : 0;
@@ -681,8 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- epilogue
     // The loaders, four to a lane quarter and 64 columns each, write O (bf16, or the sums of a part) into the
-    // stages' memory, a row of it per head, and whole rows leave as bulk copies. (Stored from the
-    // registers, 16 bytes of a row each, the rows of 64 heads took 5500 clocks, 10500 in fp32.)
+    // stages' memory, a row of it per head, and all warps store whole rows. (Stored from the registers, 16
+    // bytes of a row each, the rows of 64 heads took 5500 clocks, 10500 in fp32; as bulk copies, whose
+    // end the block has to wait for, 2300 to 5800.)
     constexpr int kRowBytes = kKvLatent * (kSplit ? 4 : 2);
     constexpr int kPitch = kRowBytes + 16;  // eight rows' stores fall into different banks
     static_assert(kHeadsPerBlock * kPitch <= kStages * kStageBytes, "the rows fit the stages");
@@ -718,17 +720,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
           }
         }
       }
-      fence_proxy_async_smem();
     }
     epilogue_bar();
-    if (tid < kHeadsPerBlock && h0 + tid < p.H) {
-      void* dst = kSplit ? static_cast<void*>(p.ws_o + (ws_row * kHeadsPerBlock + tid) * kKvLatent)
-                         : static_cast<void*>(p.out + row * p.ld_out + (h0 + tid) * p.ld_oh);
-      asm volatile(
-          "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
-          "cp.async.bulk.commit_group;\n\t"
-          "cp.async.bulk.wait_group.read 0;" ::"l"(dst), "r"(smem_u32(k_s) + tid * kPitch), "n"(kRowBytes)
-          : "memory");
+    constexpr int kUnits = kRowBytes / 16;
+    const int heads = min(kHeadsPerBlock, p.H - h0);
+    for (int i = tid; i < heads * kUnits; i += kMmaWarp * 32) {
+      const int r = i / kUnits, u = i % kUnits;
+      uint8_t* dst = kSplit ? reinterpret_cast<uint8_t*>(p.ws_o + (ws_row * kHeadsPerBlock + r) * kKvLatent)
+                            : reinterpret_cast<uint8_t*>(p.out + row * p.ld_out + (h0 + r) * p.ld_oh);
+      *reinterpret_cast<uint4*>(dst + 16 * u) = ld_shared16(smem_u32(k_s) + r * kPitch + 16 * u);
     }
   }
   tc_fence_before();
@@ -751,7 +751,8 @@ __global__ void __launch_bounds__(kJoinGroups * kKvLatent / 4) attention_join_ke
   const int row = blockIdx.x / p.H, h = blockIdx.x % p.H;
   const int64_t base = (static_cast<int64_t>(row) * p.head_blocks + h / kHeadsPerBlock) * p.parts;
   const int r = h % kHeadsPerBlock, tid = threadIdx.x;
-  const float2 ml = tid < p.parts ? __ldg(&p.ws_ml[(base + tid) * kHeadsPerBlock + r]) : make_float2(-INFINITY, 0.f);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // every part is complete and visible
+  const float2 ml = tid < p.parts ? __ldcg(&p.ws_ml[(base + tid) * kHeadsPerBlock + r]) : make_float2(-INFINITY, 0.f);
   float m = ml.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -777,7 +778,7 @@ __global__ void __launch_bounds__(kJoinGroups * kKvLatent / 4) attention_join_ke
     const float f = weight[i];
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (f != 0.f) {
-      o = __ldg(reinterpret_cast<const float4*>(p.ws_o + ((base + i) * kHeadsPerBlock + r) * kKvLatent) + at);
+      o = __ldcg(reinterpret_cast<const float4*>(p.ws_o + ((base + i) * kHeadsPerBlock + r) * kKvLatent) + at);
     }
     acc.x = fmaf(f, o.x, acc.x);
     acc.y = fmaf(f, o.y, acc.y);
@@ -926,7 +927,20 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
   kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
   st = check_launch(fn);
   if (st != IDX_OK || p.parts == 1) return st;
-  attention_join_kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * H), kJoinGroups * kKvLatent / 4, 0,
-                          stream>>>(p);
+  // launched while the parts run: its blocks wait at their first instruction for the parts' end
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(T) * static_cast<unsigned>(H));
+  cfg.blockDim = dim3(kJoinGroups * kKvLatent / 4);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t ej = cudaLaunchKernelEx(&cfg, attention_join_kernel, p);
+  if (ej != cudaSuccess) {
+    cudaGetLastError();
+    return fail(IDX_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(ej));
+  }
   return check_launch(fn);
 }

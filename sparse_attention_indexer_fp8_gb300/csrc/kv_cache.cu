@@ -79,25 +79,30 @@ __device__ __forceinline__ void load_run(const void* base, int64_t off, bool vec
   }
 }
 
+__device__ __forceinline__ float4 load4(const float* p, bool vec) {
+  return vec ? __ldg(reinterpret_cast<const float4*>(p))
+             : make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+}
+
 template <bool kBf16>
 __device__ __forceinline__ float load_one(const void* base, int64_t off) {
   if constexpr (kBf16) return bf16_bits(__ldg(static_cast<const uint16_t*>(base) + off));
   return __ldg(static_cast<const float*>(base) + off);
 }
 
-// Position of token `tok`, or -1 (and the device flag) outside the table.
-__device__ __forceinline__ int token_position(const RopeArgs& r, int tok, int lane) {
+// Row of the angle table for token `tok`, or null outside the table.
+__device__ __forceinline__ const float* angles(const RopeArgs& r, int tok) {
   const int pos = __ldg(r.positions + tok);
-  if (pos >= 0 && pos < r.max_pos) return pos;
-  if (lane == 0) atomicOr(&g_kv_cache_error, 1u);
-  return -1;
+  return pos >= 0 && pos < r.max_pos ? r.cos_sin + static_cast<int64_t>(pos) * r.ld_cs : nullptr;
 }
 
 // Indexer k: y = LayerNorm(x) * weight + bias, the first 64 dims rotated, e4m3 with
 // one scale per token, insert. Lane l owns dims 4l..4l+3 (as the plain insert
 // does), so the rotary dims are lanes 0-15: NeoX pairs (i, i + 32) meet by one
 // shuffle with lane l ^ 8, interleaved pairs lie in one lane. The variance is
-// taken of the centred values (a second sum over registers), in binary32.
+// taken of the centred values (a second sum over registers), in binary32. The
+// only chain of loads is position, then angles, and both are asked for before
+// anything is used: a token costs two memory latencies, not four.
 template <bool kBf16>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 k_norm_rope_quant_kernel(const void* __restrict__ k, int64_t ld_k, int n_tok, bool vec,
@@ -108,10 +113,25 @@ k_norm_rope_quant_kernel(const void* __restrict__ k, int64_t ld_k, int n_tok, bo
   const int lane = threadIdx.x & 31;
   if (tok >= n_tok) return;
   float x[4], y[4];
+  const float* cs = angles(rope, tok);
   load_run<kBf16, 4>(k, static_cast<int64_t>(tok) * ld_k + 4 * lane, vec, x);
   const int64_t slot = __ldg(slot_mapping + tok);
+  float wt[4], bs[4], co[4] = {}, si[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    wt[i] = __ldg(weight + 4 * lane + i);
+    bs[i] = bias ? __ldg(bias + 4 * lane + i) : 0.f;
+  }
+  if (lane < 16 && cs) {  // the angle of this lane's dim i: pair 2 l + i / 2, or 4 (l % 8) + i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pair = rope.interleaved ? 2 * lane + i / 2 : 4 * (lane & 7) + i;
+      co[i] = __ldg(cs + pair);
+      si[i] = __ldg(cs + 32 + pair);
+    }
+  }
   if (slot < 0 || slot >= n_slots) return;
-  const int pos = token_position(rope, tok, lane);
+  if (!cs && lane == 0) atomicOr(&g_kv_cache_error, 1u);
 
   const float mean = warp_sum((x[0] + x[1]) + (x[2] + x[3])) * (1.0f / kDim);
   float sq = 0.f;
@@ -123,33 +143,27 @@ k_norm_rope_quant_kernel(const void* __restrict__ k, int64_t ld_k, int n_tok, bo
   const float rstd = 1.0f / sqrtf(warp_sum(sq) * (1.0f / kDim) + eps);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float b = bias ? __ldg(bias + 4 * lane + i) : 0.f;
-    y[i] = fmaf(x[i] * rstd, __ldg(weight + 4 * lane + i), b);
+    y[i] = fmaf(x[i] * rstd, wt[i], bs[i]);
   }
 
   float other[4];  // NeoX: the partner lane's dims
 #pragma unroll
   for (int i = 0; i < 4; ++i) other[i] = __shfl_xor_sync(0xFFFFFFFFu, y[i], 8);
-  if (lane < 16 && pos >= 0) {
-    const float* cs = rope.cos_sin + static_cast<int64_t>(pos) * rope.ld_cs;
+  if (lane < 16) {
     if (rope.interleaved) {
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
-        const float c = __ldg(cs + 2 * lane + i / 2), s = __ldg(cs + 32 + 2 * lane + i / 2);
         const float a = y[i], b = y[i + 1];
-        y[i] = a * c - b * s;
-        y[i + 1] = b * c + a * s;
+        y[i] = a * co[i] - b * si[i];
+        y[i + 1] = b * co[i] + a * si[i];
       }
     } else {
       const float sign = lane < 8 ? -1.f : 1.f;  // first member: a c - b s; second: b c + a s
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float c = __ldg(cs + 4 * (lane & 7) + i), s = __ldg(cs + 32 + 4 * (lane & 7) + i);
-        y[i] = y[i] * c + sign * (other[i] * s);
-      }
+      for (int i = 0; i < 4; ++i) y[i] = y[i] * co[i] + sign * (other[i] * si[i]);
     }
   }
-  if (pos < 0) {
+  if (!cs) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = 0.f;
   }
@@ -205,13 +219,15 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&y)[8], uint32_t code) {
 template <bool kBf16>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 kv_norm_rope_quant_kernel(const void* __restrict__ c, int64_t ld_c, const void* __restrict__ pe, int64_t ld_pe,
-                          int n_tok, bool vec, const float* __restrict__ weight, float eps, const RopeArgs rope,
+                          int n_tok, bool vec, const float* __restrict__ weight, bool vec_w, float eps,
+                          const RopeArgs rope,
                           const int64_t* __restrict__ slot_mapping, uint8_t* __restrict__ cache,
                           int64_t n_slots, int block_size, int64_t block_stride) {
   const int tok = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (tok >= n_tok) return;
   float x[2][8];
+  const float* cs = rope.positions ? angles(rope, tok) : nullptr;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     load_run<kBf16, 8>(c, static_cast<int64_t>(tok) * ld_c + 256 * h + 8 * lane, vec, x[h]);
@@ -221,18 +237,18 @@ kv_norm_rope_quant_kernel(const void* __restrict__ c, int64_t ld_c, const void* 
   float a = load_one<kBf16>(pe, static_cast<int64_t>(tok) * ld_pe + ia);
   float b = load_one<kBf16>(pe, static_cast<int64_t>(tok) * ld_pe + ib);
   const int64_t slot = __ldg(slot_mapping + tok);
+  float co = 1.f, si = 0.f;
+  if (cs) {
+    co = __ldg(cs + lane);
+    si = __ldg(cs + 32 + lane);
+  }
   if (slot < 0 || slot >= n_slots) return;
-  bool zero = false;
-  if (rope.positions) {
-    const int pos = token_position(rope, tok, lane);
-    zero = pos < 0;
-    if (!zero) {
-      const float* cs = rope.cos_sin + static_cast<int64_t>(pos) * rope.ld_cs;
-      const float co = __ldg(cs + lane), si = __ldg(cs + 32 + lane);
-      const float u = a * co - b * si;
-      b = b * co + a * si;
-      a = u;
-    }
+  const bool zero = rope.positions && !cs;
+  if (zero && lane == 0) atomicOr(&g_kv_cache_error, 1u);
+  if (cs) {
+    const float u = a * co - b * si;
+    b = b * co + a * si;
+    a = u;
   }
   if (weight) {
     float sq = 0.f;
@@ -245,7 +261,13 @@ kv_norm_rope_quant_kernel(const void* __restrict__ c, int64_t ld_c, const void* 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[h][i] = x[h][i] * rstd * __ldg(weight + 256 * h + 8 * lane + i);
+      for (int i = 0; i < 8; i += 4) {
+        const float4 wt = load4(weight + 256 * h + 8 * lane + i, vec_w);
+        x[h][i] *= rstd * wt.x;
+        x[h][i + 1] *= rstd * wt.y;
+        x[h][i + 2] *= rstd * wt.z;
+        x[h][i + 3] *= rstd * wt.w;
+      }
     }
   }
   if (zero) {
@@ -491,7 +513,8 @@ extern "C" idx_status_t idx_kv_norm_rope_quant_and_cache(
   const RopeArgs rope{positions, cos_sin, ld_cs, max_pos, rope_style == IDX_ROPE_INTERLEAVED};
   const dim3 grid((static_cast<unsigned>(n_tok) + kWarpsPerBlock - 1) / kWarpsPerBlock);
   auto* kernel = bf16 ? kv_norm_rope_quant_kernel<true> : kv_norm_rope_quant_kernel<false>;
-  kernel<<<grid, kWarpsPerBlock * 32, 0, stream>>>(c, ld_c, pe, ld_pe, n_tok, vec, weight, eps, rope, slot_mapping,
+  kernel<<<grid, kWarpsPerBlock * 32, 0, stream>>>(c, ld_c, pe, ld_pe, n_tok, vec, weight, aligned(weight, 16),
+                                                   eps, rope, slot_mapping,
                                                    cache, n_slots, block_size, block_stride_bytes);
   return check_launch(fn);
 }
