@@ -87,7 +87,10 @@ constexpr int kThreads = (kRopeWarp + kStages) * 32;
 constexpr int kValidRing = 4;
 constexpr int kAhead = 4;                        // tiles between the L2 prefetch and the loads
 constexpr int kOCols = 256;                      // tensor-memory columns of O; S0 and S1 (32 each) follow
+constexpr int kQCols = 320;                      // and the first kQTmemPieces pieces of Q
+constexpr int kQTmemPieces = 6;
 constexpr int kTmemCols = 512;
+static_assert(kQCols + kQTmemPieces * 32 <= kTmemCols, "tensor memory of one block");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescaleStep = 8.0f;             // log2: P may reach 2^8 before O is rescaled
 
@@ -137,6 +140,18 @@ __device__ __forceinline__ void mma_ws_bf16(uint32_t d, uint64_t a, uint64_t b, 
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 e, %5, 0;\n\t"
       "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(acc), "r"(issue)
+      : "memory");
+}
+
+// The same with A in tensor memory: row r in lanes r and 64 + r, two elements of K a column.
+__device__ __forceinline__ void mma_ws_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                               uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
       "r"(acc), "r"(issue)
       : "memory");
 }
@@ -208,6 +223,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 2, %0;" ::"n"(kMmaWarp * 32) : "memory"); }
+
+// The softmax warps and the matrix warp: tensor memory is there (and every row of Q copied).
+__device__ __forceinline__ void tmem_bar() { asm volatile("bar.sync 3, 160;" ::: "memory"); }
 
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -479,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     __syncwarp();
     tmem_alloc(&sh.tmem, kTmemCols);
     tmem_relinquish();
+    tc_fence_before();
+    tmem_bar();
     setup();
     // ---------------------------------------------------------------- matrix instructions
     // Whichever of the next S and the next O product has its operands goes first, O before S.
@@ -489,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     const uint64_t k_desc = sw128_kmajor_desc(smem_u32(k_s));
     const uint64_t v_desc = sw128_nmajor_desc(smem_u32(k_s));
     wait_bar(sh, &sh.q_full, 0);
+    tc_fence_after();
     const int total = __shfl_sync(0xFFFFFFFFu, tiles, 0);
     int s_next = 0, o_next = 0;
     uint64_t t0 = global_timer_ns();
@@ -522,8 +543,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         for (int c = 0; c < kPieces; ++c) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            mma_ws_bf16(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks,
-                        k + ((c * kPieceBytes) >> 4) + 2 * ks, idesc_bf16(64, 64, false), c > 0 || ks > 0, lead);
+            const uint64_t b = k + ((c * kPieceBytes) >> 4) + 2 * ks;
+            if (c < kQTmemPieces) {
+              mma_ws_bf16_ta(tmem + kOCols + st * 32, tmem + kQCols + 32 * c + 8 * ks, b, idesc_bf16(64, 64, false),
+                             c > 0 || ks > 0, lead);
+            } else {
+              mma_ws_bf16(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks, b,
+                          idesc_bf16(64, 64, false), 1, lead);
+            }
           }
         }
         commit_if(&sh.s_full[st], lead);
@@ -550,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------------- softmax
-    // Q, sixteen rows a warp, rows of heads past the last one zero. All copies go out at once; what a thread
-    // copied it then puts into the loaders' order of the latent dims: 0, 2, 1, 3 of every four.
+    // Q, sixteen rows a warp, rows of heads past the last one zero, all copies out at once. The latent dims
+    // are then put into the loaders' order, 0, 2, 1, 3 of every four, and as many of them as there are columns
+    // into tensor memory: S reads less of the shared memory that the loaders and O want too.
     const uint32_t q_row = smem_u32(q_s) + 16 * warp * 128;
 #pragma unroll 4
     for (int i = 0; i < 16; ++i) {
@@ -564,22 +592,39 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       if (lane < 8) copy16_if(at + 8 * kPieceBytes, src + 1024 + 16 * lane, have);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    tmem_bar();
+    tc_fence_after();
+    tmem = sh.tmem;
+    const int r = tid & 63, half = tid >> 6;          // head of the group, and half of the tile's tokens
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    auto reorder = [](const uint4& v) {
+      return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                        __byte_perm(v.z, v.w, 0x7632));
+    };
+    const uint32_t own_row = smem_u32(q_s) + r * 128;
 #pragma unroll 1
-    for (int i = 0; i < 16; i += 4) {
-      uint4 v[8];
+    for (int u = 0; u < 8 * kQTmemPieces; u += 4) {
+      uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = ld_shared16(q_row + (i + j / 2) * 128 + (((lane & 7) ^ ((i + j / 2) & 7)) << 4) +
-                           (4 * (j & 1) + (lane >> 3)) * kPieceBytes);
+      for (int x = 0; x < 4; ++x) {
+        const uint4 v = reorder(ld_shared16(own_row + (u >> 3) * kPieceBytes + ((((u + x) & 7) ^ (r & 7)) << 4)));
+        w[4 * x] = v.x;
+        w[4 * x + 1] = v.y;
+        w[4 * x + 2] = v.z;
+        w[4 * x + 3] = v.w;
       }
+      tmem_st16(lanes + kQCols + 4 * u, w);
+    }
+    // of the latent pieces that stay in shared memory, each thread has half a row
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        st_shared16(q_row + (i + j / 2) * 128 + (((lane & 7) ^ ((i + j / 2) & 7)) << 4) +
-                        (4 * (j & 1) + (lane >> 3)) * kPieceBytes,
-                    make_uint4(__byte_perm(v[j].x, v[j].y, 0x5410), __byte_perm(v[j].x, v[j].y, 0x7632),
-                               __byte_perm(v[j].z, v[j].w, 0x5410), __byte_perm(v[j].z, v[j].w, 0x7632)));
+    for (int c = kQTmemPieces; c < kKvLatent / 64; ++c) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t at = own_row + c * kPieceBytes + (((4 * half + u) ^ (r & 7)) << 4);
+        st_shared16(at, reorder(ld_shared16(at)));
       }
     }
+    tmem_wait_st();
     setup();
     auto arrive = [&](uint64_t* bar) {
       fence_proxy_async_smem();
@@ -589,8 +634,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     };
     arrive(&sh.q_full);
 
-    const int r = tid & 63, half = tid >> 6;          // head of the group, and half of the tile's tokens
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float m = -INFINITY, l = 0.f;                     // maximum (log2 units) that P and O refer to; this half's sum
     for (int i = 0; i < tiles; ++i) {
       const int st = i & 1;
