@@ -7,6 +7,7 @@
 // and 64 position dims, value: the latent).
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -782,91 +783,114 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 }
 
 // Joins the parts of each (row, head): weights 2^(m_i - max m), a part without a valid token skipped (its
-// accumulators were never written). One block per head: four groups of 128 threads, each a float4 of the
-// row and every fourth part, so that a few rounds of loads cover the parts of one row.
-constexpr int kJoinGroups = 4;
-constexpr int kMaxParts = 256;
+// accumulators were never written). A head is the work of kWarps warps, each of which takes every kWarps-th
+// part, two at a time, 16 dims a lane: all heads of a batch run at once, and the eight loads of two parts
+// are in flight together. The maxima and sums are few enough for every warp to reduce them itself.
+constexpr int kJoinWarps = 8;   // of a block
+constexpr int kMaxParts = 128;
 
-__global__ void __launch_bounds__(kJoinGroups * kKvLatent / 4) attention_join_kernel(const AttnParams p) {
-  __shared__ float weight[kMaxParts];
-  __shared__ float4 sums[kJoinGroups - 1][kKvLatent / 4];
-  __shared__ float warp_max[kJoinGroups * 4], warp_sum[kJoinGroups * 4];
-  const int row = blockIdx.x / p.H, h = blockIdx.x % p.H;
-  const int64_t base = (static_cast<int64_t>(row) * p.head_blocks + h / kHeadsPerBlock) * p.parts;
-  const int r = h % kHeadsPerBlock, tid = threadIdx.x;
+template <int kWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttnParams p) {
+  constexpr int kHeads = kJoinWarps / kWarps;  // of a block
+  __shared__ float4 sums[kHeads][kWarps > 1 ? kWarps - 1 : 1][kKvLatent / 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp / kWarps, g = warp % kWarps;
+  const uint32_t heads = static_cast<uint32_t>(p.H), head = blockIdx.x * kHeads + sub;
+  const bool have = head < static_cast<uint32_t>(p.T) * heads;
+  const uint32_t row = have ? head / heads : 0u, h = have ? head - row * heads : 0u;
+  const int64_t base = (static_cast<int64_t>(row) * p.head_blocks + h / kHeadsPerBlock) * p.parts * kHeadsPerBlock +
+                       h % kHeadsPerBlock;
+  const float2* ml = p.ws_ml + base;  // of part i: ml[64 i], o[64 * 128 i]
+  const float4* o = reinterpret_cast<const float4*>(p.ws_o + base * kKvLatent) + lane;
+  constexpr int kStep = kHeadsPerBlock * kKvLatent / 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // every part is complete and visible
-  const float2 ml = tid < p.parts ? __ldcg(&p.ws_ml[(base + tid) * kHeadsPerBlock + r]) : make_float2(-INFINITY, 0.f);
-  float m = ml.x;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if ((tid & 31) == 0) warp_max[tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kJoinGroups * 4; ++i) m = fmaxf(m, warp_max[i]);
-  const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - m);
-  if (tid < p.parts) weight[tid] = w;
-  float l = w * ml.y;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-  if ((tid & 31) == 0) warp_sum[tid >> 5] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int i = 0; i < kJoinGroups * 4; ++i) l += warp_sum[i];
 
-  const int group = tid / (kKvLatent / 4), at = tid % (kKvLatent / 4);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = group; i < p.parts; i += kJoinGroups) {
-    const float f = weight[i];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (f != 0.f) {
-      o = __ldcg(reinterpret_cast<const float4*>(p.ws_o + ((base + i) * kHeadsPerBlock + r) * kKvLatent) + at);
-    }
-    acc.x = fmaf(f, o.x, acc.x);
-    acc.y = fmaf(f, o.y, acc.y);
-    acc.z = fmaf(f, o.z, acc.z);
-    acc.w = fmaf(f, o.w, acc.w);
-  }
-  if (group > 0) sums[group - 1][at] = acc;
-  __syncthreads();
-  if (group > 0) return;
+  float2 mine[kMaxParts / 32];
+  float m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int g = 0; g < kJoinGroups - 1; ++g) {
-    const float4 o = sums[g][at];
-    acc.x += o.x;
-    acc.y += o.y;
-    acc.z += o.z;
-    acc.w += o.w;
+  for (int c = 0; c < kMaxParts / 32; ++c) {
+    mine[c] = 32 * c + lane < p.parts ? __ldcg(ml + (32 * c + lane) * kHeadsPerBlock) : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, mine[c].x);
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+#pragma unroll
+  for (int c = 0; c < kMaxParts / 32; ++c) {
+    if (mine[c].y != 0.f) l = fmaf(exp2f(mine[c].x - m), mine[c].y, l);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+
+  float4 acc[4] = {};
+  for (int i = g; i < p.parts; i += 2 * kWarps) {
+    float2 x[2];
+    float4 v[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int part = i + j * kWarps;
+      x[j] = make_float2(-INFINITY, 0.f);
+      if (part >= p.parts) continue;
+      x[j] = __ldcg(ml + part * kHeadsPerBlock);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[j][c] = __ldcg(o + static_cast<int64_t>(part) * kStep + 32 * c);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (x[j].y == 0.f) continue;
+      const float w = exp2f(x[j].x - m);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[c].x = fmaf(w, v[j][c].x, acc[c].x);
+        acc[c].y = fmaf(w, v[j][c].y, acc[c].y);
+        acc[c].z = fmaf(w, v[j][c].z, acc[c].z);
+        acc[c].w = fmaf(w, v[j][c].w, acc[c].w);
+      }
+    }
+  }
+  if constexpr (kWarps > 1) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (g > 0) sums[sub][g - 1][lane + 32 * c] = acc[c];
+    }
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 0; i < kWarps - 1; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = sums[sub][i][lane + 32 * c];
+        acc[c].x += v.x;
+        acc[c].y += v.y;
+        acc[c].z += v.z;
+        acc[c].w += v.w;
+      }
+    }
+  }
+  if (!have) return;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.out + row * p.ld_out + h * p.ld_oh + 4 * at) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (p.lse && tid == 0) {
+  __nv_bfloat16* dst = p.out + row * p.ld_out + h * p.ld_oh + 4 * lane;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+    *reinterpret_cast<uint2*>(dst + 128 * c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  if (p.lse && lane == 0) {
     p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
-// Parts that a list of k entries is split into: the number that minimises the waves of
-// blocks times the tiles of one (a block's start and end cost about three tiles), the join
-// counted as three more tiles. One part when the rows alone fill the GPU.
+// Parts that a list of k entries is split into: as many as one wave of blocks has room for, if that
+// is cheaper than whole rows. In units of a tile (1.45 us on a GB300) a block's start and end cost six and
+// the join four. A second wave never pays: 100 rows x 64 heads x 2048 tokens measured 80 us in three
+// parts and 59 us whole; 64 rows 58 us whole, one row 55 us whole and 16 us in 32 parts.
 int attention_parts(int64_t blocks, int k, int sms) {
   const int tiles = (k + kTile - 1) / kTile;
-  if (sms <= 0 || tiles <= 1 || blocks >= sms) return 1;
-  int best = 1;
-  int64_t best_cost = (blocks + sms - 1) / sms * (tiles + 3);
-  for (int parts = 2; parts <= tiles && parts <= kMaxParts && blocks * parts <= 2 * sms; ++parts) {
-    const int per = (tiles + parts - 1) / parts;
-    if ((tiles + per - 1) / per != parts) continue;  // no part without tiles
-    const int64_t cost = (blocks * parts + sms - 1) / sms * (per + 3) + 3;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = parts;
-    }
-  }
-  return best;
+  if (sms <= 0 || tiles <= 1 || 2 * blocks > sms) return 1;
+  const int room = static_cast<int>(std::min<int64_t>(sms / blocks, kMaxParts));
+  const int per = (tiles + room - 1) / room;         // tiles of a part
+  const int parts = (tiles + per - 1) / per;         // none without tiles
+  return per + 4 < tiles ? parts : 1;
 }
 
 int64_t part_bytes() { return kHeadsPerBlock * (static_cast<int64_t>(kKvLatent) * 4 + 8); }
@@ -970,17 +994,23 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
   kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
   st = check_launch(fn);
   if (st != IDX_OK || p.parts == 1) return st;
-  // launched while the parts run: its blocks wait at their first instruction for the parts' end
+  // launched while the parts run: its blocks wait at their first reads for the parts' end; a warp takes four parts
+  const int warps = p.parts <= 4 ? 1 : p.parts <= 8 ? 2 : p.parts <= 16 ? 4 : 8;
+  auto* join = warps == 1   ? attention_join_kernel<1>
+               : warps == 2 ? attention_join_kernel<2>
+               : warps == 4 ? attention_join_kernel<4>
+                            : attention_join_kernel<8>;
+  const int heads = kJoinWarps / warps;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(T) * static_cast<unsigned>(H));
-  cfg.blockDim = dim3(kJoinGroups * kKvLatent / 4);
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(T) * H + heads - 1) / heads));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t ej = cudaLaunchKernelEx(&cfg, attention_join_kernel, p);
+  const cudaError_t ej = cudaLaunchKernelEx(&cfg, join, p);
   if (ej != cudaSuccess) {
     cudaGetLastError();
     return fail(IDX_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(ej));
