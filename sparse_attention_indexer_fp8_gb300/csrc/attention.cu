@@ -55,20 +55,29 @@ struct AttnParams {
 // for S, and runs at half the rate (N = 256: 128 clocks against 80 on a GB300).
 //
 // Roles: warps 4-19 gather and dequantise the tokens' latents, warps 21-22 copy their position
-// dims, warp 20 issues the matrix instructions, warps 0-3 do the softmax, the rescaling and the
-// epilogue.
+// dims and prefetch, warp 20 issues the matrix instructions, warps 0-3 load Q and do the
+// softmax; all but 20-22 store the result.
 //
 // Keys and values are one copy in shared memory: a token is a row of nine 128-byte swizzled
 // pieces (64 dims each). Read along the dims it is the K-major B operand of S, read along the
 // tokens the N-major B operand of O. Two tiles of 72 KB are in flight beside Q (72 KB) and P (8 KB).
 //
 // Two groups of eight loader warps own a stage each. A group converts and stores its tile, then
-// issues every load of its next one at once, into registers: HBM latency runs under the other
-// group's conversion and the matrix work, with no staging buffer. (One group that refilled each
-// register right after its conversion measured 7000 clocks a tile: loads of two tiles shared
-// scoreboards, so every conversion waited for the newest load.) What a warp keeps in flight is
-// limited whatever it asks for: random 512-byte rows read by 8 warps an SM came at 3.2 TB/s, by
-// 16 at 5.4 TB/s, by 32 at 6.4 TB/s, with 8 or 16 rows asked for by each; hence sixteen.
+// issues every load of its next one at once, into registers: memory latency runs under the other
+// group's conversion and the matrix work, with no staging buffer, for which there is no room. (One
+// group that refilled each register right after its conversion measured 7000 clocks a tile: loads
+// of two tiles shared scoreboards, so every conversion waited for the newest load.) What a warp
+// keeps in flight is limited whatever it asks for: random 512-byte rows read by 8 warps an SM came
+// at 3.2 TB/s, by 16 at 5.4 TB/s, by 32 at 6.4 TB/s, with 8 or 16 rows asked for by each; hence
+// sixteen, and the prefetch into L2.
+//
+// What bounds it: shared memory. Per tile S reads 1152 - 384 clocks' worth of 128 bytes (Q's larger
+// part comes out of tensor memory), O 640, the loaders write 576 and their loads pass 640 through the
+// same array: some 2600 of the 2700 clocks that a tile takes. Leaving out any one of them in a copy
+// saved 5 to 11 %. 128 rows x 16 heads x 2048 tokens: 57 us (3.0 TB/s of records; the records alone
+// take 26 us at the measured HBM rate); 1024 rows x 128 heads: 763 us (763 TFLOP/s). Pairs of blocks
+// that shared a tile's tokens (cta_group::2, M = 128) read less but measured 867 us there: values
+// that cross between two SMs came at 10 bytes a clock, and gathered twice they cost what was saved.
 // ---------------------------------------------------------------------------
 constexpr int kHeadsPerBlock = 64;
 constexpr int kTile = 64;
@@ -417,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
   } else if (warp >= kRopeWarp) {
     // ---------------------------------------------------------------- position dims, and L2 prefetch
-    // Position dims are bf16 in the cache as in the tile: copied asynchronously, once the stage is free.
+    // Position dims are bf16 in the cache as in the tile: copied asynchronously, as soon as S of the tile
+    // before is complete (with the rest of the stage, after O, they held every tile up: 880 against 785 us
+    // for 1024 rows x 128 heads).
     // Lane l locates tokens l and 32 + l. The same warp brings the records of the tile kAhead further
     // on into L2: a random token comes out of HBM in some 2900 clocks, out of L2 in 1200, and the
     // loaders' registers hold one tile.
@@ -881,9 +892,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
 }
 
 // Parts that a list of k entries is split into: as many as one wave of blocks has room for, if that
-// is cheaper than whole rows. In units of a tile (1.45 us on a GB300) a block's start and end cost six and
-// the join four. A second wave never pays: 100 rows x 64 heads x 2048 tokens measured 80 us in three
-// parts and 59 us whole; 64 rows 58 us whole, one row 55 us whole and 16 us in 32 parts.
+// is cheaper than whole rows. In units of a tile (1.45 us on a GB300) a block's start and end cost six, whole or
+// part, and the join four. Lists of 2048, 64 heads, in parts against whole: one row 14 us (32 parts) and
+// 57 us, 16 rows 22 (8) and 57, 64 rows 41 (2) and 58. A second wave of parts does not pay: 100 rows
+// measured 80 us in three parts and 59 whole.
 int attention_parts(int64_t blocks, int k, int sms) {
   const int tiles = (k + kTile - 1) / kTile;
   if (sms <= 0 || tiles <= 1 || 2 * blocks > sms) return 1;
