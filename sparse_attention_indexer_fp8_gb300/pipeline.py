@@ -192,8 +192,10 @@ class AttentionDecodeStep:
 
     def __init__(self, batch: int, max_ctx: int, heads: int, topk: int = W.TOPK, block_size: int = W.BLOCK_SIZE,
                  device="cuda", softmax_scale: float = W.ATTN_DIM ** -0.5, eps: float = 1e-6,
-                 interleaved: bool = False):
-        self.block_size, self.softmax_scale, self.eps, self.interleaved = block_size, softmax_scale, eps, interleaved
+                 interleaved: bool = False, index_interleaved: bool = False):
+        self.block_size, self.softmax_scale, self.eps = block_size, softmax_scale, eps
+        # pairing of the rotary dims of the attention latent and of the indexer's q and k
+        self.interleaved, self.index_interleaved = interleaved, index_interleaved
         self.indexer = DecodeStep(batch, max_ctx, topk=topk, block_size=block_size, device=device)
         self.q8 = torch.empty((batch, 64, 128), dtype=torch.uint8, device=device)
         self.w = torch.empty((batch, 64), dtype=torch.float32, device=device)
@@ -211,7 +213,7 @@ class AttentionDecodeStep:
     def insert(self, k, kv, k_weight, k_bias, kv_weight, positions, cos_sin, slots, k_cache, kv_cache, stream=None):
         """Any number of tokens: indexer k [n, 128] and attention projection [n, 576] into both caches."""
         idx_k_norm_rope_quant_and_cache(k, k_weight, k_bias, self.eps, positions, cos_sin, slots, k_cache,
-                                        self.block_size, interleaved=self.interleaved, stream=stream)
+                                        self.block_size, interleaved=self.index_interleaved, stream=stream)
         idx_kv_norm_rope_quant_and_cache(kv[:, :512], kv[:, 512:], kv_weight, self.eps, positions, cos_sin, slots,
                                          kv_cache, self.block_size, interleaved=self.interleaved, stream=stream)
 
@@ -221,7 +223,7 @@ class AttentionDecodeStep:
         self.insert(new_k, new_kv, k_weight, k_bias, kv_weight, positions, cos_sin, new_slots, k_cache, kv_cache,
                     stream=stream)
         idx_q_rope_quant(q_index, positions, cos_sin, w_index, self.q8, self.w, 128 ** -0.5, 64 ** -0.5,
-                         interleaved=self.interleaved, stream=stream)
+                         interleaved=self.index_interleaved, stream=stream)
         slots = self.indexer.run(self.q8, self.w, k_cache, block_table, ctx_lens, stream=stream)
         idx_sparse_attention(q, kv_cache, self.block_size, slots, self.out, self.softmax_scale, lse=self.lse,
                              ws=self.ws, stream=stream)

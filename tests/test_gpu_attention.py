@@ -444,6 +444,77 @@ def test_small_workspace_and_wrong_tensors_are_refused():
     idx.idx_device_error()
 
 
+def test_offsets_past_32_bits():
+    # blocks that start past 2^32 bytes and past 2^31 token bytes, written, read back and attended to
+    bs, stride = 128, 128 * 644
+    blocks = (1 << 32) // stride + 300
+    cache = torch.zeros((blocks, stride), dtype=torch.uint8, device=DEV)
+    rng = np.random.default_rng(41)
+    high = np.arange(blocks - 3, blocks)
+    slots = (high[:, None] * bs + np.arange(bs)).reshape(-1).astype(np.int64)
+    n = len(slots)
+    x = dev(rng.normal(size=(n, 576)).astype(np.float32)).bfloat16()
+    idx.idx_kv_norm_rope_quant_and_cache(x[:, :512], x[:, 512:], None, 1e-6, None, None, dev(slots), cache, bs)
+    out = torch.empty((n, 576), dtype=torch.float32, device=DEV)
+    idx.idx_gather_kv(cache, bs, dev(high.astype(np.int32)[None]), dev(np.array([0, n], np.int32)), out)
+    small = cache[blocks - 3:].cpu().numpy()
+    assert (out.double().cpu().numpy() == A.gather_kv(small, bs, [[0, 1, 2]], [0, n])).all() and bool(out.any())
+    q = bf16_encode(rng.normal(size=(1, 16, 576)).astype(np.float32))
+    lst = rng.permutation(n)[:200]
+    o, l = torch.empty((1, 16, 512), dtype=torch.bfloat16, device=DEV), torch.empty((1, 16), device=DEV)
+    idx.idx_sparse_attention(dev(q.view(np.int16)).view(torch.bfloat16), cache, bs, dev(slots[lst].astype(np.int32)[None]),
+                             o, 576 ** -0.5, lse=l)
+    idx.idx_device_error()
+    check_attention(small, lst.astype(np.int32)[None], q, bs, 576 ** -0.5, o, l)
+
+
+@pytest.mark.parametrize("T,H,K,bs", [(1, 17, 4096, 64), (9, 64, 5000, 32), (40, 48, 640, 16)])
+def test_attention_long_and_split_lists(T, H, K, bs):
+    # every number of parts' join: a part without a token, rows of fewer entries than parts, ragged ends
+    cache, slots, q = attention_case(T + K, T, H, K, bs, 2.0, holes=0.3, blocks=40)
+    n_sel = np.random.default_rng(T).integers(0, K + 1, T).astype(np.int32)
+    slots[0, : K // 2] = -1
+    n_sel[0] = K
+    if T > 2:
+        n_sel[1], n_sel[2] = 0, 1
+    out = torch.full((T, H, 512), 9.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, H), 9.0, device=DEV)
+    w = workspace(T, H, K)
+    assert w is not None or T == 40
+    idx.idx_sparse_attention(dev(q.view(np.int16)).view(torch.bfloat16), dev(cache), bs, dev(slots), out, 576 ** -0.5,
+                             lse=lse, n_sel=dev(n_sel), ws=w)
+    idx.idx_device_error()
+    pick = [t for t in range(T) if t < 4 or t % 9 == 0]
+    check_attention(cache, slots[pick], q[pick], bs, 576 ** -0.5, out[pick], lse[pick], n_sel[pick])
+    # the same row whole and in parts: the same tokens, other roundings only
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    idx.idx_sparse_attention(dev(q.view(np.int16)).view(torch.bfloat16), dev(cache), bs, dev(slots), o2, 576 ** -0.5,
+                             lse=l2, n_sel=dev(n_sel))
+    check_attention(cache, slots[pick], q[pick], bs, 576 ** -0.5, o2[pick], l2[pick], n_sel[pick])
+
+
+def test_calls_on_a_side_stream_follow_their_inputs():
+    # inputs made on a side stream, the call given that stream: no other synchronisation
+    cache, slots, q = attention_case(43, 3, 64, 500, 64, 2.0)
+    ref = torch.empty((3, 64, 512), dtype=torch.bfloat16, device=DEV)
+    qd, cd, sd = dev(q.view(np.int16)).view(torch.bfloat16), dev(cache), dev(slots)
+    idx.idx_sparse_attention(qd, cd, 64, sd, ref, 0.05)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(5_000_000)
+        c2 = torch.zeros_like(cd)
+        c2.copy_(cd)
+        out = torch.empty_like(ref)
+        idx.idx_sparse_attention(qd, c2, 64, sd, out, 0.05)                 # torch's current stream
+        packed = torch.empty((100, 576), dtype=torch.bfloat16, device=DEV)
+        idx.idx_gather_kv(c2, 64, torch.zeros((1, 2), dtype=torch.int32, device=DEV),
+                          torch.tensor([0, 64], dtype=torch.int32, device=DEV), packed)
+    st.synchronize()
+    assert torch.equal(out, ref)
+    assert (packed[:64].double().cpu().numpy() == A.gather_kv(cache, 64, [[0]], [0, 64])).all()
+
+
 # ------------------------------------------------------------------ together
 
 def test_one_layer_step_together():
@@ -457,7 +528,7 @@ def test_one_layer_step_together():
     pages = -(-L // bs)
     bt = rng.permutation(B * pages).reshape(B, pages).astype(np.int32)
     cs = dev(cos_sin(L))
-    step = AttentionDecodeStep(B, L, heads=H, topk=K, device=DEV)
+    step = AttentionDecodeStep(B, L, heads=H, topk=K, device=DEV, interleaved=True)
     kc, vc = step.make_caches(B * pages)
     w, bias, rw = (dev(rng.normal(size=n).astype(np.float32)) for n in (128, 128, 512))
     # contexts inserted by the same calls, the last token of each by the step itself
