@@ -71,13 +71,14 @@ struct AttnParams {
 // at 3.2 TB/s, by 16 at 5.4 TB/s, by 32 at 6.4 TB/s, with 8 or 16 rows asked for by each; hence
 // sixteen, and the prefetch into L2.
 //
-// What bounds it: shared memory. Per tile S reads 1152 - 384 clocks' worth of 128 bytes (Q's larger
-// part comes out of tensor memory), O 640, the loaders write 576 and their loads pass 640 through the
-// same array: some 2600 of the 2700 clocks that a tile takes. Leaving out any one of them in a copy
-// saved 5 to 11 %. 128 rows x 16 heads x 2048 tokens: 57 us (3.0 TB/s of records; the records alone
-// take 26 us at the measured HBM rate); 1024 rows x 128 heads: 763 us (763 TFLOP/s). Pairs of blocks
-// that shared a tile's tokens (cta_group::2, M = 128) read less but measured 867 us there: values
-// that cross between two SMs came at 10 bytes a clock, and gathered twice they cost what was saved.
+// What bounds it: the data pipe of shared memory and L1, busy 90 % of the time on the SMs that work (ncu).
+// Per tile, in clocks of it: S 768 and O 640 (S would take 1152 without Q's larger part in tensor
+// memory), the stores, shuffles and P 1170, the loads 660, of some 3600 in all with a block's start and
+// end. Leaving out any one kind of work in a copy saved 5 to 11 %. 128 rows x 16 heads x 2048 tokens:
+// 57 us (3.0 TB/s of records; the records alone take 26 us at the measured HBM rate); 1024 rows x 128
+// heads: 763 us (763 TFLOP/s). Pairs of blocks that shared a tile's tokens (cta_group::2, M = 128) read
+// less but measured 867 us there: values that cross between two SMs came at 10 bytes a clock, and
+// gathered twice they cost what was saved.
 // ---------------------------------------------------------------------------
 constexpr int kHeadsPerBlock = 64;
 constexpr int kTile = 64;
