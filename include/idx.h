@@ -724,7 +724,9 @@ idx_status_t idx_gather_kv(const uint8_t* cache, int32_t num_blocks, int32_t blo
  *               (block_span >= block_size, as idx_req_to_global_slots).
  *   slots       int32 [T, ld_slots], k entries used. An entry >= 0 outside the cache
  *               is skipped and raises the device flag.
- *   n_sel       int32 [T] or NULL (all k entries).
+ *   n_sel       int32 [T] or NULL (all k entries). An entry of -1 costs what a token
+ *               does and one past n_sel nothing: where contexts may be shorter than
+ *               k, pass their lengths (the selection writes -1 at the end of a row).
  *   out         bf16 [T, H, 512], ld_out between rows, ld_oh between heads (each
  *               >= 512 and a multiple of 8), 16-byte aligned.
  *   lse         float [T, ld_lse] (ld_lse >= H) or NULL.
@@ -734,7 +736,8 @@ idx_status_t idx_gather_kv(const uint8_t* cache, int32_t num_blocks, int32_t blo
  *               block's work. Its contents need no preparation and mean nothing
  *               after the call; calls that may overlap need one each.
  * Errors: IDX_ERR_INVALID_ARG for NULL pointers, negative sizes, short strides, a
- * softmax_scale that is not finite or a workspace that is too small;
+ * softmax_scale that is not finite (in units of log2 too) or a workspace that is
+ * too small;
  * IDX_ERR_UNSUPPORTED for more than IDX_ATTENTION_MAX_HEADS heads, misaligned rows,
  * block_span < block_size or a cache outside the layout's alignment.
  */

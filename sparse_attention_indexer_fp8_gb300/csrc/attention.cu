@@ -945,7 +945,7 @@ extern "C" idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_
   if (ld_slots < k || ld_q < kKvDim || ld_qh < kKvDim || ld_out < kKvLatent || ld_oh < kKvLatent || (lse && ld_lse < H)) {
     return fail(IDX_ERR_INVALID_ARG, "%s: a stride is smaller than its row", fn);
   }
-  if (!std::isfinite(softmax_scale)) return fail(IDX_ERR_INVALID_ARG, "%s: softmax_scale is not finite", fn);
+  if (!std::isfinite(softmax_scale * 1.4426950408889634f)) return fail(IDX_ERR_INVALID_ARG, "%s: softmax_scale is not finite", fn);
   if (T == 0 || H == 0) return IDX_OK;
   if (!q || !cache || !out || (!slots && k > 0)) return fail(IDX_ERR_INVALID_ARG, "%s: NULL pointer", fn);
   idx_status_t st = check_kv_cache(fn, cache, num_blocks, block_size, block_stride_bytes);

@@ -225,8 +225,9 @@ class AttentionDecodeStep:
         idx_q_rope_quant(q_index, positions, cos_sin, w_index, self.q8, self.w, 128 ** -0.5, 64 ** -0.5,
                          interleaved=self.index_interleaved, stream=stream)
         slots = self.indexer.run(self.q8, self.w, k_cache, block_table, ctx_lens, stream=stream)
+        # the lists of contexts shorter than topk end with -1: nothing past a context's length is looked at
         idx_sparse_attention(q, kv_cache, self.block_size, slots, self.out, self.softmax_scale, lse=self.lse,
-                             ws=self.ws, stream=stream)
+                             n_sel=ctx_lens, ws=self.ws, stream=stream)
         return self.out
 
 

@@ -78,7 +78,7 @@ def test_gather_refusals(lib, change, status):
     ({"T": -1}, INVALID), ({"H": -1}, INVALID), ({"k": -1}, INVALID), ({"H": 1025}, UNSUPPORTED),
     ({"ld_slots": 31}, INVALID), ({"ld_q": 575}, INVALID), ({"ld_qh": 575}, INVALID), ({"ld_out": 511}, INVALID),
     ({"ld_oh": 511}, INVALID), ({"lse": P, "ld_lse": 7}, INVALID), ({"scale": math.inf}, INVALID),
-    ({"scale": math.nan}, INVALID), ({"q": None}, INVALID), ({"cache": None}, INVALID), ({"out": None}, INVALID),
+    ({"scale": math.nan}, INVALID), ({"scale": 3e38}, INVALID), ({"q": None}, INVALID), ({"cache": None}, INVALID), ({"out": None}, INVALID),
     ({"slots": None}, INVALID), ({"bs": 24}, UNSUPPORTED), ({"stride": 41200}, INVALID), ({"stride": 41480}, UNSUPPORTED),
     ({"cache": MIS}, UNSUPPORTED), ({"span": 63}, UNSUPPORTED), ({"q": MIS}, UNSUPPORTED), ({"out": MIS}, UNSUPPORTED),
     ({"ld_q": 576 * 8 + 4}, UNSUPPORTED), ({"ld_qh": 580}, UNSUPPORTED), ({"ld_out": 512 * 8 + 4}, UNSUPPORTED),
