@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, src[0] != nullptr);
       const uint32_t v1 = __ballot_sync(0xFFFFFFFFu, src[1] != nullptr);
       if (lane == 0) {
-        // S of this tile is issued after O of tile i - 2, so entry i - 4 has been read
+        // S of tile i - 2, waited for above, was issued after O of tile i - 4, hence after entry i - 4 was read
         sh.valid[i % kValidRing][0] = v0;
         sh.valid[i % kValidRing][1] = v1;
         mbar_arrive(&sh.flags[i % kValidRing]);
