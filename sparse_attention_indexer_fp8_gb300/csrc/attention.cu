@@ -744,9 +744,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     constexpr int kRowBytes = kKvLatent * (kSplit ? 4 : 2);
     constexpr int kPitch = kRowBytes + 16;  // eight rows' stores fall into different banks
     static_assert(kHeadsPerBlock * kPitch <= kStages * kStageBytes, "the rows fit the stages");
-    wait_bar(sh, &sh.o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
-    tc_fence_after();
+    // Only the softmax warps may wait for the last O by its parity: they have followed every phase of both o_done
+    // barriers. A loader warp has followed its own stage's only, and from three tiles on could take an earlier phase
+    // of the other for the last one. It is ordered behind O by the block barrier and the fences around it.
+    if (warp < 4) {
+      wait_bar(sh, &sh.o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
+      tc_fence_after();
+      tc_fence_before();
+    }
     epilogue_bar();
+    tc_fence_after();
     if (warp >= 4) {
       const int quarter = warp & 3, r = (32 * quarter + lane) & 63, half = quarter >> 1;
       const float inv = sh.inv[r];
