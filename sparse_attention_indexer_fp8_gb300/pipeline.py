@@ -22,7 +22,8 @@ import torch
 from . import (idx_dcp_topk_merge, idx_expand_candidates, idx_k_norm_rope_quant_and_cache, idx_k_quant_and_cache,
                idx_k_quant_and_cache_mxfp4, idx_kv_norm_rope_quant_and_cache, idx_paged_mqa_logits_decode,
                idx_paged_mqa_logits_decode_mxfp4, idx_q_rope_quant, idx_req_to_global_slots, idx_sparse_attention,
-               idx_sparse_attention_workspace_bytes, idx_sparse_topk_remap, idx_topk, idx_workspace_bytes)
+               idx_sparse_attention_workspace_bytes, idx_sparse_topk_remap, idx_topk, idx_workspace_bytes,
+               _heads, _mat, _vec)
 from . import workloads as W
 
 
@@ -210,6 +211,23 @@ class AttentionDecodeStep:
         return tuple(torch.zeros((num_blocks, stride), dtype=torch.uint8, device=self.out.device)
                      for stride in (W.block_stride_bytes(self.block_size), W.kv_block_stride_bytes(self.block_size)))
 
+    def _check_batch(self, new_k, q_index, w_index, q, block_table, ctx_lens):
+        """Refuse what is not of the step's batch before anything is enqueued: the q preparation, the scoring and the
+        selection take the step's own buffers and read as many rows of these."""
+        fn, dev, (batch, heads, _) = "AttentionDecodeStep", self.out.get_device(), self.out.shape
+        _vec(fn, "ctx_lens", ctx_lens, dev, torch.int32, batch)
+        _mat(fn, "block_table", block_table, dev, torch.int32, batch, None)
+        _heads(fn, "q", q, dev, batch, heads, W.ATTN_DIM)
+        if new_k.shape[0] < batch:
+            raise ValueError(f"{fn}: new_k has {new_k.shape[0]} rows, the batch {batch}")
+        if not (q_index.shape == self.q8.shape or (q_index.dim() == 2 and q_index.shape[0] == batch
+                                                   and q_index.shape[1] >= 64 * 128)):
+            raise ValueError(f"{fn}: q_index has shape {tuple(q_index.shape)}, expected {tuple(self.q8.shape)}")
+        if w_index.dim() != 2 or w_index.shape[0] != batch or w_index.shape[1] < 64:
+            raise ValueError(f"{fn}: w_index has shape {tuple(w_index.shape)}, expected {(batch, 64)}")
+        if q_index.get_device() != dev or w_index.get_device() != dev:
+            raise ValueError(f"{fn}: q_index and w_index must be on {self.out.device}")
+
     def insert(self, k, kv, k_weight, k_bias, kv_weight, positions, cos_sin, slots, k_cache, kv_cache, stream=None):
         """Any number of tokens: indexer k [n, 128] and attention projection [n, 576] into both caches."""
         idx_k_norm_rope_quant_and_cache(k, k_weight, k_bias, self.eps, positions, cos_sin, slots, k_cache,
@@ -219,7 +237,9 @@ class AttentionDecodeStep:
 
     def run(self, new_k, new_kv, k_weight, k_bias, kv_weight, positions, cos_sin, new_slots, q_index, w_index, q,
             k_cache, kv_cache, block_table, ctx_lens, stream=None):
-        """``ctx_lens`` count the new token; ``q`` [batch, heads, 576] is the absorbed and rotated query."""
+        """``ctx_lens`` (int32 [batch], at most ``max_ctx``) count the new token; ``q`` [batch, heads, 576] is the
+        absorbed and rotated query. A request that sits a step out has length 0 and a negative slot."""
+        self._check_batch(new_k, q_index, w_index, q, block_table, ctx_lens)
         self.insert(new_k, new_kv, k_weight, k_bias, kv_weight, positions, cos_sin, new_slots, k_cache, kv_cache,
                     stream=stream)
         idx_q_rope_quant(q_index, positions, cos_sin, w_index, self.q8, self.w, 128 ** -0.5, 64 ** -0.5,

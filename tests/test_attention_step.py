@@ -1,0 +1,68 @@
+"""The layer's decode step on the host: what it refuses, in which order it calls, and where (CPU only).
+
+The step's calls are replaced by records of themselves, so nothing is computed and no GPU is needed.
+"""
+
+import contextlib
+
+import pytest
+import torch
+
+from sparse_attention_indexer_fp8_gb300 import pipeline
+
+B, H, L, BS = 3, 8, 256, 64
+CALLS = ["idx_k_norm_rope_quant_and_cache", "idx_kv_norm_rope_quant_and_cache", "idx_q_rope_quant",
+         "idx_paged_mqa_logits_decode", "idx_topk", "idx_sparse_attention"]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names of the calls made, in order."""
+    made = []
+    for name in CALLS:
+        monkeypatch.setattr(pipeline, name, lambda *a, _n=name, **k: made.append(_n))
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    return made
+
+
+def arguments(**change):
+    f = torch.zeros
+    a = dict(new_k=f(B, 128), new_kv=f(B, 576), k_weight=f(128), k_bias=None, kv_weight=f(512),
+             positions=f(B, dtype=torch.int32), cos_sin=f(L, 64), new_slots=f(B, dtype=torch.int64),
+             q_index=f(B, 64, 128), w_index=f(B, 64), q=f(B, H, 576, dtype=torch.bfloat16),
+             k_cache=f(12, 8704, dtype=torch.uint8), kv_cache=f(12, 41472, dtype=torch.uint8),
+             block_table=f(B, L // BS, dtype=torch.int32), ctx_lens=f(B, dtype=torch.int32))
+    a.update(change)
+    return a
+
+
+def test_one_step_calls_everything_once(calls):
+    step = pipeline.AttentionDecodeStep(B, L, heads=H, topk=64, device="cpu")
+    step.run(**arguments())
+    assert calls == CALLS
+    step.run(**arguments(q_index=torch.zeros(B, 8192)))          # heads laid out in one row
+    assert calls == 2 * CALLS
+
+
+@pytest.mark.parametrize("name,value", [
+    ("ctx_lens", torch.zeros(B - 1, dtype=torch.int32)),         # the selection reads one length per row of the step
+    ("ctx_lens", torch.zeros(B, dtype=torch.int64)),
+    ("ctx_lens", torch.zeros(2 * B, dtype=torch.int32)[::2]),
+    ("block_table", torch.zeros(B - 1, 4, dtype=torch.int32)),
+    ("block_table", torch.zeros(B, 4, dtype=torch.int64)),
+    ("q_index", torch.zeros(B + 1, 64, 128)),                    # the step's q8 has B rows
+    ("q_index", torch.zeros(B - 1, 64, 128)),
+    ("q_index", torch.zeros(B, 32, 128)),
+    ("q_index", torch.zeros(B, 8191)),
+    ("w_index", torch.zeros(B, 32)),
+    ("w_index", torch.zeros(B - 1, 64)),
+    ("w_index", torch.zeros(64)),
+    ("new_k", torch.zeros(B - 1, 128)),                          # with it go the positions that q is rotated by
+    ("q", torch.zeros(B, H + 1, 576, dtype=torch.bfloat16)),
+    ("q", torch.zeros(B + 1, H, 576, dtype=torch.bfloat16)),
+])
+def test_a_step_refuses_other_shapes_before_it_enqueues_anything(calls, name, value):
+    step = pipeline.AttentionDecodeStep(B, L, heads=H, topk=64, device="cpu")
+    with pytest.raises(ValueError, match=name):
+        step.run(**arguments(**{name: value}))
+    assert calls == []
