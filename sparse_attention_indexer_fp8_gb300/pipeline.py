@@ -240,14 +240,16 @@ class AttentionDecodeStep:
         """``ctx_lens`` (int32 [batch], at most ``max_ctx``) count the new token; ``q`` [batch, heads, 576] is the
         absorbed and rotated query. A request that sits a step out has length 0 and a negative slot."""
         self._check_batch(new_k, q_index, w_index, q, block_table, ctx_lens)
-        self.insert(new_k, new_kv, k_weight, k_bias, kv_weight, positions, cos_sin, new_slots, k_cache, kv_cache,
-                    stream=stream)
-        idx_q_rope_quant(q_index, positions, cos_sin, w_index, self.q8, self.w, 128 ** -0.5, 64 ** -0.5,
-                         interleaved=self.index_interleaved, stream=stream)
-        slots = self.indexer.run(self.q8, self.w, k_cache, block_table, ctx_lens, stream=stream)
-        # the lists of contexts shorter than topk end with -1: nothing past a context's length is looked at
-        idx_sparse_attention(q, kv_cache, self.block_size, slots, self.out, self.softmax_scale, lse=self.lse,
-                             n_sel=ctx_lens, ws=self.ws, stream=stream)
+        # the q preparation, the scoring and the selection run on the current device and its current stream
+        with torch.cuda.device(self.out.device):
+            self.insert(new_k, new_kv, k_weight, k_bias, kv_weight, positions, cos_sin, new_slots, k_cache, kv_cache,
+                        stream=stream)
+            idx_q_rope_quant(q_index, positions, cos_sin, w_index, self.q8, self.w, 128 ** -0.5, 64 ** -0.5,
+                             interleaved=self.index_interleaved, stream=stream)
+            slots = self.indexer.run(self.q8, self.w, k_cache, block_table, ctx_lens, stream=stream)
+            # the lists of contexts shorter than topk end with -1: nothing past a context's length is looked at
+            idx_sparse_attention(q, kv_cache, self.block_size, slots, self.out, self.softmax_scale, lse=self.lse,
+                                 n_sel=ctx_lens, ws=self.ws, stream=stream)
         return self.out
 
 

@@ -66,3 +66,47 @@ def test_a_step_refuses_other_shapes_before_it_enqueues_anything(calls, name, va
     with pytest.raises(ValueError, match=name):
         step.run(**arguments(**{name: value}))
     assert calls == []
+
+
+class OnDevice:
+    """What the step sees of a tensor on another device than the current one."""
+
+    def __init__(self, tensor, index):
+        self.tensor, self.device, self.index = tensor, torch.device("cuda", index), index
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.tensor, name)
+
+    def __getitem__(self, at):
+        return OnDevice(self.tensor[at], self.index)
+
+
+@pytest.mark.parametrize("method", ["run", "insert"])
+def test_a_step_on_another_device_makes_every_call_there(calls, monkeypatch, method):
+    current = [0]
+    seen = []
+
+    @contextlib.contextmanager
+    def device(d):
+        was, current[0] = current[0], torch.device(d).index if not isinstance(d, int) else d
+        yield
+        current[0] = was
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    for name in CALLS:
+        monkeypatch.setattr(pipeline, name, lambda *a, _n=name, **k: seen.append((_n, current[0])))
+    step = pipeline.AttentionDecodeStep(B, L, heads=H, topk=64, device="cpu")
+    step.out = OnDevice(step.out, 1)
+    args = {k: OnDevice(v, 1) if isinstance(v, torch.Tensor) else v for k, v in arguments().items()}
+    if method == "run":
+        step.run(**args)
+        assert seen == [(n, 1) for n in CALLS]
+    else:
+        step.insert(*(args[n] for n in ("new_k", "new_kv", "k_weight", "k_bias", "kv_weight", "positions", "cos_sin",
+                                        "new_slots", "k_cache", "kv_cache")))
+        assert [n for n, _ in seen] == CALLS[:2]        # they choose the device of their tensors themselves
+    assert current[0] == 0
