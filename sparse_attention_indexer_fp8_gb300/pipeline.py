@@ -189,10 +189,13 @@ class AttentionDecodeStep:
     normalised, rotated and inserted into their caches, the indexer's q is
     prepared, ``DecodeStep`` scores and selects, and every head attends to the selected
     slots. Both caches share block tables and slots. ``run`` allocates nothing.
+    ``softmax_scale`` is that of the heads before absorption, which keeps their dot products:
+    by default 192 ** -0.5 (128 dims without position, 64 with); a model whose context was
+    extended with a factor on the logits passes the product of the two.
     """
 
     def __init__(self, batch: int, max_ctx: int, heads: int, topk: int = W.TOPK, block_size: int = W.BLOCK_SIZE,
-                 device="cuda", softmax_scale: float = W.ATTN_DIM ** -0.5, eps: float = 1e-6,
+                 device="cuda", softmax_scale: float = W.ATTN_HEAD_DIM ** -0.5, eps: float = 1e-6,
                  interleaved: bool = False, index_interleaved: bool = False):
         self.block_size, self.softmax_scale, self.eps = block_size, softmax_scale, eps
         # pairing of the rotary dims of the attention latent and of the indexer's q and k

@@ -46,6 +46,7 @@ def mxfp4_block_stride_bytes(block_size: int = BLOCK_SIZE, align: int = BLOCK_AL
 
 
 ATTN_DIM = 576               # key dims of the attention cache: 512 latent (the value) + 64 position dims
+ATTN_HEAD_DIM = 192          # dims of a query head before absorption: 128 without position + 64 with
 KV_TOKEN_BYTES = 644         # 512 e4m3 bytes + 64 bf16 position dims + 4 E8M0 scales
 
 

@@ -5,9 +5,11 @@ The step's calls are replaced by records of themselves, so nothing is computed a
 
 import contextlib
 
+import numpy as np
 import pytest
 import torch
 
+from oracle.attention import sparse_attention_row
 from sparse_attention_indexer_fp8_gb300 import pipeline
 
 B, H, L, BS = 3, 8, 256, 64
@@ -110,3 +112,22 @@ def test_a_step_on_another_device_makes_every_call_there(calls, monkeypatch, met
                                         "new_slots", "k_cache", "kv_cache")))
         assert [n for n, _ in seen] == CALLS[:2]        # they choose the device of their tensors themselves
     assert current[0] == 0
+
+
+def test_the_default_scale_is_that_of_the_heads_before_absorption(calls):
+    # heads of 128 dims without and 64 with position: their attention, and the absorbed query's over the latents
+    rng = np.random.default_rng(3)
+    heads, n = 4, 40
+    up = rng.normal(size=(heads, 128, 512)) / 512 ** 0.5           # latent -> key dims of each head
+    q_nope, q_pe = rng.normal(size=(heads, 128)), rng.normal(size=(heads, 64))
+    tokens = rng.normal(size=(n, 576))
+    keys = np.einsum("hdc,nc->hnd", up, tokens[:, :512])
+    z = (np.einsum("hd,hnd->hn", q_nope, keys) + q_pe @ tokens[:, 512:].T) / 192 ** 0.5
+    p = np.exp(z - z.max(axis=1, keepdims=True))
+    want = p / p.sum(axis=1, keepdims=True) @ tokens[:, :512]
+    absorbed = np.concatenate([np.einsum("hd,hdc->hc", q_nope, up), q_pe], axis=1)
+    step = pipeline.AttentionDecodeStep(B, L, heads=H, topk=64, device="cpu")
+    out, lse, _, _ = sparse_attention_row(absorbed, tokens, step.softmax_scale)
+    assert np.allclose(out, want, rtol=1e-10, atol=1e-12)
+    assert np.allclose(lse, np.log(np.exp(z).sum(axis=1)), rtol=1e-10)
+    assert pipeline.AttentionDecodeStep(B, L, heads=H, topk=64, device="cpu", softmax_scale=0.5).softmax_scale == 0.5
