@@ -272,7 +272,18 @@ def _refuse(fn: str, name: str, t, dev: int, dtype, shape) -> None:
         raise ValueError(f"{fn}: {name} must have {len(shape)} dimensions, got {len(have)}")
     if any(w is not None and h != w for h, w in zip(have, shape)):
         raise ValueError(f"{fn}: {name} has shape {have}, expected {shape}")
+    if max(have) > _MAX_EXTENT:
+        raise ValueError(f"{fn}: {name} has shape {have}: extents of 2**31 and more are not taken")
     raise ValueError(f"{fn}: {name} must have a unit stride in its last dimension")
+
+
+_MAX_EXTENT = (1 << 31) - 1  # the entry points take extents in 32 bits, and ctypes would cut what exceeds them
+
+
+def _int32(fn: str, name: str, v: int) -> int:
+    if not -_MAX_EXTENT - 1 <= v <= _MAX_EXTENT:
+        raise ValueError(f"{fn}: {name} {v} does not fit in 32 bits")
+    return v
 
 
 def _vec(fn: str, name: str, t, dev: int, dtype, n: int) -> int:
@@ -290,7 +301,7 @@ def _mat(fn: str, name: str, t, dev: int, dtype, rows, cols):
         r, c = t.shape
         if (rows is None or r == rows) and (cols is None or c == cols):
             ld, step = t.stride()
-            if step == 1 or c < 2:
+            if (step == 1 or c < 2) and r <= _MAX_EXTENT and c <= _MAX_EXTENT:
                 return t.data_ptr(), ld if r > 1 or ld > c else c
     _refuse(fn, name, t, dev, dtype, (rows, cols))
 
@@ -301,7 +312,7 @@ def _heads(fn: str, name: str, t, dev: int, rows, heads, dims: int):
         r, h, d = t.shape
         if d == dims and (rows is None or r == rows) and (heads is None or h == heads):
             ld, ldh, step = t.stride()
-            if step == 1:
+            if step == 1 and r <= _MAX_EXTENT and h <= _MAX_EXTENT:
                 return t.data_ptr(), ld if r > 1 else dims, ldh if h > 1 else dims
     _refuse(fn, name, t, dev, torch.bfloat16, (rows, heads, dims))
 
@@ -425,7 +436,9 @@ def idx_gather_kv(cache, block_size, block_table, cu_lens, out, starts=None, str
 
 def idx_sparse_attention_workspace_bytes(rows: int, heads: int, topk: int) -> int:
     """Bytes of the workspace with which idx_sparse_attention splits these rows' lists (0: it would not)."""
-    return library().idx_sparse_attention_workspace_bytes(rows, heads, topk)
+    fn = "idx_sparse_attention_workspace_bytes"
+    return library().idx_sparse_attention_workspace_bytes(
+        _int32(fn, "rows", rows), _int32(fn, "heads", heads), _int32(fn, "topk", topk))
 
 
 def idx_sparse_attention(q, cache, block_size, slots, out, softmax_scale, lse=None, n_sel=None, block_span=None,
@@ -449,7 +462,8 @@ def idx_sparse_attention(q, cache, block_size, slots, out, softmax_scale, lse=No
         wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
     lp, ld_lse = (None, 0) if lse is None else _mat(fn, "lse", lse, dev, torch.float32, T, H)
     cp, blocks, bs, stride = _cache_args(fn, cache, dev, block_size, 644)
-    _call(fn, dev, stream, qp, ld_q, ld_qh, cp, blocks, bs, stride, bs if block_span is None else block_span, sp,
+    _call(fn, dev, stream, qp, ld_q, ld_qh, cp, blocks, bs, stride,
+          bs if block_span is None else _int32(fn, "block_span", block_span), sp,
           ld_slots, slots.shape[1], None if n_sel is None else _vec(fn, "n_sel", n_sel, dev, torch.int32, T), T, H,
           softmax_scale, op, ld_out, ld_oh, lp, ld_lse, wp, wb)
 
