@@ -631,6 +631,8 @@ idx_status_t idx_k_norm_rope_quant_and_cache(const void* k, int k_dtype, int64_t
  * stands for e4m3 * 2^(code - 127), which a bf16 holds exactly (down to 2^-126).
  * The scale of 128 dims is the smallest power of two >= amax / 448 (binary32
  * quotient), its code held to [0, 134]: latents beyond 448 * 2^7 = 57344 saturate.
+ * 128 dims one of which is an infinity or a NaN are stored as zeros under code 255,
+ * E8M0's NaN, and all of them read as NaN.
  * Split block layout: block b starts at b * block_stride_bytes; token i of it
  * keeps its e4m3 bytes at 512 i, its position dims at 512 * block_size + 128 i and
  * its four codes at 640 * block_size + 4 i. block_size is 16, 32, 64 or 128;
@@ -648,7 +650,8 @@ idx_status_t idx_k_norm_rope_quant_and_cache(const void* k, int k_dtype, int64_t
  *   y quantised as the attention cache defines, z rounded to bf16, both stored.
  *
  *   c             [n_tok, 512] of dtype (IDX_BF16 or IDX_F32), ld_c elements
- *                 between tokens (>= 512); finite.
+ *                 between tokens (>= 512). A token that is not finite, before or
+ *                 after the norm, is stored as one that reads as NaN.
  *   pe            [n_tok, 64] of dtype, ld_pe >= 64. Both may be column slices of
  *                 one [n_tok, 576] projection.
  *   weight        float [512] or NULL; eps >= 0.

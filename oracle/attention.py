@@ -104,9 +104,9 @@ def kv_put(cache, block_size, slot, codes, pe_bits, scale_codes):
 
 
 def kv_token(cache, block_size, slot) -> np.ndarray:
-    """The 576 dims that one slot stands for."""
+    """The 576 dims that one slot stands for; NaN under scale code 255."""
     codes, pe, sc = kv_record(cache, block_size, slot)
-    scale = np.exp2(sc.astype(np.float64) - 127)
+    scale = np.where(sc == 255, np.nan, np.exp2(sc.astype(np.float64) - 127))
     return np.concatenate([e4m3_decode(codes) * np.repeat(scale, 128), bf16_decode(pe).astype(np.float64)])
 
 

@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
     setup();
     for (int i = group; i < tiles; i += kStages) {
-      codes = __vminu4(next_codes, kKvMaxScaleCode * 0x01010101u);
+      codes = __vminu4(next_codes, kKvCodeLimit * 0x01010101u);
       uint4 early[kEarly][2];
 #pragma unroll
       for (int j = 0; j < kEarly; ++j) {

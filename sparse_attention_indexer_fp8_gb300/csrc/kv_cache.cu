@@ -192,16 +192,20 @@ k_norm_rope_quant_kernel(const void* __restrict__ k, int64_t ld_k, int n_tok, bo
 // E8M0 code of a 128-dim tile: the smallest power of two >= amax / 448, held to
 // 2^-127 .. 2^7 (code 0 .. 134). The upper end makes one bf16 multiplication
 // by 2^(code - 7) dequantise a value exactly (kv_layout.cuh); it saturates
-// latents beyond 57344.
-__device__ __forceinline__ uint32_t kv_scale_code(float amax) {
-  const uint32_t b = __float_as_uint(ue8m0_ceil(__fdiv_rn(amax, 448.0f)));
+// latents beyond 57344. `amax` is the bit pattern of the largest |value|: as whole numbers the patterns are
+// ordered as the values are, infinity above them and NaN above infinity, so the maximum of a tile
+// says whether all of it is finite (fmaxf would pass over a NaN).
+__device__ __forceinline__ uint32_t kv_scale_code(uint32_t amax) {
+  if (amax >= 0x7F800000u) return kKvNanScaleCode;
+  const uint32_t b = __float_as_uint(ue8m0_ceil(__fdiv_rn(__uint_as_float(amax), 448.0f)));
   return min(b >> 23, static_cast<uint32_t>(kKvMaxScaleCode));
 }
 
 // Eight dims as e4m3 under a power-of-two scale: the product by 2^(127 - code) is
 // exact (up to results far below e4m3's smallest step), so the code is the
-// definition's round-to-nearest-even of y / scale.
+// definition's round-to-nearest-even of y / scale. Zeros under the code for NaN.
 __device__ __forceinline__ uint2 e4m3x8(const float (&y)[8], uint32_t code) {
+  if (code == kKvNanScaleCode) return make_uint2(0u, 0u);
   // 2^(127 - code), code <= 134: exponent field 254 - code, a normal float
   const float inv = __uint_as_float((254u - code) << 23);
   uint32_t w[4];
@@ -287,11 +291,11 @@ kv_norm_rope_quant_kernel(const void* __restrict__ c, int64_t ld_c, const void* 
   uint32_t code[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float amax = 0.f;
+    uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[h][i]));
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[h][i]) & 0x7FFFFFFFu);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     code[h] = kv_scale_code(amax);
     *reinterpret_cast<uint2*>(base + off * kKvLatent + 256 * h + 8 * lane) = e4m3x8(x[h], code[h]);
   }

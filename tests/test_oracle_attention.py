@@ -137,3 +137,10 @@ def test_binary32_attention_with_bf16_weights_stays_within_the_stated_errors():
         o = (p.bfloat16().float() @ tok.float()[:, :512] / p.sum(1, keepdim=True)).bfloat16()
         assert (np.abs(o.double().numpy() - out) <= oerr).all()
         assert (np.abs(torch.logsumexp(z, 1).double().numpy() - lse) <= lerr).all()
+
+
+def test_scale_code_255_stands_for_nan():
+    cache = np.zeros((1, 16 * 644), dtype=np.uint8)
+    A.kv_put(cache, 16, 2, np.zeros(512), np.zeros(64), [127, 255, 134, 0])
+    t = A.kv_token(cache, 16, 2)
+    assert np.isnan(t[128:256]).all() and (np.delete(t, np.arange(128, 256)) == 0).all()
