@@ -130,3 +130,22 @@ def assert_topk_values_exact(sel, values, k: int, what: str = "topk") -> None:
     want = np.sort(values.astype(np.float64))[::-1][:m]
     got = np.sort(values[chosen].astype(np.float64))[::-1]
     assert np.array_equal(got, want), f"{what}: selected values differ from the top-{k} values"
+
+
+def assert_attention_counts(out, lse, dims, what=""):
+    """Attention with every weight 1 over tokens that are 1 at one dim each (``dims`` [n]) and 0 elsewhere.
+
+    out [H, D] is count(dim) / n and lse [H] ln(n). The counts are exact in binary32, so what differs are the roundings of
+    1 / n and of the product (2^-24 each, 2^-22 taken) and of the bf16 store (2^-8 of the value). ln(n) comes from
+    log2 (within a unit of its last place, 2^-20 at most for n < 2^16) and a product: 2^-21 of it, or of 1. A count of at most
+    100 changes by 1 % or more with one token more or less, and lse by 1 / n.
+    """
+    out, lse = np.asarray(out, dtype=np.float64), np.asarray(lse, dtype=np.float64)
+    n = len(dims)
+    if n == 0:
+        assert not out.any() and np.isneginf(lse).all(), what
+        return
+    want = np.bincount(dims, minlength=out.shape[1]) / n
+    assert want.max() * n <= 100, what
+    assert (np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -22) * want).all(), what
+    assert (np.abs(lse - np.log(n)) <= 2.0 ** -21 * max(1.0, np.log(n))).all(), what

@@ -10,7 +10,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.checks import ATOL, RTOL, assert_logits_close, bf16_rounding_interval, tol
+from tests.checks import (ATOL, RTOL, assert_attention_counts, assert_logits_close, bf16_rounding_interval,
+                          tol)
 
 
 def _bf16(x):
@@ -55,3 +56,32 @@ def test_bf16_check_accepts_rounded_in_band_values_and_rejects_one_step_out():
 def test_tolerance_constants():
     assert ATOL == 1e-3 and RTOL == 2e-3
     assert tol(0.0) == ATOL and tol(-10.0) == ATOL + RTOL * 10
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 63, 777, 5000, 8192])
+def test_attention_counts_notice_one_token(n):
+    rng = np.random.default_rng(n)
+    dims = rng.integers(0, 512, n)
+
+    def result(d):
+        counts = np.bincount(d, minlength=512).astype(np.float32)
+        m = np.float32(len(d))
+        lse = np.log2(m).astype(np.float32) * np.float32(0.69314718)
+        return _bf16(counts * (np.float32(1) / m))[None], np.array([lse])
+
+    assert_attention_counts(*result(dims), dims)
+    wrong = [np.append(dims, dims[0]), np.append(dims, (dims[-1] + 1) % 512)]
+    if n > 1:
+        wrong += [dims[:-1], dims[1:], np.concatenate([dims[:n // 2], dims[n // 2 + 1:]]),
+                  np.append(dims[:-1], (dims[-1] + 1) % 512)]       # another token in its place: the same lse
+    for d in wrong:
+        with pytest.raises(AssertionError):
+            assert_attention_counts(*result(d), dims)
+    # ... in the value alone, whatever the lse says
+    good = result(dims)[1]
+    for d in wrong:
+        if n == 1 and set(d) == set(dims):
+            continue                                               # the same token twice: the same value
+        with pytest.raises(AssertionError):
+            assert_attention_counts(result(d)[0], good, dims)
+    assert_attention_counts(np.zeros((1, 512)), np.array([-np.inf]), dims[:0])

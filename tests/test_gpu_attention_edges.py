@@ -9,6 +9,7 @@ import torch
 import sparse_attention_indexer_fp8_gb300 as idx
 from oracle import attention as A
 from oracle.codecs import bf16_decode, bf16_encode, e4m3_decode, e4m3_encode
+from tests.checks import assert_attention_counts
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -229,23 +230,12 @@ def counting_cache(blocks, bs):
 
 
 def check_counts(slots, n_sel, out, lse, K, span, bs, blocks):
-    """With softmax_scale 0 every weight is exactly 1: out is count(dim) / n, the counts exact in binary32, within
-    the roundings of 1 / n, of the product (2^-24 each) and of bf16 (2^-8 of the value); a token more or
-    less changes a count of at most 100 by 1 % or more. lse is ln(n): 2^-21 covers log2, the product and the joined sums' roundings
-    at n up to 2^13, where one token changes it by 1.2e-4."""
     got, g = out.double().cpu().numpy(), lse.double().cpu().numpy()
     for t in range(len(slots)):
         lst = slots[t][:max(0, min(K, int(n_sel[t])))]
         blk, off = lst // span, lst % span
         lst = (blk * bs + off)[(lst >= 0) & (blk < blocks) & (off < bs)]
-        count = np.bincount(lst % 512, minlength=512).astype(float)
-        n = len(lst)
-        if n == 0:
-            assert not got[t].any() and np.isneginf(g[t]).all()
-            continue
-        assert count.max() <= 100
-        assert (np.abs(got[t] - count / n) <= (2.0 ** -8 + 2.0 ** -22) * count / n).all(), (t, n)
-        assert (np.abs(g[t] - np.log(n)) <= 2.0 ** -21 * max(1.0, np.log(n))).all(), (t, n)
+        assert_attention_counts(got[t], g[t], lst % 512, (t, len(lst)))
 
 
 @pytest.mark.parametrize("T,H,K,parts", [
