@@ -52,7 +52,7 @@ struct AttnParams {
 // with tcgen05.mma.ws (M = 64) in bf16 x bf16 -> fp32. The weight-stationary form is taken
 // because its M = 64 fills all 128 tensor-memory lanes (row r, column half c / (N / 2) in lane
 // r + 64 (c / (N / 2))): O takes 256 columns, where the plain form would take all 512 and leave none
-// for S, and runs at half the rate (N = 256: 128 clocks against 80 on a GB300).
+// for S, and runs at five eighths of the rate (N = 256: 128 clocks against 80 on a GB300).
 //
 // Roles: warps 4-19 gather and dequantise the tokens' latents, warps 21-22 copy their position
 // dims and prefetch, warp 20 issues the matrix instructions, warps 0-3 load Q and do the
@@ -62,23 +62,29 @@ struct AttnParams {
 // pieces (64 dims each). Read along the dims it is the K-major B operand of S, read along the
 // tokens the N-major B operand of O. Two tiles of 72 KB are in flight beside Q (72 KB) and P (8 KB).
 //
-// Two groups of eight loader warps own a stage each. A group converts and stores its tile, then
-// issues every load of its next one at once, into registers: memory latency runs under the other
-// group's conversion and the matrix work, with no staging buffer, for which there is no room. (One
-// group that refilled each register right after its conversion measured 7000 clocks a tile: loads
-// of two tiles shared scoreboards, so every conversion waited for the newest load.) What a warp
-// keeps in flight is limited whatever it asks for: random 512-byte rows read by 8 warps an SM came
-// at 3.2 TB/s, by 16 at 5.4 TB/s, by 32 at 6.4 TB/s, with 8 or 16 rows asked for by each; hence
-// sixteen, and the prefetch into L2.
+// Two groups of eight loader warps own a stage each. A group converts and stores its tile, then issues
+// every load of its next one at once, into registers: memory latency runs under the other group's
+// conversion and the matrix work, with no staging buffer. (There was no room for one beside all of Q;
+// since two thirds of Q went to tensor memory, 48 KB of its place are read by nobody once it is there.)
+// (One group that refilled each register right after its conversion measured 7000 clocks a tile: loads of
+// two tiles shared scoreboards, so every conversion waited for the newest load.) What a warp keeps in
+// flight is limited whatever it asks for: random 512-byte rows read by 8 warps an SM came at 3.2 TB/s, by
+// 16 at 5.4 TB/s, by 32 at 6.4 TB/s, with 8 or 16 rows asked for by each; hence sixteen, and the prefetch
+// into L2.
 //
-// What bounds it: the data pipe of shared memory and L1, busy 90 % of the time on the SMs that work (ncu).
-// Per tile, in clocks of it: S 768 and O 640 (S would take 1152 without Q's larger part in tensor
-// memory), the stores, shuffles and P 1170, the loads 660, of some 3600 in all with a block's start and
-// end. Leaving out any one kind of work in a copy saved 5 to 11 %. 128 rows x 16 heads x 2048 tokens:
-// 57 us (3.0 TB/s of records; the records alone take 26 us at the measured HBM rate); 1024 rows x 128
-// heads: 763 us (763 TFLOP/s). Pairs of blocks that shared a tile's tokens (cta_group::2, M = 128) read
-// less but measured 867 us there: values that cross between two SMs came at 10 bytes a clock, and
-// gathered twice they cost what was saved.
+// What bounds it: no counter is full. A tile takes 1.45 us (16 heads) to 1.48 us (64) of a block's time,
+// some 2950 clocks: the slope from lists of 2048 to lists of 4096 entries, 128 rows. ncu counts per tile
+// 1408 wavefronts of shared memory by the tensor core (S 768, O 640; S would take 1152 without Q's larger
+// part in tensor memory) and 1830 by loads and stores (stores, shuffles and P 1170, the loads 660), 39 %
+// and 51 % of the 3580 clocks that a tile takes with its share of a block's start and end. Their sum is
+// more than the slope, so the two overlap and neither is the bound. Leaving out any one kind of work in a
+// copy saved 5 to 11 %. That fits a chain: tile i + 2 may be stored only after O of tile i, and then its
+// conversion, S, softmax and O follow in a row. 128 rows x 16 heads x 2048 tokens: 57 us where rows share
+// eight contexts of 32 K tokens (the records of the entries take 26 us at the measured HBM rate, the
+// distinct ones 16), 64 us where each row has 96 K tokens of its own (25 us); 1024 rows x 128 heads: 763
+// us (763 TFLOP/s). Pairs of blocks that shared a tile's tokens (cta_group::2, M = 128) read less but
+// measured 867 us there: values that cross between two SMs came at 10 bytes a clock, and gathered twice
+// they cost what was saved.
 // ---------------------------------------------------------------------------
 constexpr int kHeadsPerBlock = 64;
 constexpr int kTile = 64;
@@ -704,6 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
       }
       m = m_new;
+      // The weights are rounded to bf16 for the product: its operands have one type, and bf16 is the one that holds every
+      // token exactly. l sums them unrounded, so lse keeps its 32 bits, and out differs from the exact value by 2.1e-3
+      // (norm) where its own rounding alone makes 1.65e-3. A second product with the rest would cost O again.
       const float ref = m == -INFINITY ? 0.f : m;
       uint32_t w[16];
 #pragma unroll
@@ -900,8 +909,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
 }
 
 // Parts that a list of k entries is split into: as many as one wave of blocks has room for, if that
-// is cheaper than whole rows. In units of a tile (1.45 us on a GB300) a block's start and end cost six, whole or
-// part, and the join four. Lists of 2048, 64 heads, in parts against whole: one row 14 us (32 parts) and
+// is cheaper than whole rows. In units of a tile (1.46 us on a GB300) a block's start and end cost some seven with the
+// launch, whole or part, and the join four. Lists of 2048, 64 heads, in parts against whole: one row 14 us (32 parts) and
 // 57 us, 16 rows 22 (8) and 57, 64 rows 41 (2) and 58. A second wave of parts does not pay: 100 rows
 // measured 80 us in three parts and 59 whole.
 int attention_parts(int64_t blocks, int k, int sms) {

@@ -103,7 +103,8 @@ __device__ __forceinline__ const float* angles(const RopeArgs& r, int tok) {
 // taken of the centred values (a second sum over registers), in binary32. The
 // only chain of loads is position, then angles, and both are asked for before
 // anything is used: a token costs two memory latencies, not four. Measured on a
-// GB300 (bf16 in): 128 tokens 4.1 us, 8192 tokens 6.4 us (0.8 us of bytes).
+// GB300 (bf16 in): 128 tokens 4.2 us, 8192 tokens 6.4 us (0.8 us of bytes; at 39
+// registers 48 warps fit an SM, so these are 1.12 waves of two latencies each).
 template <bool kBf16>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 k_norm_rope_quant_kernel(const void* __restrict__ k, int64_t ld_k, int n_tok, bool vec,
@@ -220,8 +221,9 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&y)[8], uint32_t code) {
 // position dims (optional), e4m3 with one E8M0 scale per 128 dims, insert. Lane l
 // owns dims 8l..8l+7 and 256 + 8l..+7, so each of the two loads and stores of the
 // warp is one contiguous run and a scale's tile is half a warp. Of the position
-// dims it owns one pair. Measured on a GB300 (bf16 in): 128 tokens 4.1 us, 8192
-// tokens 8.3 us (2.5 us of bytes; with the angles asked for after the slot 11.3).
+// dims it owns one pair. Measured on a GB300 (bf16 in): 128 tokens 4.2 us, 8192
+// tokens 8.3 us (2.5 us of bytes; at 43 registers 40 warps fit an SM: 1.35 waves;
+// with the angles asked for after the slot 11.3).
 template <bool kBf16>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 kv_norm_rope_quant_kernel(const void* __restrict__ c, int64_t ld_c, const void* __restrict__ pe, int64_t ld_pe,
