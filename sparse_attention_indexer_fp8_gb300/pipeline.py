@@ -219,14 +219,15 @@ class AttentionDecodeStep:
         selection take the step's own buffers and read as many rows of these."""
         fn, dev, (batch, heads, _) = "AttentionDecodeStep", self.out.get_device(), self.out.shape
         _vec(fn, "ctx_lens", ctx_lens, dev, torch.int32, batch)
-        _mat(fn, "block_table", block_table, dev, torch.int32, batch, None)
+        _mat(fn, "block_table", block_table, dev, torch.int32, None, None)
         _heads(fn, "q", q, dev, batch, heads, W.ATTN_DIM)
-        if new_k.shape[0] < batch:
-            raise ValueError(f"{fn}: new_k has {new_k.shape[0]} rows, the batch {batch}")
+        for name, t in (("new_k", new_k), ("block_table", block_table), ("w_index", w_index)):
+            if t.shape[0] < batch:
+                raise ValueError(f"{fn}: {name} has {t.shape[0]} rows, the batch {batch}")
         if not (q_index.shape == self.q8.shape or (q_index.dim() == 2 and q_index.shape[0] == batch
                                                    and q_index.shape[1] >= 64 * 128)):
             raise ValueError(f"{fn}: q_index has shape {tuple(q_index.shape)}, expected {tuple(self.q8.shape)}")
-        if w_index.dim() != 2 or w_index.shape[0] != batch or w_index.shape[1] < 64:
+        if w_index.dim() != 2 or w_index.shape[1] < 64:
             raise ValueError(f"{fn}: w_index has shape {tuple(w_index.shape)}, expected {(batch, 64)}")
         if q_index.get_device() != dev or w_index.get_device() != dev:
             raise ValueError(f"{fn}: q_index and w_index must be on {self.out.device}")

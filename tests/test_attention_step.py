@@ -44,6 +44,9 @@ def test_one_step_calls_everything_once(calls):
     assert calls == CALLS
     step.run(**arguments(q_index=torch.zeros(B, 8192)))          # heads laid out in one row
     assert calls == 2 * CALLS
+    # tables and weights of a larger batch, of which the step uses the first rows
+    step.run(**arguments(block_table=torch.zeros(B + 5, 4, dtype=torch.int32), w_index=torch.zeros(B + 1, 64)))
+    assert calls == 3 * CALLS
 
 
 @pytest.mark.parametrize("name,value", [
