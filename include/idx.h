@@ -755,6 +755,119 @@ idx_status_t idx_sparse_attention(const void* q, int64_t ld_q, int64_t ld_qh, co
 size_t idx_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t k);
 
 /*
+ * idx_build_tables - block tables, slots and positions of a step's new tokens, from lengths.
+ *
+ * Request b < B has cached_lens[b] tokens in the cache and brings new_lens[b] more. With bs = block_size:
+ *   ctx_lens[b]  = cached_lens[b] + new_lens[b]
+ *   fresh(b)     = max(0, min(ceil(ctx_lens[b] / bs), n_pages) - held_pages[b])  blocks to take;
+ *                  held_pages NULL: min(ceil(cached_lens[b] / bs), n_pages)
+ *   block_table[b, held_pages[b] + j] = free_blocks[free_start + sum of fresh over the requests before b + j]
+ * Pages below held_pages[b] keep their entries, so blocks that an earlier step took for drafted tokens that were
+ * dropped are used again. The new tokens are the rows of the step, packed request after request:
+ *   cu_rows      int32 [B + 1]: first row of each request (the sums of new_lens)
+ *   cu_ctx       int32 [B + 1]: the sums of ctx_lens (the cu_lens of idx_gather_kv)
+ *   positions    int32 [n_rows]: cached_lens[b] + i for row i of request b
+ *   slot_mapping int64 [n_rows]: block_table[b, position / bs] * bs + position % bs; -1 without a block
+ *   row_to_req   int32 [n_rows]: b
+ *   row_ke       int32 [n_rows]: position + 1, the columns that the row sees
+ * Rows from cu_rows[B] on are padding: position 0, slot -1 (the inserts skip it), request 0, row_ke 0.
+ *   held_out     int32 [B]: held_pages and the blocks taken
+ *   free_end     int32 [1]: free_start and all blocks taken
+ * cu_ctx, held_out, free_end, row_to_req and row_ke may be NULL. So may free_start (int32 [1]; 0).
+ * ctx_lens may be cached_lens, held_out held_pages and free_end free_start: a captured step then advances its own
+ * lengths at every replay. No other output may overlap an input.
+ *   block_table  int32 [B, n_pages], row stride ld_bt (>= n_pages), pages below held_pages read, fresh ones written.
+ *   free_blocks  int32 [n_free].
+ * Where free_blocks ends, later pages get -1 and are not counted in held_out or free_end: their requests can be
+ * served by a later call. That, a context longer than n_pages blocks (its tokens beyond have slot -1), a negative
+ * length (its request counts as empty), a page count outside [0, n_pages] or more new tokens than n_rows (those
+ * beyond are not written) raise the device flag. Sums beyond 2^31 - 1 are held to it.
+ * Errors: IDX_ERR_INVALID_ARG for NULL pointers, negative sizes or a short stride; IDX_ERR_UNSUPPORTED for another
+ * block_size or more than IDX_TABLES_MAX_REQUESTS requests.
+ */
+#define IDX_TABLES_MAX_REQUESTS 8192
+idx_status_t idx_build_tables(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* held_pages,
+                              int32_t B, const int32_t* free_blocks, int32_t n_free, const int32_t* free_start,
+                              int32_t* block_table, int64_t ld_bt, int32_t n_pages, int32_t block_size,
+                              int32_t* ctx_lens, int32_t* cu_rows, int32_t* cu_ctx, int32_t* held_out,
+                              int32_t* free_end, int32_t* positions, int64_t* slot_mapping, int32_t* row_to_req,
+                              int32_t* row_ke, int32_t n_rows, cudaStream_t stream);
+
+/*
+ * idx_tree_mask - who sees whom among the drafted tokens of trees.
+ *
+ * Rows [cu_rows[b], cu_rows[b + 1]) are the nodes of request b's tree, parents before children.
+ *   parents    int32 [n_rows]: the node's parent, counted within its request, or -1 for a child of the request's
+ *              last token in the cache.
+ *   mask       int32 [n_rows, words], row stride ld_mask (>= words): bit m % 32 of word m / 32 is set where node m of
+ *              the row's request is the row's own or one of its ancestors (idx_tree_attention reads it).
+ *   positions  int32 [n_rows] or NULL: base_lens[b] + the number of the node's ancestors, for the rotation (the
+ *              slots of drafted tokens go by their order: idx_build_tables). base_lens int32 [B], or NULL: 0.
+ * Rows outside [cu_rows[0], cu_rows[B]) are left as they were. A parent that is not an earlier node counts as
+ * -1; a node from 32 * words on has no bit: its mask is empty and its position base_lens[b]. Both raise the
+ * device flag.
+ * Errors: IDX_ERR_INVALID_ARG for NULL pointers, negative sizes, words < 1 or a short stride; IDX_ERR_UNSUPPORTED
+ * for more than IDX_TREE_MAX_WORDS words.
+ */
+#define IDX_TREE_MAX_WORDS 32
+idx_status_t idx_tree_mask(const int32_t* parents, const int32_t* cu_rows, int32_t B, int32_t n_rows,
+                           const int32_t* base_lens, int32_t* mask, int64_t ld_mask, int32_t words,
+                           int32_t* positions, cudaStream_t stream);
+
+/*
+ * idx_window_attention - causal attention of new tokens over the paged attention cache, within a sliding window and
+ * over the first tokens of the request.
+ *
+ * Rows [cu_rows[b], cu_rows[b + 1]) of q are the last tokens of request b, whose ctx_lens[b] tokens (the new ones
+ * among them) are in the cache: token j in block block_table[b, j / block_size] at offset j % block_size. With
+ * n = cu_rows[b + 1] - cu_rows[b], row i has position p = ctx_lens[b] - n + i and attends to the tokens
+ *   j <= p with j > p - window or j < sinks.
+ * window >= ctx_lens is plain causal attention. With K_j the token's 576 dims and V_j its first 512:
+ *   s[h, j] = softmax_scale * sum_d q[t, h, d] * K_j[d]
+ *   out[t, h] = sum_j exp(s[h, j]) V_j / sum_j exp(s[h, j]),   lse[t, h] = ln(sum_j exp(s[h, j])).
+ * A row that sees no token (p < 0) gets out = 0 and lse = -inf; rows outside [cu_rows[0], cu_rows[B]) are left as
+ * they were. Pages that no row sees are not looked up: their table entries and blocks may be anything. A token that
+ * a row does not see has no part in its result, whatever the record holds; one that reads as NaN (see
+ * idx_kv_norm_rope_quant_and_cache) makes the results of the rows that see it NaN. Precision as idx_sparse_attention.
+ *
+ *   q, out, lse, H, softmax_scale, the cache: as idx_sparse_attention (T rows of q, out and lse).
+ *   block_table  int32 [B, n_pages], row stride ld_bt (>= n_pages). A visible page outside [0, n_pages), or whose
+ *                block is outside [0, num_blocks), is skipped and raises the device flag.
+ *   cu_rows      int32 [B + 1], ascending, within [0, T];  ctx_lens int32 [B].
+ *   window >= 1, sinks >= 0.
+ *   ws           NULL, or idx_paged_attention_workspace_bytes(T, B, H) bytes, 16-byte aligned: with it the contexts
+ *                of a few rows are split over the GPU's SMs and joined by a second launch. Its contents need no
+ *                preparation and mean nothing after the call; calls that may overlap need one each.
+ * Errors: as idx_sparse_attention, and IDX_ERR_INVALID_ARG for window < 1 or sinks < 0.
+ */
+idx_status_t idx_window_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache,
+                                  int32_t num_blocks, int32_t block_size, int64_t block_stride_bytes,
+                                  const int32_t* block_table, int64_t ld_bt, int32_t n_pages, const int32_t* cu_rows,
+                                  const int32_t* ctx_lens, int32_t B, int32_t window, int32_t sinks, int32_t T,
+                                  int32_t H, float softmax_scale, void* out, int64_t ld_out, int64_t ld_oh,
+                                  float* lse, int64_t ld_lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * idx_tree_attention - attention of a tree of drafted tokens over the cache.
+ *
+ * As idx_window_attention, but row i of request b is node i of its tree, whose n nodes are the last n of the
+ * request's ctx_lens[b] tokens in the cache, in this order. It attends to every token j < ctx_lens[b] - n, and to
+ * node m (token ctx_lens[b] - n + m) where bit m % 32 of mask[t, m / 32] is set (idx_tree_mask). Nodes from
+ * 32 * words on are seen by none.
+ *   mask  int32 [T, words], row stride ld_mask (>= words), 0 <= words <= IDX_TREE_MAX_WORDS.
+ */
+idx_status_t idx_tree_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache, int32_t num_blocks,
+                                int32_t block_size, int64_t block_stride_bytes, const int32_t* block_table,
+                                int64_t ld_bt, int32_t n_pages, const int32_t* cu_rows, const int32_t* ctx_lens,
+                                int32_t B, const int32_t* mask, int64_t ld_mask, int32_t words, int32_t T, int32_t H,
+                                float softmax_scale, void* out, int64_t ld_out, int64_t ld_oh, float* lse,
+                                int64_t ld_lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of the optional workspace of idx_window_attention and idx_tree_attention on the current device (host only; 0:
+ * none is used). */
+size_t idx_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H);
+
+/*
  * idx_block_span - tokens per physical block of a pool (host only).
  *
  * The DSV4 packed-KV fix, 实现拆解 item 1: block_span = block_stride /

@@ -22,7 +22,8 @@ __all__ = [
     "idx_req_to_global_slots", "idx_dcp_topk_merge", "idx_q_rope_quant", "idx_block_span",
     "idx_workspace_bytes", "idx_device_error", "library",
     "idx_k_norm_rope_quant_and_cache", "idx_kv_norm_rope_quant_and_cache", "idx_gather_kv", "idx_sparse_attention",
-    "idx_sparse_attention_workspace_bytes",
+    "idx_sparse_attention_workspace_bytes", "idx_build_tables", "idx_tree_mask", "idx_window_attention",
+    "idx_tree_attention", "idx_paged_attention_workspace_bytes",
 ]
 
 
@@ -466,6 +467,107 @@ def idx_sparse_attention(q, cache, block_size, slots, out, softmax_scale, lse=No
           bs if block_span is None else _int32(fn, "block_span", block_span), sp,
           ld_slots, slots.shape[1], None if n_sel is None else _vec(fn, "n_sel", n_sel, dev, torch.int32, T), T, H,
           softmax_scale, op, ld_out, ld_oh, lp, ld_lse, wp, wb)
+
+
+def idx_build_tables(cached_lens, new_lens, free_blocks, block_table, block_size, ctx_lens, cu_rows, positions,
+                     slot_mapping, held_pages=None, held_out=None, free_start=None, free_end=None, cu_ctx=None,
+                     row_to_req=None, row_ke=None, stream=None):
+    """Block tables, slots and positions of a step's new tokens, from lengths.
+
+    cached_lens, new_lens, ctx_lens int32 [B], held_pages, held_out int32 [B] or None, free_blocks int32 [n],
+    free_start, free_end int32 [1] or None, block_table int32 [B, pages] (updated), cu_rows int32 [B + 1], cu_ctx int32
+    [B + 1] or None, positions int32 [rows], slot_mapping int64 [rows], row_to_req, row_ke int32 [rows] or None. ctx_lens
+    may be cached_lens, held_out held_pages and free_end free_start.
+    """
+    fn = "idx_build_tables"
+    dev = _cuda_device(fn, "cached_lens", cached_lens)
+    i32 = torch.int32
+    B, n_rows, n_free = cached_lens.shape[0], positions.shape[0], free_blocks.shape[0]
+    bt, ld_bt = _mat(fn, "block_table", block_table, dev, i32, B, None)
+    _call(fn, dev, stream, _vec(fn, "cached_lens", cached_lens, dev, i32, B), _vec(fn, "new_lens", new_lens, dev, i32, B),
+          None if held_pages is None else _vec(fn, "held_pages", held_pages, dev, i32, B), B,
+          _vec(fn, "free_blocks", free_blocks, dev, i32, n_free), _int32(fn, "free_blocks' length", n_free),
+          None if free_start is None else _vec(fn, "free_start", free_start, dev, i32, 1), bt, ld_bt,
+          block_table.shape[1], block_size, _vec(fn, "ctx_lens", ctx_lens, dev, i32, B),
+          _vec(fn, "cu_rows", cu_rows, dev, i32, B + 1),
+          None if cu_ctx is None else _vec(fn, "cu_ctx", cu_ctx, dev, i32, B + 1),
+          None if held_out is None else _vec(fn, "held_out", held_out, dev, i32, B),
+          None if free_end is None else _vec(fn, "free_end", free_end, dev, i32, 1),
+          _vec(fn, "positions", positions, dev, i32, n_rows),
+          _vec(fn, "slot_mapping", slot_mapping, dev, torch.int64, n_rows),
+          None if row_to_req is None else _vec(fn, "row_to_req", row_to_req, dev, i32, n_rows),
+          None if row_ke is None else _vec(fn, "row_ke", row_ke, dev, i32, n_rows), _int32(fn, "rows", n_rows))
+
+
+def idx_tree_mask(parents, cu_rows, mask, base_lens=None, positions=None, stream=None):
+    """The ancestors of every node of drafted trees, as bits, and the nodes' positions.
+
+    parents int32 [rows] (within the request, -1: none), cu_rows int32 [B + 1], mask int32 [rows, words], base_lens
+    int32 [B] or None, positions int32 [rows] or None.
+    """
+    fn = "idx_tree_mask"
+    dev = _cuda_device(fn, "parents", parents)
+    n, B = parents.shape[0], cu_rows.shape[0] - 1
+    if B < 0:
+        raise ValueError(f"{fn}: cu_rows is empty")
+    mp, ld_mask = _mat(fn, "mask", mask, dev, torch.int32, n, None)
+    _call(fn, dev, stream, _vec(fn, "parents", parents, dev, torch.int32, n),
+          _vec(fn, "cu_rows", cu_rows, dev, torch.int32, B + 1), _int32(fn, "requests", B), _int32(fn, "rows", n),
+          None if base_lens is None else _vec(fn, "base_lens", base_lens, dev, torch.int32, B), mp, ld_mask, mask.shape[1],
+          None if positions is None else _vec(fn, "positions", positions, dev, torch.int32, n))
+
+
+def idx_paged_attention_workspace_bytes(rows: int, requests: int, heads: int) -> int:
+    """Bytes of the workspace with which the window and tree attention split these rows' contexts (0: they would not)."""
+    fn = "idx_paged_attention_workspace_bytes"
+    return library().idx_paged_attention_workspace_bytes(
+        _int32(fn, "rows", rows), _int32(fn, "requests", requests), _int32(fn, "heads", heads))
+
+
+def _paged_attention(fn, q, cache, block_size, block_table, cu_rows, ctx_lens, seen, out, softmax_scale, lse, ws, stream):
+    dev = _cuda_device(fn, "q", q)
+    qp, ld_q, ld_qh = _heads(fn, "q", q, dev, None, None, 576)
+    T, H, _ = q.shape
+    op, ld_out, ld_oh = _heads(fn, "out", out, dev, T, H, 512)
+    bt, ld_bt = _mat(fn, "block_table", block_table, dev, torch.int32, None, None)
+    B, pages = block_table.shape
+    wp, wb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"{fn}: ws must be a contiguous tensor on cuda:{dev}")
+        wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
+    lp, ld_lse = (None, 0) if lse is None else _mat(fn, "lse", lse, dev, torch.float32, T, H)
+    cp, blocks, bs, stride = _cache_args(fn, cache, dev, block_size, 644)
+    _call(fn, dev, stream, qp, ld_q, ld_qh, cp, blocks, bs, stride, bt, ld_bt, pages,
+          _vec(fn, "cu_rows", cu_rows, dev, torch.int32, B + 1), _vec(fn, "ctx_lens", ctx_lens, dev, torch.int32, B), B,
+          *seen(dev, T), T, H, softmax_scale, op, ld_out, ld_oh, lp, ld_lse, wp, wb)
+
+
+def idx_window_attention(q, cache, block_size, block_table, cu_rows, ctx_lens, out, softmax_scale, window, sinks=0,
+                         lse=None, ws=None, stream=None):
+    """Causal attention of the last tokens of each request within a sliding window and over its first ``sinks`` tokens.
+
+    q bf16 [T, H, 576] (rows packed by cu_rows int32 [B + 1]), cache uint8 [num_blocks, block_stride] (644 bytes per
+    token), block_table int32 [B, pages], ctx_lens int32 [B] (the new tokens among them), out bf16 [T, H, 512], lse fp32
+    [T, H] or None, ws: a contiguous tensor of idx_paged_attention_workspace_bytes(T, B, H) bytes, or None.
+    """
+    fn = "idx_window_attention"
+    # a window or a number of first tokens beyond 32 bits is one beyond every context
+    seen = (max(min(window, _MAX_EXTENT), -1), max(min(sinks, _MAX_EXTENT), -1))
+    _paged_attention(fn, q, cache, block_size, block_table, cu_rows, ctx_lens, lambda dev, T: seen, out, softmax_scale,
+                     lse, ws, stream)
+
+
+def idx_tree_attention(q, cache, block_size, block_table, cu_rows, ctx_lens, mask, out, softmax_scale, lse=None, ws=None,
+                       stream=None):
+    """Attention of drafted tokens over the earlier tokens of their request and their ancestors in the tree.
+
+    mask int32 [T, words] (idx_tree_mask); the rest as idx_window_attention.
+    """
+    fn = "idx_tree_attention"
+    _paged_attention(fn, q, cache, block_size, block_table, cu_rows, ctx_lens,
+                     lambda dev, T: (*_mat(fn, "mask", mask, dev, torch.int32, T, None), mask.shape[1]), out,
+                     softmax_scale, lse, ws, stream)
 
 
 def idx_block_span(block_stride: int, token_stride: int) -> int:

@@ -159,7 +159,11 @@ idx_status_t idx_device_error(cudaStream_t stream) {
   if (e != cudaSuccess) return idx::fail(IDX_ERR_CUDA, "idx_device_error: %s", cudaGetErrorString(e));
   unsigned int h = idx::attention_read_and_clear_error(stream, &e);
   if (e != cudaSuccess) return idx::fail(IDX_ERR_CUDA, "idx_device_error: %s", cudaGetErrorString(e));
-  if (a || b || c || d || f || g || h) {
+  unsigned int i = idx::paged_attention_read_and_clear_error(stream, &e);
+  if (e != cudaSuccess) return idx::fail(IDX_ERR_CUDA, "idx_device_error: %s", cudaGetErrorString(e));
+  unsigned int j = idx::tables_read_and_clear_error(stream, &e);
+  if (e != cudaSuccess) return idx::fail(IDX_ERR_CUDA, "idx_device_error: %s", cudaGetErrorString(e));
+  if (a || b || c || d || f || g || h || i || j) {
     return idx::fail(IDX_ERR_DEVICE,
                      "device error flags: logits 0x%08x (bit w: wait site w expired; first: site %lld "
                      "block %lld tile-ordinal %lld group %lld tile %lld barrier %lld parity %lld), "
@@ -168,8 +172,11 @@ idx_status_t idx_device_error(cudaStream_t stream) {
                      "top-k 0x%08x (2 = a fused slot beyond int32), diagnostics 0x%08x (1 = a wait "
                      "for the tensor core expired), cache inserts and read-back 0x%08x (1 = a position "
                      "outside the cos/sin table, 2 = a page outside the cache), attention 0x%08x (1 = a slot "
-                     "outside the cache, 2 = a wait expired)",
-                     a, info[0], info[1], info[2], info[3], info[4], info[5], info[6], b, c, d, f, g, h);
+                     "outside the cache, 2 = a wait expired), window and tree attention 0x%08x (1 = a page outside "
+                     "the table or the cache, 2 = a wait expired), tables 0x%08x (1 = a length, page count or "
+                     "free_start out of range, 2 = free blocks ran out, 4 = a context beyond the table, 8 = more "
+                     "rows than n_rows, 16 = a tree's parent, or a node without a bit)",
+                     a, info[0], info[1], info[2], info[3], info[4], info[5], info[6], b, c, d, f, g, h, i, j);
   }
   return IDX_OK;
 }

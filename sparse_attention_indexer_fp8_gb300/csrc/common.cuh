@@ -42,6 +42,8 @@ unsigned int topk_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
 unsigned int diag_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
 unsigned int kv_cache_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
 unsigned int attention_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
+unsigned int paged_attention_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
+unsigned int tables_read_and_clear_error(cudaStream_t stream, cudaError_t* err);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
