@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "attention_mma.cuh"
 #include "common.cuh"
 #include "kv_layout.cuh"
 
@@ -89,7 +90,6 @@ struct AttnParams {
 constexpr int kHeadsPerBlock = 64;
 constexpr int kTile = 64;
 constexpr int kPieces = kKvDim / 64;             // 128-byte pieces of a token's bf16 row
-constexpr int kPieceBytes = 64 * 128;            // one piece of 64 rows
 constexpr int kQBytes = kPieces * kPieceBytes;
 constexpr int kStageBytes = kPieces * kPieceBytes;
 constexpr int kStages = 2;
@@ -128,95 +128,6 @@ struct Shared {
 constexpr int kSmemBytes = kQBytes + kStages * kStageBytes + kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
 static_assert(kSmemBytes <= 232448, "shared memory of one block");
 
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_n_major) {
-  // D fp32 (bits 4-5), A and B bf16 (7-9, 10-12), B's major (16), N >> 3 (17-22), M >> 4 (24-28)
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_major ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// N-major operand of 64-element (128-byte) swizzled rows: rows of the K dimension
-// 128 bytes apart, the next 8 of them 1024 bytes on (stride offset), the next 64
-// elements of N a piece on (leading offset).
-__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kPieceBytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// Issued by the lane with `issue` set; the whole warp passes here converged, so the descriptors stay in
-// uniform registers (N = 64 products then go out every 32 clocks; issued from a branch of one
-// lane, every 45 to 56).
-__device__ __forceinline__ void mma_ws_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
-                                            uint32_t issue) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(acc), "r"(issue)
-      : "memory");
-}
-
-// The same with A in tensor memory: row r in lanes r and 64 + r, two elements of K a column.
-__device__ __forceinline__ void mma_ws_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
-                                               uint32_t issue) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(acc), "r"(issue)
-      : "memory");
-}
-
-// Arrives on the barrier once everything issued so far is complete.
-__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t issue) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(issue)
-      : "memory");
-}
-
-// Sixteen columns of the thread's lane, read (valid after the wait inside) or written.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-
-// One look at a barrier, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // Bounded wait. A wait that takes two seconds marks the block dead and raises the device
 // flag; from then on no wait blocks, every role runs its remaining iterations on whatever it
 // finds (all addresses stay in bounds), and the block ends in order.
@@ -233,53 +144,12 @@ __device__ __forceinline__ void wait_bar(Shared& sh, uint64_t* bar, uint32_t par
   __syncwarp();
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 2, %0;" ::"n"(kMmaWarp * 32) : "memory"); }
 
 // The softmax warps and the matrix warp: tensor memory is there (and every row of Q copied).
 __device__ __forceinline__ void tmem_bar() { asm volatile("bar.sync 3, 160;" ::: "memory"); }
 
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// 16 bytes of global memory into shared memory, asynchronously; zeros where `ok` is false.
-__device__ __forceinline__ void copy16_if(uint32_t dst, const uint8_t* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-
-// 8 bytes of the cache, or zeros. Volatile: the load is issued where it stands, a tile ahead of its use.
-__device__ __forceinline__ uint2 load8_if(const uint8_t* ptr, bool ok) {
-  uint2 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y)
-      : "l"(ptr), "r"(static_cast<int>(ok)));
-  return v;
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
-
-__device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* ptr, int lane) {
-  return reinterpret_cast<const uint8_t*>(
-      __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(ptr), lane));
-}
 
 // Where the token of a list entry lies; all null for an entry that does not count.
 struct Token {

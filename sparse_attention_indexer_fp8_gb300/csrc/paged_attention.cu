@@ -1,178 +1,151 @@
 // Attention over whole contexts of the paged attention cache: within a sliding
 // window and over a few first tokens (idx_window_attention), and of trees of drafted
 // tokens (idx_tree_attention).
-#include <cuda_bf16.h>
-
 #include <algorithm>
 #include <cmath>
 
-#include "common.cuh"
-#include "kv_layout.cuh"
+#include "paged_attention.cuh"
+#include "paged_block.cuh"
 
 namespace idx {
 namespace {
 
-// Bit 0: a visible page outside the table or the cache (its tokens are skipped). Bit 1: a wait expired.
-__device__ unsigned int g_paged_error = 0;
+// Joins the parts of each (row, head): weights 2^(m_i - max m), a part without a visible token skipped (its
+// accumulators were never written). A head is the work of kWarps warps, each of which takes every kWarps-th
+// part, two at a time: all heads of a batch run at once, and the loads of two parts are in flight together. Rows
+// whose context was not split are complete already.
+constexpr int kJoinWarps = 8;   // of a block
+constexpr int kMaxParts = 160;
+constexpr int kPartRows = block::kRows;
 
-struct PagedParams {
-  const __nv_bfloat16* q;
-  int64_t ld_q, ld_qh;  // elements between rows, between heads
-  const uint8_t* cache;
-  int num_blocks, block_size;
-  int64_t block_stride;
-  const int32_t* block_table;
-  int64_t ld_bt;
-  int n_pages;
-  const int32_t* cu_rows;
-  const int32_t* ctx_lens;
-  int B;
-  int window, sinks;     // of the window attention
-  const int32_t* mask;   // of the tree attention
-  int64_t ld_mask;
-  int words;
-  int T, H;
-  float scale_log2;  // softmax_scale * log2(e)
-  __nv_bfloat16* out;
-  int64_t ld_out, ld_oh;
-  float* lse;
-  int64_t ld_lse;
-};
-
-// ---------------------------------------------------------------------------
-// One block per row and group of eight heads: tiles of 32 tokens dequantised into shared memory, a thread per
-// (head, token) for the logits, two dims of every head a thread for the sums.
-// ---------------------------------------------------------------------------
-constexpr int kHeadsPerBlock = 8;
-constexpr int kTile = 32;
-constexpr int kThreads = 256;
-constexpr int kPitch = kKvDim + 1;
-
-struct Shared {
-  float q[kHeadsPerBlock][kKvDim];
-  float k[kTile][kPitch];
-  float p[kHeadsPerBlock][kTile];
-  int see[kTile];
-};
-
-template <bool kTree>
-__global__ void __launch_bounds__(kThreads) paged_attention_kernel(const PagedParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x, h0 = blockIdx.y * kHeadsPerBlock;
-  int lo = 0, hi = p.B;
+template <int kWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedParams p) {
+  constexpr int kHeads = kJoinWarps / kWarps;  // of a block
+  __shared__ float4 sums[kHeads][kWarps > 1 ? kWarps - 1 : 1][kKvLatent / 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp / kWarps, g = warp % kWarps;
+  const uint32_t heads = static_cast<uint32_t>(p.H), head = blockIdx.x * kHeads + sub;
+  bool have = head < static_cast<uint32_t>(p.T) * heads;
+  const int row = have ? static_cast<int>(head / heads) : 0, h = have ? static_cast<int>(head % heads) : 0;
+  int lo = 0, hi = p.B;  // the last b with cu_rows[b] <= row
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu_rows + mid) <= row) lo = mid; else hi = mid;
+    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+    const bool before = b < hi && (lane == 0 || row_at(p, b) <= row);
+    lo += (__popc(__ballot_sync(0xFFFFFFFFu, before)) - 1) * step;
+    hi = min(lo + step, hi);
   }
-  const int b = lo, first = __ldg(p.cu_rows + b), end = __ldg(p.cu_rows + b + 1);
-  if (row < first || row >= end) return;
-  const int64_t ctx = __ldg(p.ctx_lens + b), base = ctx - (end - first), pos = base + (row - first);
-  // tokens [0, a) and [c, d) may be seen
-  int64_t a, c, d;
-  if (kTree) {
-    a = 0, c = 0, d = ctx;
-  } else {
-    d = pos + 1;
-    c = max(pos - p.window + 1, int64_t{0});
-    a = min(static_cast<int64_t>(p.sinks), min(c, d));
-  }
-  for (int i = tid; i < kHeadsPerBlock * kKvDim; i += kThreads) {
-    const int h = h0 + i / kKvDim;
-    sh.q[i / kKvDim][i % kKvDim] =
-        h < p.H ? __bfloat162float(p.q[row * p.ld_q + h * p.ld_qh + i % kKvDim]) * p.scale_log2 : 0.f;
-  }
-  float m = -INFINITY, l = 0.f;  // of head `warp`
-  float acc[kHeadsPerBlock][2] = {};
-  const int64_t n = a + max(d - c, int64_t{0});
-  for (int64_t t0 = 0; t0 < n; t0 += kTile) {
-    __syncthreads();
-    for (int t = warp; t < kTile; t += kThreads / 32) {
-      const int64_t i = t0 + t, j = i < a ? i : c + i - a;
-      bool see = i < n;
-      if (kTree && see && j >= base) {
-        const int64_t node = j - base;
-        see = node < 32 * p.words && (__ldg(p.mask + row * p.ld_mask + node / 32) >> (node % 32) & 1);
+  const int at = row_at(p, lo), n = row_at(p, lo + 1) - at, in = row - at;
+  have = have && in >= 0 && in < n;
+  const int units = (n + p.tokens - 1) / p.tokens * p.head_blocks;
+  const int unit = in / p.tokens * p.head_blocks + h / p.heads;
+  const int r = in % p.tokens * p.heads + h % p.heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // every part is complete and visible
+  const int2 sched = have ? __ldcg(p.ws_sched + lo) : make_int2(0, 1);
+  const int parts = min(sched.y, kMaxParts);
+  have = have && parts > 1;
+  const int64_t step = static_cast<int64_t>(units) * kPartRows;
+  const float2* ml = p.ws_ml + static_cast<int64_t>(sched.x + unit) * kPartRows + r;  // of part i: ml[step * i]
+  const float4* o = reinterpret_cast<const float4*>(p.ws_o + (static_cast<int64_t>(sched.x + unit) * kPartRows + r) * kKvLatent) + lane;
+
+  float4 acc[4] = {};
+  float m = -INFINITY, l = 0.f;
+  if (have) {
+    float2 mine[kMaxParts / 32];
+#pragma unroll
+    for (int c = 0; c < kMaxParts / 32; ++c) {
+      mine[c] = 32 * c + lane < parts ? __ldcg(ml + (32 * c + lane) * step) : make_float2(-INFINITY, 0.f);
+      m = fmaxf(m, mine[c].x);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+#pragma unroll
+    for (int c = 0; c < kMaxParts / 32; ++c) {
+      if (mine[c].y != 0.f) l = fmaf(exp2f(mine[c].x - m), mine[c].y, l);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    for (int i = g; i < parts; i += 2 * kWarps) {
+      float2 x[2];
+      float4 v[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int part = i + j * kWarps;
+        x[j] = make_float2(-INFINITY, 0.f);
+        if (part >= parts) continue;
+        x[j] = __ldcg(ml + part * step);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[j][c] = __ldcg(o + part * step * (kKvLatent / 4) + 32 * c);
       }
-      int blk = -1;
-      if (see) {
-        const int64_t page = j / p.block_size;
-        if (page < p.n_pages) blk = __ldg(p.block_table + b * p.ld_bt + page);
-        if (blk < 0 || blk >= p.num_blocks) {
-          see = false;
-          if (lane == 0) atomicOr(&g_paged_error, 1u);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (x[j].y == 0.f) continue;
+        const float w = exp2f(x[j].x - m);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[c].x = fmaf(w, v[j][c].x, acc[c].x);
+          acc[c].y = fmaf(w, v[j][c].y, acc[c].y);
+          acc[c].z = fmaf(w, v[j][c].z, acc[c].z);
+          acc[c].w = fmaf(w, v[j][c].w, acc[c].w);
         }
       }
-      if (lane == 0) sh.see[t] = see;
-      if (!see) {
-        for (int x = lane; x < kKvDim; x += 32) sh.k[t][x] = 0.f;
-        continue;
-      }
-      const int off = static_cast<int>(j % p.block_size);
-      const uint8_t* base_ptr = p.cache + blk * p.block_stride;
-      const uint32_t* lat = reinterpret_cast<const uint32_t*>(base_ptr + off * kKvLatent);
-      const uint32_t codes = *reinterpret_cast<const uint32_t*>(base_ptr + p.block_size * kKvScaleAt + 4 * off);
-      const uint32_t* pe = reinterpret_cast<const uint32_t*>(base_ptr + p.block_size * kKvRopeAt + off * (2 * kKvRope));
+    }
+  }
+  if constexpr (kWarps > 1) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t w[2];
-        kv_dequant4(lat[32 * x + lane], kv_dequant_multiplier((codes >> (8 * x)) & 0xFFu), w[0], w[1]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          sh.k[t][128 * x + 4 * lane + y] = __uint_as_float(y & 1 ? w[y / 2] & 0xFFFF0000u : w[y / 2] << 16);
-        }
-      }
-      const uint32_t w = pe[lane];
-      sh.k[t][kKvLatent + 2 * lane] = __uint_as_float(w << 16);
-      sh.k[t][kKvLatent + 2 * lane + 1] = __uint_as_float(w & 0xFFFF0000u);
+    for (int c = 0; c < 4; ++c) {
+      if (g > 0) sums[sub][g - 1][lane + 32 * c] = acc[c];
     }
     __syncthreads();
-    float s = 0.f;
-    for (int x = 0; x < kKvDim; ++x) s = fmaf(sh.q[warp][x], sh.k[lane][x], s);
-    if (!sh.see[lane]) s = -INFINITY;
-    float top = s;
+    if (g > 0) return;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float m_new = fmaxf(m, top), ref = m_new == -INFINITY ? 0.f : m_new;
-    const float f = exp2f(m - ref), e = exp2f(s - ref);
-    m = m_new;
-    float sum = e;
+    for (int i = 0; i < kWarps - 1; ++i) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    l = l * f + sum;
-    sh.p[warp][lane] = e;
-    __shared__ float scale[kHeadsPerBlock];
-    if (lane == 0) scale[warp] = f;
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < kHeadsPerBlock; ++h) {
-      acc[h][0] *= scale[h];
-      acc[h][1] *= scale[h];
-    }
-    for (int t = 0; t < kTile; ++t) {
-      if (!sh.see[t]) continue;
-      const float v0 = sh.k[t][2 * tid], v1 = sh.k[t][2 * tid + 1];
-#pragma unroll
-      for (int h = 0; h < kHeadsPerBlock; ++h) {
-        acc[h][0] = fmaf(sh.p[h][t], v0, acc[h][0]);
-        acc[h][1] = fmaf(sh.p[h][t], v1, acc[h][1]);
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = sums[sub][i][lane + 32 * c];
+        acc[c].x += v.x;
+        acc[c].y += v.y;
+        acc[c].z += v.z;
+        acc[c].w += v.w;
       }
     }
   }
-  __shared__ float total[kHeadsPerBlock];
-  if (lane == 0) {
-    total[warp] = l;
-    if (p.lse && h0 + warp < p.H) {
-      p.lse[row * p.ld_lse + h0 + warp] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-    }
+  if (!have) return;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  __nv_bfloat16* dst = p.out + row * p.ld_out + h * p.ld_oh + 4 * lane;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+    *reinterpret_cast<uint2*>(dst + 128 * c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
-  __syncthreads();
-  for (int h = 0; h < kHeadsPerBlock && h0 + h < p.H; ++h) {
-    const float inv = total[h] == 0.f ? 0.f : 1.0f / total[h];
-    *reinterpret_cast<__nv_bfloat162*>(p.out + row * p.ld_out + (h0 + h) * p.ld_oh + 2 * tid) =
-        __floats2bfloat162_rn(acc[h][0] * inv, acc[h][1] * inv);
+  if (p.lse && lane == 0) {
+    p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
+}
+
+// How a call's rows are cut into units, and whether their contexts are split: where one wave of blocks has room for
+// more than the units.
+struct Plan {
+  int head_blocks, heads, tokens, capacity;
+  int64_t blocks;
+};
+
+Plan plan_of(int32_t T, int32_t B, int32_t H, int sms) {
+  Plan plan{};
+  plan.head_blocks = (H + block::kRows - 1) / block::kRows;
+  plan.heads = (H + plan.head_blocks - 1) / plan.head_blocks;
+  plan.tokens = block::kRows / plan.heads;
+  const int64_t groups = T / plan.tokens + static_cast<int64_t>(B);
+  plan.blocks = groups * plan.head_blocks;
+  // no more groups hold rows: each request's last one may be part-filled
+  const int64_t filled = std::min<int64_t>(T, groups) * plan.head_blocks;
+  plan.capacity = sms > 0 && filled < sms && B <= kMaxSplitRequests ? sms : 0;
+  return plan;
+}
+
+int64_t plan_bytes(const Plan& plan, int32_t B) {
+  const int64_t head = (static_cast<int64_t>(B) * sizeof(int2) + 15) / 16 * 16;
+  return plan.capacity ? head + plan.capacity * static_cast<int64_t>(kPartRows) * (kKvLatent * 4 + 8) : 0;
 }
 
 // What both calls check and launch; `p` holds what they were given.
@@ -196,12 +169,55 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
     return fail(IDX_ERR_UNSUPPORTED, "%s: q and out rows must be 16-byte aligned", fn);
   }
   if (ws && !aligned(ws, 16)) return fail(IDX_ERR_UNSUPPORTED, "%s: the workspace is not 16-byte aligned", fn);
-  (void)ws_bytes;
-  auto* kernel = tree ? paged_attention_kernel<true> : paged_attention_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+  const int sms = device_sm_count();
+  if (sms <= 0) return fail(IDX_ERR_CUDA, "%s: cannot query the SM count", fn);
+  const Plan plan = plan_of(p.T, p.B, p.H, sms);
+  if (plan.blocks > INT32_MAX || static_cast<int64_t>(p.T) * p.H > INT32_MAX) {
+    return fail(IDX_ERR_UNSUPPORTED, "%s: %d rows of %d heads in %d requests", fn, p.T, p.H, p.B);
+  }
+  p.page_shift = p.block_size == 16 ? 4 : p.block_size == 32 ? 5 : p.block_size == 64 ? 6 : 7;
+  p.head_blocks = plan.head_blocks;
+  p.heads = plan.heads;
+  p.tokens = plan.tokens;
+  p.capacity = ws ? plan.capacity : 0;
+  if (p.capacity) {
+    const int64_t need = plan_bytes(plan, p.B);
+    if (ws_bytes < static_cast<size_t>(need)) {
+      return fail(IDX_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %lld are needed", fn, ws_bytes,
+                  static_cast<long long>(need));
+    }
+    p.ws_sched = static_cast<int2*>(ws);
+    p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (static_cast<int64_t>(p.B) * sizeof(int2) + 15) / 16 * 16);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + p.capacity * static_cast<int64_t>(kPartRows) * kKvLatent);
+  }
+  auto* kernel = tree ? block::paged_block_kernel<true> : block::paged_block_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block::kSmemBytes);
   if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-  const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>((p.H + kHeadsPerBlock - 1) / kHeadsPerBlock));
-  kernel<<<grid, kThreads, sizeof(Shared), stream>>>(p);
+  const unsigned grid = static_cast<unsigned>(p.capacity ? p.capacity : plan.blocks);
+  kernel<<<grid, block::kThreads, block::kSmemBytes, stream>>>(p);
+  const idx_status_t launched = check_launch(fn);
+  if (launched != IDX_OK || !p.capacity) return launched;
+  // Launched while the parts run: its blocks wait at their first reads for the parts' end. The host knows the most
+  // parts that a row can have.
+  const int64_t least = static_cast<int64_t>(p.head_blocks);  // units of a request
+  const int most = static_cast<int>(std::min<int64_t>(p.capacity / least, kMaxParts));
+  const int warps = most <= 4 ? 1 : most <= 8 ? 2 : most <= 16 ? 4 : 8;
+  auto* join = warps == 1 ? paged_join_kernel<1> : warps == 2 ? paged_join_kernel<2> : warps == 4 ? paged_join_kernel<4> : paged_join_kernel<8>;
+  const int heads = kJoinWarps / warps;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.T) * p.H + heads - 1) / heads));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t ej = cudaLaunchKernelEx(&cfg, join, static_cast<const PagedParams>(p));
+  if (ej != cudaSuccess) {
+    cudaGetLastError();
+    return fail(IDX_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(ej));
+  }
   return check_launch(fn);
 }
 
@@ -223,10 +239,8 @@ unsigned int paged_attention_read_and_clear_error(cudaStream_t stream, cudaError
 using namespace idx;
 
 extern "C" size_t idx_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H) {
-  (void)T;
-  (void)B;
-  (void)H;
-  return 0;
+  if (T <= 0 || B <= 0 || H <= 0 || H > IDX_ATTENTION_MAX_HEADS) return 0;
+  return static_cast<size_t>(plan_bytes(plan_of(T, B, H, device_sm_count()), B));
 }
 
 extern "C" idx_status_t idx_window_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache,

@@ -1,0 +1,594 @@
+// Window and tree attention of few rows a request: one block per unit of up to 64 query rows (a row is one
+// head of one token), all 512 dims of the values.
+#pragma once
+
+#include "paged_attention.cuh"
+
+namespace idx {
+namespace block {
+
+// ---------------------------------------------------------------------------
+// Per tile of 64 tokens
+//   S = Q K^T   64 rows x 64 tokens, 36 steps of K = 16 over the 576 dims
+//   P = exp2(S * scale - m)    the running maximum m of each row in registers
+//   O += P V    64 rows x 512 dims, 4 steps of K = 16 over the 64 tokens, two halves of N = 256
+// with tcgen05.mma.ws (M = 64) in bf16 x bf16 -> fp32, the form and the roles of the sparse attention: warps 4-19
+// load and dequantise the tokens' latents, warps 21-22 copy their position dims and prefetch, warp 20 issues the
+// matrix instructions, warps 0-3 load Q and do the softmax; all but 20-22 store the result. Keys and values are one
+// copy in shared memory: a token is a row of nine 128-byte swizzled pieces (64 dims each), read along the dims as the
+// K-major B operand of S and along the tokens as the N-major one of O. Two groups of eight loader warps own a stage
+// each, and hold the next tile in registers.
+//
+// What differs: tokens lie in pages, so eight of a warp share one block and one address; rows of several
+// query tokens see different tokens, so each thread of the softmax has its own mask of a tile; and parts of a
+// context are found on the device from the lengths, which the host does not know.
+// ---------------------------------------------------------------------------
+constexpr int kRows = 64;                        // of a unit
+constexpr int kQBytes = kPieces * kPieceBytes;
+constexpr int kStageBytes = kPieces * kPieceBytes;
+constexpr int kStages = 2;
+constexpr int kLoaderWarps = 16;
+constexpr int kGroupWarps = kLoaderWarps / kStages;  // each stage has its own group of loader warps
+constexpr int kTokensPerWarp = kTile / kGroupWarps;
+static_assert(kTokensPerWarp == 8, "a loader warp's tokens are eight rows of the swizzle, within one page");
+constexpr int kEarly = 3;  // of a warp's tokens, those converted while the stage is still in use
+constexpr int kMmaWarp = 4 + kLoaderWarps;
+constexpr int kRopeWarp = kMmaWarp + 1;          // one per stage
+constexpr int kThreads = (kRopeWarp + kStages) * 32;
+constexpr int kRing = 4;
+constexpr int kOCols = 256;                      // tensor-memory columns of O; S0 and S1 (32 each) follow
+constexpr int kQCols = 320;                      // and the first kQTmemPieces pieces of Q
+constexpr int kQTmemPieces = 6;
+constexpr int kTmemCols = 512;
+static_assert(kQCols + kQTmemPieces * 32 <= kTmemCols, "tensor memory of one block");
+
+struct Shared {
+  uint64_t q_full, drained;
+  uint64_t k_full[kStages];                      // a stage's tokens are stored
+  uint64_t s_full[kStages];                      // S of the tile is complete
+  uint64_t p_full[kStages];                      // P is stored
+  uint64_t o_done[kStages];                      // the tile's share of O is complete: P and the stage are free
+  uint64_t flags[kRing];                         // `valid` and `poison` are written
+  uint32_t tmem;
+  volatile uint32_t dead;                        // a wait expired: no further wait blocks
+  uint32_t valid[kRing][2];                      // bit t: token t of the tile is there
+  uint32_t poison[kRing][2];                     // bit t: and not finite
+  float xchg[2][128];
+  float inv[kRows];                              // 1 / sum of each row
+};
+
+constexpr int kSmemBytes = kQBytes + kStages * kStageBytes + kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
+static_assert(kSmemBytes <= 232448, "shared memory of one block");
+
+__device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 2, %0;" ::"n"(kMmaWarp * 32) : "memory"); }
+
+// The softmax warps and the matrix warp: tensor memory is there (and every row of Q copied).
+__device__ __forceinline__ void tmem_bar() { asm volatile("bar.sync 3, 160;" ::: "memory"); }
+
+__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <bool kTree>
+__global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* q_s = smem;
+  uint8_t* k_s = q_s + kQBytes;
+  uint8_t* p_s = k_s + kStages * kStageBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(p_s + kPieceBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (p.capacity) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
+  Unit u;
+  if (!find_unit<kTree, 1>(p, blockIdx.x, u)) return;
+  const int tiles = u.tiles;
+  const bool split = u.parts > 1;
+  // query row r of the unit: head r % heads of token r / heads
+  auto q_row_of = [&](int r) { return r / p.heads; };
+
+  if (tiles == 0) {
+    if (split) {
+      if (tid < kRows) p.ws_ml[static_cast<int64_t>(u.part) * kRows + tid] = make_float2(-INFINITY, 0.f);
+    } else {
+      for (int i = tid; i < u.rows * u.heads * (kKvLatent / 8); i += kThreads) {
+        const int r = i / (kKvLatent / 8);
+        *reinterpret_cast<uint4*>(p.out + (u.row0 + r / u.heads) * p.ld_out + (u.head0 + r % u.heads) * p.ld_oh +
+                                  8 * (i % (kKvLatent / 8))) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (p.lse && tid < u.rows * u.heads) p.lse[(u.row0 + tid / u.heads) * p.ld_lse + u.head0 + tid % u.heads] = -INFINITY;
+    }
+    return;
+  }
+
+  // Barriers and tensor memory are set up by the matrix warp; every role first does what needs neither.
+  uint32_t tmem = 0;
+  auto setup = [&]() {
+    tc_fence_before();
+    __syncwarp();
+    asm volatile("bar.sync 0;" ::: "memory");
+    tc_fence_after();
+    tmem = sh.tmem;
+  };
+
+  if (warp >= 4 && warp < kMmaWarp) {
+    // ---------------------------------------------------------------- loaders
+    const int group = (warp - 4) / kGroupWarps, lw = (warp - 4) % kGroupWarps;  // this group's tiles: group, group + 2, ...
+    const int r0 = kTokensPerWarp * lw;  // the warp's first token of a tile
+    // Lane l stores unit l % 8 of piece l / 8 and of piece 4 + l / 8: it holds the eight dims of either half
+    // that the swizzle puts there. So the loads' addresses depend on the row, and the stores', which
+    // would take registers, do not.
+    uint2 raw[kTokensPerWarp][2];
+    // A tile's block is looked up one tile of the group before its tokens are loaded, and they two before their
+    // conversion: nothing between two tiles' loads waits for an address.
+    uint32_t mults = 0, next_codes = 0, found_codes = 0;
+    uint32_t there = 0;  // bit j: token j of the found tile is loaded
+    int next_block = -1;
+    const uint8_t* latent = nullptr;  // of the warp's first token
+    // of a lane's own token, lane % 8; the warp's tokens that a row sees share one block
+    auto lookup = [&](int tile) {
+      return tile < tiles ? block_of(p, u, tile_start(u, tile) + r0 + (lane & 7), false) : -1;
+    };
+    auto find = [&](int tile) {
+      there = __ballot_sync(0xFFFFFFFFu, next_block >= 0) & 0xFFu;
+      const int blk = there ? __shfl_sync(0xFFFFFFFFu, next_block, __ffs(there) - 1) : 0;
+      found_codes = 0;
+      if (there) {
+        const int off = (tile_start(u, tile) + r0) & (p.block_size - 1);
+        const uint8_t* base = p.cache + blk * p.block_stride;
+        latent = base + off * kKvLatent;
+        if (next_block >= 0) {
+          found_codes = __ldg(reinterpret_cast<const uint32_t*>(base + p.block_size * kKvScaleAt) + off + (lane & 7));
+        }
+      }
+      next_block = lookup(tile + kStages);
+    };
+    auto load = [&]() {
+#pragma unroll
+      for (int j = 0; j < kTokensPerWarp; ++j) {
+        const bool ok = (there >> j) & 1u;
+        raw[j][0] = load8_if(latent + kKvLatent * j + 8 * (lane ^ j), ok);  // r0 is a multiple of eight: row j of the swizzle
+        raw[j][1] = load8_if(latent + kKvLatent * j + 256 + 8 * (lane ^ j), ok);
+      }
+    };
+    // eight dims in half h of the token with these multipliers
+    auto word_of = [&](int j) { return __shfl_sync(0xFFFFFFFFu, mults, j); };
+    auto convert = [&](const uint2& x, uint32_t word, uint32_t h) {
+      const uint32_t mul = __byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)) * 0x00800080u;
+      uint4 w;
+      kv_dequant4_even_odd(x.x, mul, w.x, w.y);
+      kv_dequant4_even_odd(x.y, mul, w.z, w.w);
+      return w;
+    };
+    const uint32_t unit = smem_u32(k_s) + group * kStageBytes + (lane >> 3) * kPieceBytes + r0 * 128 + 16 * (lane & 7);
+
+    if (group < tiles) {
+      next_block = lookup(group);
+      find(group);
+      load();
+      next_codes = found_codes;
+      if (group + kStages < tiles) find(group + kStages);
+    }
+    setup();
+    for (int i = group; i < tiles; i += kStages) {
+      mults = multiplier_bytes(next_codes);
+      uint4 early[kEarly][2];
+#pragma unroll
+      for (int j = 0; j < kEarly; ++j) {
+        const uint32_t word = word_of(j);
+        early[j][0] = convert(raw[j][0], word, 0);
+        early[j][1] = convert(raw[j][1], word, 1);
+      }
+      if (i >= kStages) wait_for(sh, &sh.o_done[group], ((i >> 1) - 1) & 1);
+#pragma unroll
+      for (int j = 0; j < kTokensPerWarp; ++j) {
+        const uint32_t word = j < kEarly ? 0u : word_of(j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          st_shared16(unit + 4 * h * kPieceBytes + j * 128, j < kEarly ? early[j % kEarly][h] : convert(raw[j][h], word, h));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full[group]);
+      if (i + kStages < tiles) {
+        load();
+        next_codes = found_codes;
+        if (i + 2 * kStages < tiles) find(i + 2 * kStages);
+      }
+    }
+  } else if (warp >= kRopeWarp) {
+    // ---------------------------------------------------------------- position dims, and L2 prefetch
+    // Position dims are bf16 in the cache as in the tile: copied asynchronously, as soon as S of the tile
+    // before is complete. Lane l locates tokens l and 32 + l. The same warp says which tokens are there and finite, and
+    // brings the records of the tile kAhead further on into L2.
+    const int group = warp - kRopeWarp;
+    struct Token {
+      const uint8_t* rope;
+      const uint32_t* codes;
+    };
+    auto locate = [&](int tile, int h, bool report) {
+      Token t{nullptr, nullptr};
+      if (tile >= tiles) return t;
+      const int j = tile_start(u, tile) + 32 * h + lane;
+      const int blk = block_of(p, u, j, report);
+      if (blk < 0) return t;
+      const int off = j & (p.block_size - 1);
+      const uint8_t* base = p.cache + blk * p.block_stride;
+      t.rope = base + p.block_size * kKvRopeAt + off * (2 * kKvRope);
+      t.codes = reinterpret_cast<const uint32_t*>(base + p.block_size * kKvScaleAt) + off;
+      return t;
+    };
+    // 32 tokens: each lane's own position dims and codes, and 8 x 4 lines of latents an instruction
+    auto prefetch = [&](int tile, int h) {
+      if (tile >= tiles) return;
+      const int j = tile_start(u, tile) + 32 * h + lane;
+      const int blk = block_of(p, u, j, false);
+      const uint8_t* latent = nullptr;
+      if (blk >= 0) {
+        const int off = j & (p.block_size - 1);
+        const uint8_t* base = p.cache + blk * p.block_stride;
+        latent = base + off * kKvLatent;
+        prefetch_l2(base + p.block_size * kKvRopeAt + off * (2 * kKvRope));
+        if ((lane & 15) == 0) prefetch_l2(base + p.block_size * kKvScaleAt + 4 * off);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t* src = shfl_ptr(latent, 8 * k + (lane >> 2));
+        if (src) prefetch_l2(src + 128 * (lane & 3));
+      }
+      __syncwarp();
+    };
+    for (int i = group; i < kAhead && i < tiles; i += kStages) {
+      prefetch(i, 0);
+      prefetch(i, 1);
+    }
+    const uint32_t piece = smem_u32(k_s) + group * kStageBytes + (kPieces - 1) * kPieceBytes;
+    setup();
+    for (int i = group; i < tiles; i += kStages) {
+      const Token tok[2] = {locate(i, 0, true), locate(i, 1, true)};
+      uint32_t valid[2], poison[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        valid[h] = __ballot_sync(0xFFFFFFFFu, tok[h].rope != nullptr);
+        poison[h] = __ballot_sync(0xFFFFFFFFu, tok[h].rope != nullptr && !codes_finite(__ldg(tok[h].codes)));
+      }
+      // only S reads position dims, so their piece is free long before the stage is
+      if (i >= kStages) wait_for(sh, &sh.s_full[group], ((i >> 1) - 1) & 1);
+#pragma unroll
+      for (int c = 0; c < kTile / 4; ++c) {
+        const int t = 4 * c + (lane >> 3), x = lane & 7;
+        const uint8_t* from = shfl_ptr(tok[c / 8].rope, t & 31);
+        copy16_if(piece + t * 128 + ((x ^ (t & 7)) << 4), from ? from + 16 * x : p.cache, from != nullptr);
+      }
+      if (lane == 0) {
+        // S of tile i - 2, waited for above, was issued after O of tile i - 4, hence after entry i - 4 was read
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sh.valid[i % kRing][h] = valid[h];
+          sh.poison[i % kRing][h] = poison[h];
+        }
+        mbar_arrive(&sh.flags[i % kRing]);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full[group]);
+      prefetch(i + kAhead, 0);
+      prefetch(i + kAhead, 1);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      mbar_init(&sh.q_full, 4);
+      mbar_init(&sh.drained, 1);
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&sh.k_full[i], kGroupWarps + 1);
+        mbar_init(&sh.s_full[i], 1);
+        mbar_init(&sh.p_full[i], 4);
+        mbar_init(&sh.o_done[i], 1);
+      }
+      for (int i = 0; i < kRing; ++i) mbar_init(&sh.flags[i], 1);
+      sh.dead = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(&sh.tmem, kTmemCols);
+    tmem_relinquish();
+    tc_fence_before();
+    tmem_bar();
+    setup();
+    // ---------------------------------------------------------------- matrix instructions
+    // Whichever of the next S and the next O product has its operands goes first, O before S.
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(lead));
+    const uint64_t q_desc = sw128_kmajor_desc(smem_u32(q_s));
+    const uint64_t p_desc = sw128_kmajor_desc(smem_u32(p_s));
+    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(k_s));
+    const uint64_t v_desc = sw128_nmajor_desc(smem_u32(k_s));
+    wait_for(sh, &sh.q_full, 0);
+    tc_fence_after();
+    const int total = __shfl_sync(0xFFFFFFFFu, tiles, 0);
+    int s_next = 0, o_next = 0;
+    uint64_t t0 = global_timer_ns();
+    int idle = 0;
+    while (o_next < total) {
+      const bool can_o = o_next < s_next && mbar_test(&sh.p_full[o_next & 1], (o_next >> 1) & 1);
+      if (__all_sync(0xFFFFFFFFu, can_o)) {
+        tc_fence_after();
+        const int st = o_next & 1;
+        const uint64_t v = v_desc + st * (kStageBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            mma_ws_bf16(tmem + half * (kOCols / 2), p_desc + 2 * ks, v + ((4 * half * kPieceBytes + 2048 * ks) >> 4),
+                        idesc_bf16(64, 256, true), o_next > 0 || ks > 0, lead);
+          }
+        }
+        commit_if(&sh.o_done[st], lead);
+        ++o_next;
+        idle = 0;
+        continue;
+      }
+      const bool can_s = s_next < total && s_next - o_next < kStages &&
+                         mbar_test(&sh.k_full[s_next & 1], (s_next >> 1) & 1);
+      if (__all_sync(0xFFFFFFFFu, can_s)) {
+        tc_fence_after();
+        const int st = s_next & 1;
+        const uint64_t k = k_desc + st * (kStageBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t b = k + ((c * kPieceBytes) >> 4) + 2 * ks;
+            if (c < kQTmemPieces) {
+              mma_ws_bf16_ta(tmem + kOCols + st * 32, tmem + kQCols + 32 * c + 8 * ks, b, idesc_bf16(64, 64, false),
+                             c > 0 || ks > 0, lead);
+            } else {
+              mma_ws_bf16(tmem + kOCols + st * 32, q_desc + ((c * kPieceBytes) >> 4) + 2 * ks, b,
+                          idesc_bf16(64, 64, false), 1, lead);
+            }
+          }
+        }
+        commit_if(&sh.s_full[st], lead);
+        ++s_next;
+        idle = 0;
+        continue;
+      }
+      // nothing was ready: the limit of two seconds runs from the first such pass
+      if (idle++ == 0) t0 = global_timer_ns();
+      bool expired = sh.dead != 0;
+      if (!expired && (idle & 63) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
+        expired = true;
+        atomicOr(&g_paged_error, 2u);
+        sh.dead = 1;
+      }
+      if (__any_sync(0xFFFFFFFFu, expired)) break;
+    }
+    if (o_next < total) {  // given up: whatever was issued finishes before the tensor memory is freed
+      commit_if(&sh.drained, lead);
+      t0 = global_timer_ns();
+      while (!mbar_test(&sh.drained, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+      }
+      __syncwarp();
+    }
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- softmax
+    // Q, sixteen rows a warp, rows past the unit's last one zero, all copies out at once. The latent dims
+    // are then put into the loaders' order, 0, 2, 1, 3 of every four, and as many of them as there are columns
+    // into tensor memory: S reads less of the shared memory that the loaders and O want too.
+    const uint32_t q_row = smem_u32(q_s) + 16 * warp * 128;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const int r = 16 * warp + i, t = q_row_of(r), h = r - t * p.heads;
+      const bool have = t < u.rows && h < u.heads;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q + (have ? (u.row0 + t) * p.ld_q + (u.head0 + h) * p.ld_qh : 0));
+      const uint32_t at = q_row + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
+      copy16_if(at + (lane >> 3) * kPieceBytes, src + 16 * lane, have);
+      copy16_if(at + (4 + (lane >> 3)) * kPieceBytes, src + 512 + 16 * lane, have);
+      if (lane < 8) copy16_if(at + 8 * kPieceBytes, src + 1024 + 16 * lane, have);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    tmem_bar();
+    tc_fence_after();
+    tmem = sh.tmem;
+    const int r = tid & 63, half = tid >> 6;          // row of the unit, and half of the tile's tokens
+    const int t = q_row_of(r), h = r - t * p.heads;
+    const bool have = t < u.rows && h < u.heads;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    auto reorder = [](const uint4& v) {
+      return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                        __byte_perm(v.z, v.w, 0x7632));
+    };
+    const uint32_t own_row = smem_u32(q_s) + r * 128;
+#pragma unroll 1
+    for (int x = 0; x < 8 * kQTmemPieces; x += 4) {
+      uint32_t w[16];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint4 v = reorder(ld_shared16(own_row + (x >> 3) * kPieceBytes + ((((x + y) & 7) ^ (r & 7)) << 4)));
+        w[4 * y] = v.x;
+        w[4 * y + 1] = v.y;
+        w[4 * y + 2] = v.z;
+        w[4 * y + 3] = v.w;
+      }
+      tmem_st16(lanes + kQCols + 4 * x, w);
+    }
+    // of the latent pieces that stay in shared memory, each thread has half a row
+#pragma unroll
+    for (int c = kQTmemPieces; c < kKvLatent / 64; ++c) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t at = own_row + c * kPieceBytes + (((4 * half + x) ^ (r & 7)) << 4);
+        st_shared16(at, reorder(ld_shared16(at)));
+      }
+    }
+    tmem_wait_st();
+    setup();
+    auto arrive = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    arrive(&sh.q_full);
+
+    float m = -INFINITY, l = 0.f;                     // maximum (log2 units) that P and O refer to; this half's sum
+    bool poisoned = false;                            // the row sees a token that is not finite
+    for (int i = 0; i < tiles; ++i) {
+      const int st = i & 1;
+      uint32_t seen = have ? row_sees<kTree>(p, u, t, tile_start(u, i) + 32 * half) : 0u;
+      wait_for(sh, &sh.s_full[st], (i >> 1) & 1);
+      wait_for(sh, &sh.flags[i % kRing], (i / kRing) & 1);  // long complete
+      tc_fence_after();
+      uint32_t v[32];
+      tmem_ld_x32(lanes + kOCols + st * 32, v);
+      seen &= sh.valid[i % kRing][half];
+      const uint32_t bad = sh.poison[i % kRing][half];
+      poisoned |= (seen & bad) != 0u;
+      seen &= ~bad;
+      tmem_wait_ld(v);
+      // v * unit is the logit in log2 units: the raw products as they are where every token counts, or
+      // scaled here with -inf for the others
+      float unit = p.scale_log2;
+      float top = -INFINITY;
+      if (seen != 0xFFFFFFFFu) {
+        unit = 1.0f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          v[c] = (seen >> c) & 1u ? __float_as_uint(__uint_as_float(v[c]) * p.scale_log2) : 0xFF800000u;
+        }
+      }
+      if (unit >= 0.f) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+      } else {
+        top = INFINITY;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) top = fminf(top, fminf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+      }
+      top *= unit;
+      sh.xchg[st][tid] = top;
+      softmax_bar();
+      top = fmaxf(top, sh.xchg[st][tid ^ 64]);
+      // P and O keep an old reference until the maximum has risen by 2^8: P stays finite and
+      // its relative precision is the same, and most tiles leave O alone
+      const bool rise = top > m + kRescaleStep || (m == -INFINITY && top > -INFINITY);
+      const float m_new = rise ? top : m;
+      if (i > 0) {
+        // O is complete up to the last tile (for a rescaling), and with it the only P is free
+        const bool scale_o = __any_sync(0xFFFFFFFFu, rise);
+        wait_for(sh, &sh.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
+        if (scale_o) {
+          tc_fence_after();
+          const float f = rise ? exp2_approx(m - m_new) : 1.0f;  // m = -inf: 0, and O is 0
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < kOCols; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(lanes + c, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(lanes + c, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      m = m_new;
+      // The weights are rounded to bf16 for the product: its operands have one type, and bf16 is the one that holds every
+      // token exactly. l sums them unrounded, so lse keeps its 32 bits.
+      const float ref = m == -INFINITY ? 0.f : m;
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const float e0 = exp2_approx(fmaf(__uint_as_float(v[c]), unit, -ref));
+        const float e1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), unit, -ref));
+        l += e0 + e1;
+        const __nv_bfloat162 e = __floats2bfloat162_rn(e0, e1);
+        w[c / 2] = *reinterpret_cast<const uint32_t*>(&e);
+      }
+      const uint32_t p_row = smem_u32(p_s) + r * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        st_shared16(p_row + (((4 * half + c) ^ (r & 7)) << 4), make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
+      }
+      arrive(&sh.p_full[st]);
+    }
+    if (poisoned) l = __int_as_float(0x7FC00000);
+    softmax_bar();
+    sh.xchg[0][tid] = l;
+    softmax_bar();
+    l += sh.xchg[0][tid ^ 64];
+    if (half == 0) {
+      sh.inv[r] = split ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
+      if (split) {
+        p.ws_ml[static_cast<int64_t>(u.part) * kRows + r] = make_float2(m, l);
+      } else if (p.lse && have) {
+        p.lse[(u.row0 + t) * p.ld_lse + u.head0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      }
+    }
+  }
+  if (warp < kMmaWarp) {
+    // ---------------------------------------------------------------- epilogue
+    // The loaders, four to a lane quarter and 64 columns each, write O (bf16, or the sums of a part) into the
+    // stages' memory, a row of it per query row, and all warps store whole rows.
+    constexpr int kPitchBf16 = kKvLatent * 2 + 16, kPitchF32 = kKvLatent * 4 + 16;  // eight rows' stores fall into different banks
+    static_assert(kRows * kPitchF32 <= kStages * kStageBytes, "the rows fit the stages");
+    // Only the softmax warps may wait for the last O by its parity: they have followed every phase of both o_done
+    // barriers. The loader warps are ordered behind O by the block barrier and the fences around it.
+    if (warp < 4) {
+      wait_for(sh, &sh.o_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
+      tc_fence_after();
+      tc_fence_before();
+    }
+    epilogue_bar();
+    tc_fence_after();
+    if (warp >= 4) {
+      const int quarter = warp & 3, r = (32 * quarter + lane) & 63, half = quarter >> 1;
+      const float inv = sh.inv[r];
+#pragma unroll 1
+      for (int c = 64 * ((warp - 4) >> 2); c < 64 * ((warp - 4) >> 2) + 64; c += 32) {
+        uint32_t o[32];
+        tmem_ld_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c, o);
+        tmem_wait_ld(o);
+        // A product has 256 dims, 128 to each lane half. Dims 1 and 2 of every four have changed places.
+        const int dim = (c / 128) * 256 + half * 128 + (c % 128);
+        if (split) {
+          const uint32_t at = smem_u32(k_s) + r * kPitchF32 + dim * 4;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) st_shared16(at + 16 * j, make_uint4(o[4 * j], o[4 * j + 2], o[4 * j + 1], o[4 * j + 3]));
+        } else {
+          const uint32_t at = smem_u32(k_s) + r * kPitchBf16 + dim * 2;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int e = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
+              const __nv_bfloat162 b =
+                  __floats2bfloat162_rn(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 2]) * inv);
+              w[x] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            st_shared16(at + 16 * j, make_uint4(w[0], w[1], w[2], w[3]));
+          }
+        }
+      }
+    }
+    epilogue_bar();
+    const int units = split ? kKvLatent / 4 : kKvLatent / 8, pitch = split ? kPitchF32 : kPitchBf16;  // of 16 bytes
+    const int rows = u.rows * p.heads;
+    for (int i = tid; i < rows * units; i += kMmaWarp * 32) {
+      const int r = i / units, x = i % units, t = q_row_of(r), h = r - t * p.heads;
+      if (h >= u.heads) continue;
+      uint8_t* dst = split ? reinterpret_cast<uint8_t*>(p.ws_o + (static_cast<int64_t>(u.part) * kRows + r) * kKvLatent)
+                           : reinterpret_cast<uint8_t*>(p.out + (u.row0 + t) * p.ld_out + (u.head0 + h) * p.ld_oh);
+      *reinterpret_cast<uint4*>(dst + 16 * x) = ld_shared16(smem_u32(k_s) + r * pitch + 16 * x);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace block
+}  // namespace idx
