@@ -13,9 +13,12 @@ namespace idx {
 constexpr int kTile = 64;                        // tokens
 constexpr int kPieces = kKvDim / 64;             // 128-byte pieces of a token's bf16 row
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr float kRescaleStep = 8.0f;             // log2: P may reach 2^8 before O is rescaled
+// log2 of what P may reach before O is rescaled. P, l and O are floating point, so their relative precision does not
+// depend on the reference; with 2^31 tokens of values below 2^17, O stays below 2^88.
+constexpr float kRescaleStep = 40.0f;
 constexpr int kAhead = 4;                        // tiles between the L2 prefetch and the loads
 constexpr int kMaxSplitRequests = 160;           // of a call whose contexts are split
+constexpr int kJoinTiles = 3;                    // a part's extra stores and the join, in tiles
 
 // Bit 0: a visible page outside the table or the cache (its tokens are skipped). Bit 1: a wait expired.
 static __device__ unsigned int g_paged_error = 0;
@@ -110,61 +113,86 @@ template <bool kTree, int kHalves>
 __device__ __forceinline__ bool find_unit(const PagedParams& p, int index, Unit& u) {
   const int lane = threadIdx.x & 31;
   const int U = p.tokens;
-  int group;
-  int split = 0;
+  int group, at, n;
   if (p.capacity == 0) {
     // Groups of U rows of all requests have numbers: those of request b start at floor(cu_rows[b] / U) + b, which
     // leaves room for its last, part-filled one.
     u.half = index % kHalves;
     u.head0 = index / kHalves % p.head_blocks * p.heads;
     const int g = index / kHalves / p.head_blocks;
-    int lo = 0, hi = p.B;  // the last b with a first group <= g
-    if (row_at(p, 0) / U > g) return false;
-    while (hi - lo > 1) {
+    int lo = 0, hi = p.B;  // the last b with a first group <= g, 32 candidates a round
+    while (true) {
       const int step = (hi - lo + 31) / 32, b = lo + lane * step;
-      const bool before = b < hi && row_at(p, b) / U + b <= g;
-      lo += (__popc(__ballot_sync(0xFFFFFFFFu, before)) - 1) * step;
+      int first = 0, next = 0, ctx = 0;
+      if (b < hi) {
+        first = row_at(p, b);
+        if (step == 1) {  // the last round: what is needed of the request comes along
+          next = row_at(p, b + 1);
+          ctx = __ldg(p.ctx_lens + b);
+        }
+      }
+      const int src = __popc(__ballot_sync(0xFFFFFFFFu, b < hi && first / U + b <= g)) - 1;
+      if (src < 0) return false;
+      lo += src * step;
+      if (step == 1) {
+        at = __shfl_sync(0xFFFFFFFFu, first, src);
+        n = __shfl_sync(0xFFFFFFFFu, next, src) - at;
+        u.ctx = __shfl_sync(0xFFFFFFFFu, ctx, src);
+        break;
+      }
       hi = min(lo + step, hi);
     }
     u.request = lo;
-    group = g - row_at(p, lo) / U - lo;
+    group = g - at / U - lo;
     u.part = 0;
     u.parts = 1;
   } else {
     // Every request's units are cut into parts of `per` tiles, `per` the same for all and about the smallest with
     // which one wave has room for all parts.
     constexpr int kPer = kMaxSplitRequests / 32;
-    int units[kPer], most[kPer];
-    int64_t sum = 0;
+    int first[kPer], rows[kPer], ctxs[kPer], units[kPer], most[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int b = 32 * k + lane;
-      units[k] = most[k] = 0;
+      first[k] = rows[k] = ctxs[k] = 0;
       if (b < p.B) {
-        const int n = row_at(p, b + 1) - row_at(p, b);
-        if (n > 0) {
-          units[k] = (n + U - 1) / U * p.head_blocks * kHalves;
-          most[k] = most_tiles<kTree>(p, n, max(__ldg(p.ctx_lens + b), 0));
-        }
+        first[k] = row_at(p, b);
+        rows[k] = row_at(p, b + 1);
+        ctxs[k] = __ldg(p.ctx_lens + b);
+      }
+    }
+    int64_t sum = 0;
+    int longest = 1;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      rows[k] -= first[k];
+      units[k] = most[k] = 0;
+      if (rows[k] > 0) {
+        units[k] = (rows[k] + U - 1) / U * p.head_blocks * kHalves;
+        most[k] = most_tiles<kTree>(p, rows[k], max(ctxs[k], 0));
       }
       sum += static_cast<int64_t>(units[k]) * most[k];
+      longest = max(longest, most[k]);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    int per = static_cast<int>(max((sum + p.capacity - 1) / p.capacity, int64_t{1}));
-    int count[kPer], total;
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    int per = static_cast<int>(min(max((sum + p.capacity - 1) / p.capacity, int64_t{1}), static_cast<int64_t>(longest)));
+    int count[kPer];
     while (true) {
-      total = 0;
+      if (per + kJoinTiles >= longest) per = longest;  // whole contexts cost less than parts and their join
+      int total = 0;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         count[k] = (most[k] + per - 1) / per;
         total += units[k] * count[k];
       }
       total = __reduce_add_sync(0xFFFFFFFFu, total);
-      if (total <= p.capacity || per >= (1 << 25)) break;
+      if (total <= p.capacity || per == longest) break;
       per += max(per / 8, 1);
     }
-    int before = 0, found = -1, found_at = 0, found_units = 0, found_parts = 0;
+    int before = 0, found_at = 0, found_units = 0, found_parts = 0;
+    u.request = -1;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int mine = units[k] * count[k];
@@ -174,37 +202,37 @@ __device__ __forceinline__ bool find_unit(const PagedParams& p, int index, Unit&
         const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
         if (lane >= d) upto += o;
       }
-      const int at = before + upto - mine;
-      if (index == 0 && threadIdx.x < 32 && 32 * k + lane < p.B) p.ws_sched[32 * k + lane] = make_int2(at, count[k]);
-      const uint32_t who = __ballot_sync(0xFFFFFFFFu, index >= at && index < at + mine);
+      const int start = before + upto - mine;
+      if (index == 0 && threadIdx.x < 32 && 32 * k + lane < p.B) p.ws_sched[32 * k + lane] = make_int2(start, count[k]);
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, index >= start && index < start + mine);
       if (who) {
         const int src = __ffs(who) - 1;
-        found = 32 * k + src;
-        found_at = __shfl_sync(0xFFFFFFFFu, at, src);
+        u.request = 32 * k + src;
+        found_at = __shfl_sync(0xFFFFFFFFu, start, src);
         found_units = __shfl_sync(0xFFFFFFFFu, units[k], src);
         found_parts = __shfl_sync(0xFFFFFFFFu, count[k], src);
+        at = __shfl_sync(0xFFFFFFFFu, first[k], src);
+        n = __shfl_sync(0xFFFFFFFFu, rows[k], src);
+        u.ctx = __shfl_sync(0xFFFFFFFFu, ctxs[k], src);
       }
       before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    if (found < 0) return false;
+    if (u.request < 0) return false;
     const int in = index - found_at, unit = in % found_units;  // units vary fastest: they read the same tokens
-    u.request = found;
     u.half = unit % kHalves;
     u.head0 = unit / kHalves % p.head_blocks * p.heads;
     group = unit / kHalves / p.head_blocks;
     u.part = index;
     u.parts = found_parts;
-    split = in / found_units;
-    u.tile0 = split * per;
+    u.tile0 = in / found_units * per;
     u.tiles = per;
   }
-  const int at = row_at(p, u.request), n = row_at(p, u.request + 1) - at;
   const int start = group * U;
   if (start >= n) return false;
   u.row0 = at + start;
   u.rows = min(U, n - start);
   u.heads = min(p.heads, p.H - u.head0);
-  u.ctx = max(__ldg(p.ctx_lens + u.request), 0);
+  u.ctx = max(u.ctx, 0);
   u.base = u.ctx - n;
   u.pos0 = u.base + start;
   const int all = seen_tiles<kTree>(p, start, start + u.rows - 1, u);
@@ -227,15 +255,15 @@ __device__ __forceinline__ int tile_start(const Unit& u, int i) {
 // Whether a row of the unit sees token j.
 __device__ __forceinline__ bool unit_sees(const Unit& u, int j) { return j <= u.hi && (j >= u.lo || j < u.first); }
 
-// The cache block of token j, -1 if no row sees it or its page is missing (flagged where `report`).
-__device__ __forceinline__ int block_of(const PagedParams& p, const Unit& u, int j, bool report) {
-  if (!unit_sees(u, j)) return -1;
+// The table's entry for token j, as it stands there; -1 if no row sees the token or the table has no such page. Nothing
+// here waits for the entry, so that it can be asked for long before its use.
+__device__ __forceinline__ int entry_of(const PagedParams& p, const Unit& u, int j) {
   const int page = j >> p.page_shift;
-  int blk = -1;
-  if (page < p.n_pages) blk = __ldg(p.block_table + u.request * p.ld_bt + page);
-  if (blk >= 0 && blk < p.num_blocks) return blk;
-  if (report) atomicOr(&g_paged_error, 1u);
-  return -1;
+  return unit_sees(u, j) && page < p.n_pages ? __ldg(p.block_table + u.request * p.ld_bt + page) : -1;
+}
+
+__device__ __forceinline__ bool is_block(const PagedParams& p, int entry) {
+  return static_cast<uint32_t>(entry) < static_cast<uint32_t>(p.num_blocks);
 }
 
 // The lowest n bits.

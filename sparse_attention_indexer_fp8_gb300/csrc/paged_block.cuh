@@ -35,7 +35,6 @@ constexpr int kEarly = 3;  // of a warp's tokens, those converted while the stag
 constexpr int kMmaWarp = 4 + kLoaderWarps;
 constexpr int kRopeWarp = kMmaWarp + 1;          // one per stage
 constexpr int kThreads = (kRopeWarp + kStages) * 32;
-constexpr int kRing = 4;
 constexpr int kOCols = 256;                      // tensor-memory columns of O; S0 and S1 (32 each) follow
 constexpr int kQCols = 320;                      // and the first kQTmemPieces pieces of Q
 constexpr int kQTmemPieces = 6;
@@ -48,13 +47,13 @@ struct Shared {
   uint64_t s_full[kStages];                      // S of the tile is complete
   uint64_t p_full[kStages];                      // P is stored
   uint64_t o_done[kStages];                      // the tile's share of O is complete: P and the stage are free
-  uint64_t flags[kRing];                         // `valid` and `poison` are written
   uint32_t tmem;
   volatile uint32_t dead;                        // a wait expired: no further wait blocks
-  uint32_t valid[kRing][2];                      // bit t: token t of the tile is there
-  uint32_t poison[kRing][2];                     // bit t: and not finite
+  alignas(8) uint8_t there[kStages][kGroupWarps];   // bit j of byte w: token 8 w + j of the tile is there
+  alignas(8) uint8_t poison[kStages][kGroupWarps];  // and not finite
   float xchg[2][128];
   float inv[kRows];                              // 1 / sum of each row
+  Unit unit;                                     // for the end: the roles' registers are all taken
 };
 
 constexpr int kSmemBytes = kQBytes + kStages * kStageBytes + kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
@@ -81,12 +80,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
   Unit u;
   if (!find_unit<kTree, 1>(p, blockIdx.x, u)) return;
   const int tiles = u.tiles;
-  const bool split = u.parts > 1;
   // query row r of the unit: head r % heads of token r / heads
   auto q_row_of = [&](int r) { return r / p.heads; };
 
   if (tiles == 0) {
-    if (split) {
+    if (u.parts > 1) {
       if (tid < kRows) p.ws_ml[static_cast<int64_t>(u.part) * kRows + tid] = make_float2(-INFINITY, 0.f);
     } else {
       for (int i = tid; i < u.rows * u.heads * (kKvLatent / 8); i += kThreads) {
@@ -99,6 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     return;
   }
 
+  if (tid == 0) sh.unit = u;
   // Barriers and tensor memory are set up by the matrix warp; every role first does what needs neither.
   uint32_t tmem = 0;
   auto setup = [&]() {
@@ -121,25 +120,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     // conversion: nothing between two tiles' loads waits for an address.
     uint32_t mults = 0, next_codes = 0, found_codes = 0;
     uint32_t there = 0;  // bit j: token j of the found tile is loaded
-    int next_block = -1;
     const uint8_t* latent = nullptr;  // of the warp's first token
     // of a lane's own token, lane % 8; the warp's tokens that a row sees share one block
     auto lookup = [&](int tile) {
-      return tile < tiles ? block_of(p, u, tile_start(u, tile) + r0 + (lane & 7), false) : -1;
+      return tile < tiles ? entry_of(p, u, tile_start(u, tile) + r0 + (lane & 7)) : -1;
     };
-    auto find = [&](int tile) {
-      there = __ballot_sync(0xFFFFFFFFu, next_block >= 0) & 0xFFu;
-      const int blk = there ? __shfl_sync(0xFFFFFFFFu, next_block, __ffs(there) - 1) : 0;
+    auto find = [&](int tile, int block) {  // the lane's token is in `block`
+      const bool mine = is_block(p, block);
+      there = __ballot_sync(0xFFFFFFFFu, mine) & 0xFFu;
+      const int blk = there ? __shfl_sync(0xFFFFFFFFu, block, __ffs(there) - 1) : 0;
       found_codes = 0;
       if (there) {
         const int off = (tile_start(u, tile) + r0) & (p.block_size - 1);
         const uint8_t* base = p.cache + blk * p.block_stride;
         latent = base + off * kKvLatent;
-        if (next_block >= 0) {
+        if (mine) {
           found_codes = __ldg(reinterpret_cast<const uint32_t*>(base + p.block_size * kKvScaleAt) + off + (lane & 7));
         }
       }
-      next_block = lookup(tile + kStages);
     };
     auto load = [&]() {
 #pragma unroll
@@ -160,16 +158,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     };
     const uint32_t unit = smem_u32(k_s) + group * kStageBytes + (lane >> 3) * kPieceBytes + r0 * 128 + 16 * (lane & 7);
 
-    if (group < tiles) {
-      next_block = lookup(group);
-      find(group);
+    int next_block;
+    uint32_t now;  // `there` of the tile in the registers
+    {
+      const int here = lookup(group);
+      next_block = lookup(group + kStages);
+      find(group, here);
       load();
       next_codes = found_codes;
-      if (group + kStages < tiles) find(group + kStages);
+      now = there;
+      if (group + kStages < tiles) find(group + kStages, next_block);
+      next_block = lookup(group + 2 * kStages);
     }
     setup();
     for (int i = group; i < tiles; i += kStages) {
       mults = multiplier_bytes(next_codes);
+      const uint32_t bad = __ballot_sync(0xFFFFFFFFu, mults == 0u) & now;
       uint4 early[kEarly][2];
 #pragma unroll
       for (int j = 0; j < kEarly; ++j) {
@@ -186,46 +190,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
           st_shared16(unit + 4 * h * kPieceBytes + j * 128, j < kEarly ? early[j % kEarly][h] : convert(raw[j][h], word, h));
         }
       }
+      if (lane == 0) {
+        // O of tile i - 2, waited for above, was issued once its softmax had read this place
+        sh.there[group][lw] = static_cast<uint8_t>(now);
+        sh.poison[group][lw] = static_cast<uint8_t>(bad);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[group]);
       if (i + kStages < tiles) {
         load();
         next_codes = found_codes;
-        if (i + 2 * kStages < tiles) find(i + 2 * kStages);
+        now = there;
+        if (i + 2 * kStages < tiles) find(i + 2 * kStages, next_block);
+        next_block = lookup(i + 3 * kStages);
       }
     }
   } else if (warp >= kRopeWarp) {
     // ---------------------------------------------------------------- position dims, and L2 prefetch
     // Position dims are bf16 in the cache as in the tile: copied asynchronously, as soon as S of the tile
-    // before is complete. Lane l locates tokens l and 32 + l. The same warp says which tokens are there and finite, and
-    // brings the records of the tile kAhead further on into L2.
+    // before is complete. Lane l locates tokens l and 32 + l. The same warp reports missing pages, and brings the records
+    // of the tile kAhead further on into L2.
     const int group = warp - kRopeWarp;
-    struct Token {
-      const uint8_t* rope;
-      const uint32_t* codes;
-    };
-    auto locate = [&](int tile, int h, bool report) {
-      Token t{nullptr, nullptr};
-      if (tile >= tiles) return t;
-      const int j = tile_start(u, tile) + 32 * h + lane;
-      const int blk = block_of(p, u, j, report);
-      if (blk < 0) return t;
-      const int off = j & (p.block_size - 1);
-      const uint8_t* base = p.cache + blk * p.block_stride;
-      t.rope = base + p.block_size * kKvRopeAt + off * (2 * kKvRope);
-      t.codes = reinterpret_cast<const uint32_t*>(base + p.block_size * kKvScaleAt) + off;
-      return t;
-    };
+    auto entry = [&](int tile, int h) { return tile < tiles ? entry_of(p, u, tile_start(u, tile) + 32 * h + lane) : -1; };
     // 32 tokens: each lane's own position dims and codes, and 8 x 4 lines of latents an instruction
-    auto prefetch = [&](int tile, int h) {
+    auto prefetch = [&](int tile, int h, int block) {
       if (tile >= tiles) return;
-      const int j = tile_start(u, tile) + 32 * h + lane;
-      const int blk = block_of(p, u, j, false);
+      const int off = (tile_start(u, tile) + 32 * h + lane) & (p.block_size - 1);
       const uint8_t* latent = nullptr;
-      if (blk >= 0) {
-        const int off = j & (p.block_size - 1);
-        const uint8_t* base = p.cache + blk * p.block_stride;
+      if (is_block(p, block)) {
+        const uint8_t* base = p.cache + block * p.block_stride;
         latent = base + off * kKvLatent;
         prefetch_l2(base + p.block_size * kKvRopeAt + off * (2 * kKvRope));
         if ((lane & 15) == 0) prefetch_l2(base + p.block_size * kKvScaleAt + 4 * off);
@@ -237,43 +231,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       }
       __syncwarp();
     };
+    int here[2], ahead[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      here[h] = entry(group, h);
+      ahead[h] = entry(group + kAhead, h);
+    }
     for (int i = group; i < kAhead && i < tiles; i += kStages) {
-      prefetch(i, 0);
-      prefetch(i, 1);
+      prefetch(i, 0, entry(i, 0));
+      prefetch(i, 1, entry(i, 1));
     }
     const uint32_t piece = smem_u32(k_s) + group * kStageBytes + (kPieces - 1) * kPieceBytes;
     setup();
     for (int i = group; i < tiles; i += kStages) {
-      const Token tok[2] = {locate(i, 0, true), locate(i, 1, true)};
-      uint32_t valid[2], poison[2];
+      const uint8_t* rope[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        valid[h] = __ballot_sync(0xFFFFFFFFu, tok[h].rope != nullptr);
-        poison[h] = __ballot_sync(0xFFFFFFFFu, tok[h].rope != nullptr && !codes_finite(__ldg(tok[h].codes)));
+        const int j = tile_start(u, i) + 32 * h + lane;
+        const bool mine = is_block(p, here[h]);
+        rope[h] = mine ? p.cache + here[h] * p.block_stride + p.block_size * kKvRopeAt +
+                             (j & (p.block_size - 1)) * (2 * kKvRope)
+                       : nullptr;
+        if (!mine && unit_sees(u, j)) atomicOr(&g_paged_error, 1u);
+        here[h] = entry(i + kStages, h);
       }
       // only S reads position dims, so their piece is free long before the stage is
       if (i >= kStages) wait_for(sh, &sh.s_full[group], ((i >> 1) - 1) & 1);
 #pragma unroll
       for (int c = 0; c < kTile / 4; ++c) {
         const int t = 4 * c + (lane >> 3), x = lane & 7;
-        const uint8_t* from = shfl_ptr(tok[c / 8].rope, t & 31);
+        const uint8_t* from = shfl_ptr(rope[c / 8], t & 31);
         copy16_if(piece + t * 128 + ((x ^ (t & 7)) << 4), from ? from + 16 * x : p.cache, from != nullptr);
-      }
-      if (lane == 0) {
-        // S of tile i - 2, waited for above, was issued after O of tile i - 4, hence after entry i - 4 was read
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          sh.valid[i % kRing][h] = valid[h];
-          sh.poison[i % kRing][h] = poison[h];
-        }
-        mbar_arrive(&sh.flags[i % kRing]);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[group]);
-      prefetch(i + kAhead, 0);
-      prefetch(i + kAhead, 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        prefetch(i + kAhead, h, ahead[h]);
+        ahead[h] = entry(i + kAhead + kStages, h);
+      }
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
@@ -285,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
         mbar_init(&sh.p_full[i], 4);
         mbar_init(&sh.o_done[i], 1);
       }
-      for (int i = 0; i < kRing; ++i) mbar_init(&sh.flags[i], 1);
       sh.dead = 0;
       fence_mbar_init();
     }
@@ -437,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       const int st = i & 1;
       uint32_t seen = have ? row_sees<kTree>(p, u, t, tile_start(u, i) + 32 * half) : 0u;
       wait_for(sh, &sh.s_full[st], (i >> 1) & 1);
-      wait_for(sh, &sh.flags[i % kRing], (i / kRing) & 1);  // long complete
+      wait_for(sh, &sh.k_full[st], (i >> 1) & 1);  // long complete: `there` is written
       tc_fence_after();
       uint32_t v[32];
       tmem_ld_x32(lanes + kOCols + st * 32, v);
-      seen &= sh.valid[i % kRing][half];
-      const uint32_t bad = sh.poison[i % kRing][half];
+      seen &= *reinterpret_cast<const uint32_t*>(&sh.there[st][4 * half]);
+      const uint32_t bad = *reinterpret_cast<const uint32_t*>(&sh.poison[st][4 * half]);
       poisoned |= (seen & bad) != 0u;
       seen &= ~bad;
       tmem_wait_ld(v);
@@ -469,17 +466,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       sh.xchg[st][tid] = top;
       softmax_bar();
       top = fmaxf(top, sh.xchg[st][tid ^ 64]);
-      // P and O keep an old reference until the maximum has risen by 2^8: P stays finite and
-      // its relative precision is the same, and most tiles leave O alone
+      // P and O keep an old reference until the maximum has risen by 2^40, so hardly a tile rescales O
       const bool rise = top > m + kRescaleStep || (m == -INFINITY && top > -INFINITY);
       const float m_new = rise ? top : m;
       if (i > 0) {
         // O is complete up to the last tile (for a rescaling), and with it the only P is free
-        const bool scale_o = __any_sync(0xFFFFFFFFu, rise);
+        const float f = rise && m != -INFINITY ? exp2_approx(m - m_new) : 1.0f;  // without a reference, l and O are 0
+        const bool scale_o = __any_sync(0xFFFFFFFFu, f != 1.0f);
         wait_for(sh, &sh.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
         if (scale_o) {
           tc_fence_after();
-          const float f = rise ? exp2_approx(m - m_new) : 1.0f;  // m = -inf: 0, and O is 0
           l *= f;
 #pragma unroll 1
           for (int c = 0; c < kOCols; c += 16) {
@@ -518,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     softmax_bar();
     l += sh.xchg[0][tid ^ 64];
     if (half == 0) {
+      const bool split = u.parts > 1;
       sh.inv[r] = split ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
       if (split) {
         p.ws_ml[static_cast<int64_t>(u.part) * kRows + r] = make_float2(m, l);
@@ -541,6 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     }
     epilogue_bar();
     tc_fence_after();
+    const volatile Unit& e = sh.unit;
+    const bool split = e.parts > 1;
+    tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
     if (warp >= 4) {
       const int quarter = warp & 3, r = (32 * quarter + lane) & 63, half = quarter >> 1;
       const float inv = sh.inv[r];
@@ -562,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
             uint32_t w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int e = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
+              const int c0 = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
               const __nv_bfloat162 b =
-                  __floats2bfloat162_rn(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 2]) * inv);
+                  __floats2bfloat162_rn(__uint_as_float(o[c0]) * inv, __uint_as_float(o[c0 + 2]) * inv);
               w[x] = *reinterpret_cast<const uint32_t*>(&b);
             }
             st_shared16(at + 16 * j, make_uint4(w[0], w[1], w[2], w[3]));
@@ -574,12 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     }
     epilogue_bar();
     const int units = split ? kKvLatent / 4 : kKvLatent / 8, pitch = split ? kPitchF32 : kPitchBf16;  // of 16 bytes
-    const int rows = u.rows * p.heads;
+    const int rows = e.rows * p.heads, row0 = e.row0, heads = e.heads, head0 = e.head0, part = e.part;
     for (int i = tid; i < rows * units; i += kMmaWarp * 32) {
       const int r = i / units, x = i % units, t = q_row_of(r), h = r - t * p.heads;
-      if (h >= u.heads) continue;
-      uint8_t* dst = split ? reinterpret_cast<uint8_t*>(p.ws_o + (static_cast<int64_t>(u.part) * kRows + r) * kKvLatent)
-                           : reinterpret_cast<uint8_t*>(p.out + (u.row0 + t) * p.ld_out + (u.head0 + h) * p.ld_oh);
+      if (h >= heads) continue;
+      uint8_t* dst = split ? reinterpret_cast<uint8_t*>(p.ws_o + (static_cast<int64_t>(part) * kRows + r) * kKvLatent)
+                           : reinterpret_cast<uint8_t*>(p.out + (row0 + t) * p.ld_out + (head0 + h) * p.ld_oh);
       *reinterpret_cast<uint4*>(dst + 16 * x) = ld_shared16(smem_u32(k_s) + r * pitch + 16 * x);
     }
   }
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
   __syncwarp();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
 }
 
 }  // namespace block
