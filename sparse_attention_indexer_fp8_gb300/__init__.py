@@ -290,7 +290,7 @@ def _int32(fn: str, name: str, v: int) -> int:
 def _vec(fn: str, name: str, t, dev: int, dtype, n: int) -> int:
     """Device pointer of the contiguous vector ``t`` [n]. These checks run on every call of a decode step, so the
     common case is one expression."""
-    if t.get_device() == dev and t.dtype is dtype and t.shape == (n,) and (n < 2 or t.stride(0) == 1):
+    if t.get_device() == dev and t.dtype is dtype and t.numel() == n and t.dim() == 1 and t.is_contiguous():
         return t.data_ptr()
     _refuse(fn, name, t, dev, dtype, (n,))
 
@@ -484,19 +484,23 @@ def idx_build_tables(cached_lens, new_lens, free_blocks, block_table, block_size
     i32 = torch.int32
     B, n_rows, n_free = cached_lens.shape[0], positions.shape[0], free_blocks.shape[0]
     bt, ld_bt = _mat(fn, "block_table", block_table, dev, i32, B, None)
+    def per_request(name, t):
+        return None if t is None else _vec(fn, name, t, dev, i32, B)
+
+    def per_row(name, t):
+        return None if t is None else _vec(fn, name, t, dev, i32, n_rows)
+
     _call(fn, dev, stream, _vec(fn, "cached_lens", cached_lens, dev, i32, B), _vec(fn, "new_lens", new_lens, dev, i32, B),
-          None if held_pages is None else _vec(fn, "held_pages", held_pages, dev, i32, B), B,
-          _vec(fn, "free_blocks", free_blocks, dev, i32, n_free), _int32(fn, "free_blocks' length", n_free),
+          per_request("held_pages", held_pages), B, _vec(fn, "free_blocks", free_blocks, dev, i32, n_free),
+          _int32(fn, "free_blocks' length", n_free),
           None if free_start is None else _vec(fn, "free_start", free_start, dev, i32, 1), bt, ld_bt,
           block_table.shape[1], block_size, _vec(fn, "ctx_lens", ctx_lens, dev, i32, B),
           _vec(fn, "cu_rows", cu_rows, dev, i32, B + 1),
-          None if cu_ctx is None else _vec(fn, "cu_ctx", cu_ctx, dev, i32, B + 1),
-          None if held_out is None else _vec(fn, "held_out", held_out, dev, i32, B),
+          None if cu_ctx is None else _vec(fn, "cu_ctx", cu_ctx, dev, i32, B + 1), per_request("held_out", held_out),
           None if free_end is None else _vec(fn, "free_end", free_end, dev, i32, 1),
           _vec(fn, "positions", positions, dev, i32, n_rows),
-          _vec(fn, "slot_mapping", slot_mapping, dev, torch.int64, n_rows),
-          None if row_to_req is None else _vec(fn, "row_to_req", row_to_req, dev, i32, n_rows),
-          None if row_ke is None else _vec(fn, "row_ke", row_ke, dev, i32, n_rows), _int32(fn, "rows", n_rows))
+          _vec(fn, "slot_mapping", slot_mapping, dev, torch.int64, n_rows), per_row("row_to_req", row_to_req),
+          per_row("row_ke", row_ke), _int32(fn, "rows", n_rows))
 
 
 def idx_tree_mask(parents, cu_rows, mask, base_lens=None, positions=None, stream=None):

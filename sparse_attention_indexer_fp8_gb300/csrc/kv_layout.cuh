@@ -57,4 +57,16 @@ __device__ __forceinline__ void kv_dequant4_even_odd(uint32_t w, uint32_t mul, u
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(b), "r"(mul));
 }
 
+// The same as kv_dequant4 in eight operations instead of nine to ten: each byte beside eight copies of its sign, both
+// shifted at once, and one mask for what belongs to neither the sign nor the seven bits.
+__device__ __forceinline__ void kv_dequant4_signs(uint32_t w, uint32_t mul, uint32_t& lo, uint32_t& hi) {
+  uint32_t p, q;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(p) : "r"(w));  // bytes 0, sign of 0, 1, sign of 1
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(q) : "r"(w));
+  const uint32_t a = (p << 4) & 0x87F087F0u;
+  const uint32_t b = (q << 4) & 0x87F087F0u;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(mul));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(mul));
+}
+
 }  // namespace idx

@@ -12,93 +12,111 @@
 namespace idx {
 namespace {
 
-// How a call's rows are cut into units, and whether their contexts are split: where one wave has room for more parts
-// than there are units.
+// How a call's rows are cut into units, and the workers among whom they are shared out.
 struct Plan {
   bool pairs;
-  int head_blocks, heads, tokens, capacity;
+  int head_blocks, heads, tokens, workers;
   int64_t units;
   int64_t part_floats, part_rows;  // of a part: accumulators, maxima and sums
 };
 
-// Joins the parts of each row (one head of one token), of a unit with half of the dims each half by itself: weights
-// 2^(m_i - max m), a part without a visible token skipped (its accumulators were never written). That is the work of
-// kWarps warps, each of which takes every kWarps-th part, two at a time: all rows of a batch run at once, and the loads
-// of two parts are in flight together. Rows whose context was not split are complete already.
+// Joins the parts of the units that the workers' shares cut: weights 2^(m_i - max m), a part without a visible token
+// skipped (its accumulators were never written). The rows of all cut units are dealt out to the warps, or where there
+// are few to groups of up to eight warps, each of which takes its share of the parts, four at a time. The first part of a
+// unit is its worker's last (2 worker + 1), every other its worker's first (2 worker).
 constexpr int kJoinWarps = 8;   // of a block
-constexpr int kMaxParts = 160;
+constexpr int kJoinBlocks = 2;  // of an SM
+constexpr int kMaxWorkers = kJoinWarps * 32;
 
-template <bool kPair, int kWarps>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedParams p) {
-  constexpr int kItems = kJoinWarps / kWarps;  // of a block
+template <bool kPair>
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocks) paged_join_kernel(const PagedParams p) {
   constexpr int kHalves = kPair ? pair::kHalves : 1;
   constexpr int kDims = kKvLatent / kHalves, kVecs = kDims / 128;
   constexpr int kPartRows = kPair ? pair::kRows : block::kRows;
-  __shared__ float4 sums[kItems][kWarps > 1 ? kWarps - 1 : 1][kDims / 4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp / kWarps, g = warp % kWarps;
-  const uint32_t heads = static_cast<uint32_t>(p.H), item = blockIdx.x * kItems + sub;
-  const int d = static_cast<int>(item % kHalves);
-  const uint32_t head = item / kHalves;
-  bool have = head < static_cast<uint32_t>(p.T) * heads;
-  const int row = have ? static_cast<int>(head / heads) : 0, h = have ? static_cast<int>(head % heads) : 0;
-  int lo = 0, hi = p.B;  // the last b with cu_rows[b] <= row
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
-    const bool before = b < hi && (lane == 0 || row_at(p, b) <= row);
-    lo += (__popc(__ballot_sync(0xFFFFFFFFu, before)) - 1) * step;
-    hi = min(lo + step, hi);
-  }
-  const int at = row_at(p, lo), n = row_at(p, lo + 1) - at, in = row - at;
-  have = have && in >= 0 && in < n;
-  const int units = (n + p.tokens - 1) / p.tokens * p.head_blocks * kHalves;
-  const int unit = (in / p.tokens * p.head_blocks + h / p.heads) * kHalves + d;
-  int r = in % p.tokens;
-  if (kPair) {
-    const int own = p.tokens / 2;
-    r = r / own * pair::kBlockRows + r % own * p.heads + h % p.heads;
-  } else {
-    r = r * p.heads + h % p.heads;
-  }
+  __shared__ int ends[kMaxWorkers];  // rows of the cut units up to and with each worker's
+  __shared__ float4 sums[kJoinWarps][kDims / 4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // every part is complete and visible
-  const int2 sched = have ? __ldcg(p.ws_sched + lo) : make_int2(0, 1);
-  const int parts = min(sched.y, kMaxParts);
-  have = have && parts > 1;
-  const int64_t step = static_cast<int64_t>(units) * kPartRows;
-  const int64_t first = static_cast<int64_t>(sched.x + unit) * kPartRows + r;
-  const float2* ml = p.ws_ml + first;  // of part i: ml[step * i]
-  const float4* o = reinterpret_cast<const float4*>(p.ws_o + first * kDims) + lane;
-
-  float4 acc[kVecs] = {};
-  float m = -INFINITY, l = 0.f;
-  if (have) {
-    float2 mine[kMaxParts / 32];
+  const int cuts = min(p.workers, kMaxWorkers);
+  int mine = 0;
+  if (tid < cuts && __ldcg(&p.ws_cuts[tid].parts) > 0) mine = __ldcg(&p.ws_cuts[tid].rows) * __ldcg(&p.ws_cuts[tid].heads);
+  if (!__syncthreads_or(mine)) return;
+  ends[tid] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    int before = 0;
+    for (int k = 0; k < kMaxWorkers; k += 32) {
+      int upto = ends[k + lane];
 #pragma unroll
-    for (int c = 0; c < kMaxParts / 32; ++c) {
-      mine[c] = 32 * c + lane < parts ? __ldcg(ml + (32 * c + lane) * step) : make_float2(-INFINITY, 0.f);
-      m = fmaxf(m, mine[c].x);
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      ends[k + lane] = before + upto;
+      before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-#pragma unroll
-    for (int c = 0; c < kMaxParts / 32; ++c) {
-      if (mine[c].y != 0.f) l = fmaf(exp2f(mine[c].x - m), mine[c].y, l);
+  }
+  __syncthreads();
+  const int total = ends[kMaxWorkers - 1];
+  int team = kJoinWarps;  // warps of a row
+  while (team > 1 && static_cast<int64_t>(total) * team > static_cast<int64_t>(gridDim.x) * kJoinWarps) team >>= 1;
+  const int teams = kJoinWarps / team, g = warp % team;
+  for (int base = blockIdx.x * teams; base < total; base += gridDim.x * teams) {  // the same for all warps
+    const int item = base + warp / team;
+    const bool have = item < total;
+    Cut cut{};
+    int worker = 0, r = 0, t = 0, h = 0;
+    if (have) {
+      int lo = 0, hi = kMaxWorkers - 1;  // the first worker with ends > item
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > item) hi = mid; else lo = mid + 1;
+      }
+      worker = lo;
+      const int4* c = reinterpret_cast<const int4*>(p.ws_cuts + worker);
+      const int4 c0 = __ldcg(c), c1 = __ldcg(c + 1);
+      cut = Cut{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, {0, 0}};
+      const int in = item - (lo > 0 ? ends[lo - 1] : 0);
+      t = in / cut.heads;
+      h = in - t * cut.heads;
+      r = t * p.heads + h;
+      if (kPair) {
+        const int own = p.tokens / 2;
+        r = t / own * pair::kBlockRows + t % own * p.heads + h;
+      }
     }
+    auto place = [&](int i) { return static_cast<int64_t>(2 * (worker + i) + (i == 0 ? 1 : 0)) * kPartRows + r; };
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < cut.parts; i += 32) {
+      const float2 x = __ldcg(p.ws_ml + place(i));
+      const float top = fmaxf(m, x.x);
+      if (l != 0.f) l *= exp2f(m - top);
+      if (x.y != 0.f) l += x.y * exp2f(x.x - top);
+      m = top;
+    }
+    float top = m;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    if (l != 0.f) l *= exp2f(m - top);
+    m = top;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
-    for (int i = g; i < parts; i += 2 * kWarps) {
-      float2 x[2];
-      float4 v[2][kVecs];
+    float4 acc[kVecs] = {};
+    for (int i0 = g; i0 < cut.parts; i0 += 4 * team) {
+      float2 x[4];
+      float4 v[4][kVecs];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int part = i + j * kWarps;
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * team;
         x[j] = make_float2(-INFINITY, 0.f);
-        if (part >= parts) continue;
-        x[j] = __ldcg(ml + part * step);
+        if (i >= cut.parts) continue;
+        x[j] = __ldcg(p.ws_ml + place(i));
+        const float4* o = reinterpret_cast<const float4*>(p.ws_o + place(i) * kDims) + lane;
 #pragma unroll
-        for (int c = 0; c < kVecs; ++c) v[j][c] = __ldcg(o + part * step * (kDims / 4) + 32 * c);
+        for (int c = 0; c < kVecs; ++c) v[j][c] = __ldcg(o + 32 * c);
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 4; ++j) {
         if (x[j].y == 0.f) continue;
         const float w = exp2f(x[j].x - m);
 #pragma unroll
@@ -110,38 +128,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
         }
       }
     }
-  }
-  if constexpr (kWarps > 1) {
+    if (team > 1) {
+      __syncthreads();  // the last row's sums are read
 #pragma unroll
-    for (int c = 0; c < kVecs; ++c) {
-      if (g > 0) sums[sub][g - 1][lane + 32 * c] = acc[c];
-    }
-    __syncthreads();
-    if (g > 0) return;
+      for (int c = 0; c < kVecs; ++c) sums[warp][lane + 32 * c] = acc[c];
+      __syncthreads();
+      if (g > 0) continue;
+      for (int i = 1; i < team; ++i) {
 #pragma unroll
-    for (int i = 0; i < kWarps - 1; ++i) {
-#pragma unroll
-      for (int c = 0; c < kVecs; ++c) {
-        const float4 v = sums[sub][i][lane + 32 * c];
-        acc[c].x += v.x;
-        acc[c].y += v.y;
-        acc[c].z += v.z;
-        acc[c].w += v.w;
+        for (int c = 0; c < kVecs; ++c) {
+          const float4 v = sums[warp + i][lane + 32 * c];
+          acc[c].x += v.x;
+          acc[c].y += v.y;
+          acc[c].z += v.z;
+          acc[c].w += v.w;
+        }
       }
     }
-  }
-  if (!have) return;
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  __nv_bfloat16* dst = p.out + row * p.ld_out + h * p.ld_oh + d * kDims + 4 * lane;
+    if (!have) continue;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const int64_t q = cut.row0 + t;
+    __nv_bfloat16* dst = p.out + q * p.ld_out + (cut.head0 + h) * p.ld_oh + cut.half * kDims + 4 * lane;
 #pragma unroll
-  for (int c = 0; c < kVecs; ++c) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
-    *reinterpret_cast<uint2*>(dst + 128 * c) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-  if (p.lse && lane == 0 && d == 0) {
-    p.lse[row * p.ld_lse + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    for (int c = 0; c < kVecs; ++c) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+      *reinterpret_cast<uint2*>(dst + 128 * c) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+    if (p.lse && lane == 0 && cut.half == 0) {
+      p.lse[q * p.ld_lse + cut.head0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
   }
 }
 
@@ -181,37 +198,22 @@ int device_pairs() {
 
 Plan plan_of(int32_t T, int32_t B, int32_t H) {
   Plan plan{};
-  const int per_request = T / B;  // query tokens, on average
   const char* env = getenv("IDX_PAIR");
-  plan.pairs = env ? atoi(env) : static_cast<int64_t>(per_request) * H >= 192;
+  plan.pairs = env ? atoi(env) : static_cast<int64_t>(T) * H >= 256 * static_cast<int64_t>(B);
   const int rows = plan.pairs ? pair::kBlockRows : block::kRows;
   plan.head_blocks = (H + rows - 1) / rows;
   plan.heads = (H + plan.head_blocks - 1) / plan.head_blocks;
   plan.tokens = rows / plan.heads * (plan.pairs ? 2 : 1);
   const int each = plan.head_blocks * (plan.pairs ? pair::kHalves : 1);  // units of a group of tokens
-  const int64_t groups = T / plan.tokens + static_cast<int64_t>(B);
-  plan.units = groups * each;
-  // no more groups hold rows: each request's last one may be part-filled
-  const int64_t filled = std::min<int64_t>(T, groups) * each;
-  const int room = plan.pairs ? device_pairs() : device_sm_count();
-  plan.capacity = filled < room && B <= kMaxSplitRequests ? std::min(room, kMaxParts) : 0;
+  plan.units = (T / plan.tokens + static_cast<int64_t>(B)) * each;
+  plan.workers = B <= kMaxSharedRequests ? std::min(plan.pairs ? device_pairs() : device_sm_count(), kMaxWorkers) : 0;
   plan.part_rows = plan.pairs ? pair::kRows : block::kRows;
   plan.part_floats = plan.part_rows * (plan.pairs ? pair::kDims : kKvLatent);
   return plan;
 }
 
-int64_t sched_bytes(int32_t B) { return (static_cast<int64_t>(B) * sizeof(int2) + 15) / 16 * 16; }
-
-int64_t plan_bytes(const Plan& plan, int32_t B) {
-  return plan.capacity ? sched_bytes(B) + plan.capacity * (plan.part_floats * 4 + plan.part_rows * 8) : 0;
-}
-
-template <bool kPair>
-auto* join_kernel(int warps) {
-  return warps == 1   ? paged_join_kernel<kPair, 1>
-         : warps == 2 ? paged_join_kernel<kPair, 2>
-         : warps == 4 ? paged_join_kernel<kPair, 4>
-                      : paged_join_kernel<kPair, 8>;
+int64_t plan_bytes(const Plan& plan) {
+  return plan.workers * (static_cast<int64_t>(sizeof(Cut)) + 2 * (plan.part_floats * 4 + plan.part_rows * 8));
 }
 
 // What both calls check and launch; `p` holds what they were given.
@@ -244,18 +246,17 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
   p.head_blocks = plan.head_blocks;
   p.heads = plan.heads;
   p.tokens = plan.tokens;
-  p.capacity = ws ? plan.capacity : 0;
-  if (p.capacity) {
-    const int64_t need = plan_bytes(plan, p.B);
-    if (ws_bytes < static_cast<size_t>(need)) {
+  p.workers = ws ? plan.workers : 0;
+  if (p.workers) {
+    if (ws_bytes < static_cast<size_t>(plan_bytes(plan))) {
       return fail(IDX_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %lld are needed", fn, ws_bytes,
-                  static_cast<long long>(need));
+                  static_cast<long long>(plan_bytes(plan)));
     }
-    p.ws_sched = static_cast<int2*>(ws);
-    p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sched_bytes(p.B));
-    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + p.capacity * plan.part_floats);
+    p.ws_cuts = static_cast<Cut*>(ws);
+    p.ws_o = reinterpret_cast<float*>(p.ws_cuts + p.workers);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + 2 * p.workers * plan.part_floats);
   }
-  const unsigned units = static_cast<unsigned>(p.capacity ? p.capacity : plan.units);
+  const unsigned units = static_cast<unsigned>(p.workers ? p.workers : plan.units);
   cudaLaunchAttribute attr[1];
   cudaError_t e;
   if (plan.pairs) {
@@ -271,20 +272,15 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
     kernel<<<units, block::kThreads, block::kSmemBytes, stream>>>(p);
     e = cudaSuccess;
   }
-  if (e == cudaSuccess && p.capacity) {
+  if (e == cudaSuccess && p.workers > 1) {
     const idx_status_t launched = check_launch(fn);
     if (launched != IDX_OK) return launched;
-    // Launched while the parts run: its blocks wait at their first reads for the parts' end. A warp takes some four of
-    // the parts that a row has on average.
-    const int64_t each = p.head_blocks * (plan.pairs ? pair::kHalves : 1);
-    const int64_t parts = p.capacity / std::max<int64_t>(std::min<int64_t>(p.T, plan.units / each) * each, 1);
-    const int warps = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
-    auto* join = plan.pairs ? join_kernel<true>(warps) : join_kernel<false>(warps);
-    const int64_t items = static_cast<int64_t>(p.T) * p.H * (plan.pairs ? pair::kHalves : 1), per = kJoinWarps / warps;
+    // launched while the parts run: its blocks wait at their first reads for the parts' end
+    auto* join = plan.pairs ? paged_join_kernel<true> : paged_join_kernel<false>;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((items + per - 1) / per));
+    cfg.gridDim = dim3(static_cast<unsigned>(kJoinBlocks * device_sm_count()));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -317,7 +313,7 @@ using namespace idx;
 
 extern "C" size_t idx_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t H) {
   if (T <= 0 || B <= 0 || H <= 0 || H > IDX_ATTENTION_MAX_HEADS) return 0;
-  return static_cast<size_t>(plan_bytes(plan_of(T, B, H), B));
+  return static_cast<size_t>(plan_bytes(plan_of(T, B, H)));
 }
 
 extern "C" idx_status_t idx_window_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache,

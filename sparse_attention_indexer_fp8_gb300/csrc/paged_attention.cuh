@@ -17,7 +17,8 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // depend on the reference; with 2^31 tokens of values below 2^17, O stays below 2^88.
 constexpr float kRescaleStep = 40.0f;
 constexpr int kAhead = 4;                        // tiles between the L2 prefetch and the loads
-constexpr int kMaxSplitRequests = 160;           // of a call whose contexts are split
+constexpr int kMaxSharedRequests = 160;          // of a call whose work is shared out evenly
+constexpr int kUnitTiles = 6;                    // a unit's start and end, in tiles
 constexpr int kJoinTiles = 3;                    // a part's extra stores and the join, in tiles
 
 // Bit 0: a visible page outside the table or the cache (its tokens are skipped). Bit 1: a wait expired.
@@ -48,10 +49,17 @@ struct PagedParams {
   int page_shift;              // log2(block_size)
   int head_blocks, heads;      // groups of heads, and the heads of one
   int tokens;                  // query rows of a unit
-  int capacity;                // parts that there is room for; 0: contexts are not split
-  int2* ws_sched;              // [B]: first part of a request and its parts a unit
-  float2* ws_ml;               // [capacity, rows of a part]: maximum (log2 units) and sum
-  float* ws_o;                 // [capacity, rows of a part, dims of a part]: accumulators
+  int workers;                 // blocks (pairs) that share the work out evenly; 0: a block (pair) a unit
+  struct Cut* ws_cuts;         // [workers]
+  float2* ws_ml;               // [2 workers, rows of a part]: maximum (log2 units) and sum
+  float* ws_o;                 // [2 workers, rows of a part, dims of a part]: accumulators
+};
+
+// The unit that the end of a worker's share cuts, if the worker has its first part: for the join.
+struct alignas(16) Cut {
+  int row0, rows, head0, heads, half;
+  int parts;  // 0: none
+  int unused[2];
 };
 
 // A unit of work: consecutive query rows of one request with one group of heads, and a range of the tiles of the
@@ -67,7 +75,9 @@ struct Unit {
   int skip;                 // tiles from 0 that hold the first tokens; the others start at tile_lo
   int tile_lo;
   int tile0, tiles;         // this part's range
-  int part, parts;          // global number of the part (of a split context), and the parts of the unit
+  int part;                 // number of the part; -1: the unit is whole
+  int parts;                // of the unit
+  bool any;                 // false: there is no unit left
 };
 
 __device__ __forceinline__ int row_at(const PagedParams& p, int b) {
@@ -107,54 +117,78 @@ __device__ __forceinline__ int most_tiles(const PagedParams& p, int n, int ctx) 
   return max(static_cast<int>(min(static_cast<int64_t>(all), near + (min(p.sinks, ctx) + kTile - 1) / kTile)), 1);
 }
 
-// The block's (pair's) unit, found by every warp for itself; false: there is none. `kHalves`: units that share
-// their rows. All lanes get the same.
+// Completes a unit of rows from `start` on, of a request whose n new rows begin at row `at`; its tiles are [u.tile0,
+// u.tile0 + u.tiles) as far as there are as many. False: it has no row.
+template <bool kTree>
+__device__ __forceinline__ bool complete_unit(const PagedParams& p, int at, int n, int start, Unit& u) {
+  if (start >= n) return false;
+  u.row0 = at + start;
+  u.rows = min(p.tokens, n - start);
+  u.heads = min(p.heads, p.H - u.head0);
+  u.ctx = max(u.ctx, 0);
+  u.base = u.ctx - n;
+  u.pos0 = u.base + start;
+  const int all = seen_tiles<kTree>(p, start, start + u.rows - 1, u);
+  if (u.ctx > table_tokens(p) && threadIdx.x == 0) atomicOr(&g_paged_error, 1u);
+  u.tiles = max(min(u.tiles, all - u.tile0), 0);
+  return true;
+}
+
+// Unit number `index` of the grid; false: there is none. All lanes get the same. `kHalves`: units that share their rows.
 template <bool kTree, int kHalves>
 __device__ __forceinline__ bool find_unit(const PagedParams& p, int index, Unit& u) {
-  const int lane = threadIdx.x & 31;
-  const int U = p.tokens;
-  int group, at, n;
-  if (p.capacity == 0) {
-    // Groups of U rows of all requests have numbers: those of request b start at floor(cu_rows[b] / U) + b, which
-    // leaves room for its last, part-filled one.
-    u.half = index % kHalves;
-    u.head0 = index / kHalves % p.head_blocks * p.heads;
-    const int g = index / kHalves / p.head_blocks;
-    int lo = 0, hi = p.B;  // the last b with a first group <= g, 32 candidates a round
-    while (true) {
-      const int step = (hi - lo + 31) / 32, b = lo + lane * step;
-      int first = 0, next = 0, ctx = 0;
-      if (b < hi) {
-        first = row_at(p, b);
-        if (step == 1) {  // the last round: what is needed of the request comes along
-          next = row_at(p, b + 1);
-          ctx = __ldg(p.ctx_lens + b);
-        }
+  const int lane = threadIdx.x & 31, U = p.tokens;
+  // Groups of U rows of all requests have numbers: those of request b start at floor(cu_rows[b] / U) + b, which
+  // leaves room for its last, part-filled one.
+  u.half = index % kHalves;
+  u.head0 = index / kHalves % p.head_blocks * p.heads;
+  const int g = index / kHalves / p.head_blocks;
+  int at, n, lo = 0, hi = p.B;  // the last b with a first group <= g, 32 candidates a round
+  while (true) {
+    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+    int first = 0, next = 0, ctx = 0;
+    if (b < hi) {
+      first = row_at(p, b);
+      if (step == 1) {  // the last round: what is needed of the request comes along
+        next = row_at(p, b + 1);
+        ctx = __ldg(p.ctx_lens + b);
       }
-      const int src = __popc(__ballot_sync(0xFFFFFFFFu, b < hi && first / U + b <= g)) - 1;
-      if (src < 0) return false;
-      lo += src * step;
-      if (step == 1) {
-        at = __shfl_sync(0xFFFFFFFFu, first, src);
-        n = __shfl_sync(0xFFFFFFFFu, next, src) - at;
-        u.ctx = __shfl_sync(0xFFFFFFFFu, ctx, src);
-        break;
-      }
-      hi = min(lo + step, hi);
     }
-    u.request = lo;
-    group = g - at / U - lo;
-    u.part = 0;
-    u.parts = 1;
-  } else {
-    // Every request's units are cut into parts of `per` tiles, `per` the same for all and about the smallest with
-    // which one wave has room for all parts.
-    constexpr int kPer = kMaxSplitRequests / 32;
-    int first[kPer], rows[kPer], ctxs[kPer], units[kPer], most[kPer];
+    const int src = __popc(__ballot_sync(0xFFFFFFFFu, b < hi && first / U + b <= g)) - 1;
+    if (src < 0) return false;
+    lo += src * step;
+    if (step == 1) {
+      at = __shfl_sync(0xFFFFFFFFu, first, src);
+      n = __shfl_sync(0xFFFFFFFFu, next, src) - at;
+      u.ctx = __shfl_sync(0xFFFFFFFFu, ctx, src);
+      break;
+    }
+    hi = min(lo + step, hi);
+  }
+  u.request = lo;
+  u.part = -1;
+  u.tile0 = 0;
+  u.tiles = INT32_MAX;
+  return complete_unit<kTree>(p, at, n, (g - at / U - lo) * U, u);
+}
+
+// All units of a call in one line, request after request, each as long as its tiles, and where there are more units than
+// workers, as what its start and end cost besides; every worker gets the same share of the line. Only the line's cuts
+// split a unit. It is computed by one warp from the lengths, which the host does not know.
+template <bool kTree, int kHalves>
+struct Line {
+  static constexpr int kPer = kMaxSharedRequests / 32;  // requests of a lane: b = 32 k + lane
+  int first[kPer], rows[kPer], ctxs[kPer], units[kPer], length[kPer];
+  int64_t start[kPer];  // of the request's units
+  int64_t total, share;
+  int extra;  // of a unit's length, the part that is not tiles
+
+  __device__ __forceinline__ explicit Line(const PagedParams& p) {
+    const int lane = threadIdx.x & 31, used = (p.B + 31) / 32;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int b = 32 * k + lane;
       first[k] = rows[k] = ctxs[k] = 0;
+      const int b = 32 * k + lane;
       if (b < p.B) {
         first[k] = row_at(p, b);
         rows[k] = row_at(p, b + 1);
@@ -162,88 +196,163 @@ __device__ __forceinline__ bool find_unit(const PagedParams& p, int index, Unit&
       }
     }
     int64_t sum = 0;
-    int longest = 1;
+    int longest = 1, all = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
+      units[k] = length[k] = 0;
+      if (k >= used) continue;
       rows[k] -= first[k];
-      units[k] = most[k] = 0;
       if (rows[k] > 0) {
-        units[k] = (rows[k] + U - 1) / U * p.head_blocks * kHalves;
-        most[k] = most_tiles<kTree>(p, rows[k], max(ctxs[k], 0));
+        units[k] = (rows[k] + p.tokens - 1) / p.tokens * p.head_blocks * kHalves;
+        length[k] = most_tiles<kTree>(p, rows[k], max(ctxs[k], 0));
       }
-      sum += static_cast<int64_t>(units[k]) * most[k];
-      longest = max(longest, most[k]);
+      all += units[k];
+      sum += static_cast<int64_t>(units[k]) * length[k];
+      longest = max(longest, length[k]);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-    int per = static_cast<int>(min(max((sum + p.capacity - 1) / p.capacity, int64_t{1}), static_cast<int64_t>(longest)));
-    int count[kPer];
-    while (true) {
-      if (per + kJoinTiles >= longest) per = longest;  // whole contexts cost less than parts and their join
-      int total = 0;
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    extra = all > p.workers ? kUnitTiles : 0;
+    sum += static_cast<int64_t>(all) * extra;
+    // A share is the workers' part of the line, or where the 128 KB that every part stores and the join reads (0.04 us at
+    // 6.6 TB/s) cost as much as one more tile for each (1.6 us).
+    const float least = 0.5f + sqrtf(0.025f * static_cast<float>(sum));
+    share = static_cast<int64_t>(fmaxf(static_cast<float>(sum) / static_cast<float>(p.workers), least));
+    while (share * p.workers < sum) ++share;  // what the rounding took
+    // With fewer units than workers, a share may begin in one unit and end in another, and has two starts and ends. Where
+    // that costs more, units are lengthened to whole numbers of shares: of `per` tiles, the fewest with which all have room,
+    // or all of the longest.
+    int per = 0;
+    if (all <= p.workers) {
+      per = min(static_cast<int>(share), longest);
+      while (true) {
+        if (per + kJoinTiles >= longest) per = longest;  // whole contexts cost less than parts and their join
+        int total_parts = 0;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        count[k] = (most[k] + per - 1) / per;
-        total += units[k] * count[k];
+        for (int k = 0; k < kPer; ++k) {
+          if (k < used) total_parts += units[k] * ((length[k] + per - 1) / per);
+        }
+        total_parts = __reduce_add_sync(0xFFFFFFFFu, total_parts);
+        if (total_parts <= p.workers || per == longest) break;
+        per += max(per / 8, 1);
       }
-      total = __reduce_add_sync(0xFFFFFFFFu, total);
-      if (total <= p.capacity || per == longest) break;
-      per += max(per / 8, 1);
+      if (per > share + kUnitTiles) per = 0;
     }
-    int before = 0, found_at = 0, found_units = 0, found_parts = 0;
-    u.request = -1;
+    if (per) share = per;
+    int64_t before = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int mine = units[k] * count[k];
-      int upto = mine;
+      start[k] = 0;
+      if (k >= used) continue;
+      length[k] = per ? (length[k] + per - 1) / per * per : length[k] + extra;
+      const int64_t mine = static_cast<int64_t>(units[k]) * length[k];
+      int64_t upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
         if (lane >= d) upto += o;
       }
-      const int start = before + upto - mine;
-      if (index == 0 && threadIdx.x < 32 && 32 * k + lane < p.B) p.ws_sched[32 * k + lane] = make_int2(start, count[k]);
-      const uint32_t who = __ballot_sync(0xFFFFFFFFu, index >= start && index < start + mine);
+      start[k] = before + upto - mine;
+      before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    total = before;
+  }
+
+  // The unit at `at` of the line: where it starts there, and its length. Sets the unit's request, ctx, half and heads;
+  // `row`, `n` and `from` are the request's first row, its rows, and the unit's first of them.
+  __device__ __forceinline__ int64_t unit_at(const PagedParams& p, int64_t at, Unit& u, int& len, int& row, int& n, int& from) const {
+    const int lane = threadIdx.x & 31, used = (p.B + 31) / 32;
+    int64_t begin = 0;
+    u.request = 0;
+    len = 1;
+    row = n = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (k >= used) continue;
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, at >= start[k] && at < start[k] + static_cast<int64_t>(units[k]) * length[k]);
       if (who) {
         const int src = __ffs(who) - 1;
         u.request = 32 * k + src;
-        found_at = __shfl_sync(0xFFFFFFFFu, start, src);
-        found_units = __shfl_sync(0xFFFFFFFFu, units[k], src);
-        found_parts = __shfl_sync(0xFFFFFFFFu, count[k], src);
-        at = __shfl_sync(0xFFFFFFFFu, first[k], src);
+        begin = __shfl_sync(0xFFFFFFFFu, start[k], src);
+        len = __shfl_sync(0xFFFFFFFFu, length[k], src);
+        row = __shfl_sync(0xFFFFFFFFu, first[k], src);
         n = __shfl_sync(0xFFFFFFFFu, rows[k], src);
         u.ctx = __shfl_sync(0xFFFFFFFFu, ctxs[k], src);
       }
-      before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    if (u.request < 0) return false;
-    const int in = index - found_at, unit = in % found_units;  // units vary fastest: they read the same tokens
+    const int unit = static_cast<int>((at - begin) / len);
     u.half = unit % kHalves;
     u.head0 = unit / kHalves % p.head_blocks * p.heads;
-    group = unit / kHalves / p.head_blocks;
-    u.part = index;
-    u.parts = found_parts;
-    u.tile0 = in / found_units * per;
-    u.tiles = per;
+    from = unit / kHalves / p.head_blocks * p.tokens;
+    return begin + static_cast<int64_t>(unit) * len;
   }
-  const int start = group * U;
-  if (start >= n) return false;
-  u.row0 = at + start;
-  u.rows = min(U, n - start);
-  u.heads = min(p.heads, p.H - u.head0);
-  u.ctx = max(u.ctx, 0);
-  u.base = u.ctx - n;
-  u.pos0 = u.base + start;
-  const int all = seen_tiles<kTree>(p, start, start + u.rows - 1, u);
-  if (u.ctx > table_tokens(p) && threadIdx.x == 0) atomicOr(&g_paged_error, 1u);
-  if (p.capacity == 0) {
-    u.tile0 = 0;
-    u.tiles = all;
-  } else {
-    u.tiles = max(min(u.tiles, all - u.tile0), 0);
+};
+
+// A worker's place on the line, and the end of its share; pos < 0 at first.
+struct Place {
+  int64_t pos, end;
+};
+
+// The worker's next unit, or part of one, found by one warp. False: there is none left.
+template <bool kTree, int kHalves>
+__device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Place& place, Unit& u) {
+  int64_t pos = place.pos, end = place.end;
+  if (p.workers == 0) {
+    place.pos = 0;
+    return pos < 0 && find_unit<kTree, kHalves>(p, worker, u);
   }
-  return true;
+  if (pos >= 0 && pos >= end) return false;
+  const Line<kTree, kHalves> line(p);
+  if (pos < 0) {
+    pos = worker * line.share;
+    place.end = end = min(pos + line.share, line.total);
+    place.pos = pos;
+    if (pos >= end) return false;
+  }
+  int len, row, n, from;
+  const int64_t begin = line.unit_at(p, pos, u, len, row, n, from);
+  const int64_t stop = min(begin + len, end);
+  u.tile0 = max(static_cast<int>(pos - begin) - line.extra, 0);
+  u.tiles = max(static_cast<int>(stop - begin) - line.extra, 0) - u.tile0;
+  // A unit's first part is its worker's last, any other its worker's first.
+  u.part = pos == begin && stop == begin + len ? -1 : pos == begin ? 2 * worker + 1 : 2 * worker;
+  u.parts = static_cast<int>((begin + len - 1) / line.share) - worker + 1;  // where this is the first
+  place.pos = stop;
+  return complete_unit<kTree>(p, row, n, from, u);
+}
+
+// Called by all threads before each unit: the first warp finds it and all get it. `sh.unit` may be overwritten: everybody
+// has passed the end of the last unit.
+template <bool kTree, int kHalves, class S>
+__device__ __forceinline__ Unit fetch_unit(const PagedParams& p, S& sh, int worker, bool first, bool leads) {
+  if (threadIdx.x < 32) {
+    Unit u;
+    Place place = first ? Place{-1, 0} : sh.place;
+    const bool any = next_unit<kTree, kHalves>(p, worker, place, u);
+    u.any = any;
+    __syncwarp();
+    if (threadIdx.x == 0) {
+      sh.unit = u;
+      sh.place = place;
+      if (p.workers && leads) {
+        if (first) p.ws_cuts[worker].parts = 0;
+        if (any && u.part == 2 * worker + 1) {
+          p.ws_cuts[worker] = Cut{u.row0, u.rows, u.head0, u.heads, u.half, u.parts, {0, 0}};
+        }
+      }
+    }
+  }
+  __syncthreads();
+  return sh.unit;
+}
+
+// The thread's number, anew at each call: what is derived from it is not kept in registers from one unit to the next.
+__device__ __forceinline__ int thread_number() {
+  int t;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+  return t;
 }
 
 // First token of the part's tile i.
@@ -268,6 +377,15 @@ __device__ __forceinline__ bool is_block(const PagedParams& p, int entry) {
 
 // The lowest n bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Tokens [lo, hi] are all seen by row t of the unit; most tiles lie within.
+template <bool kTree>
+__device__ __forceinline__ int2 all_seen(const PagedParams& p, const Unit& u, bool have, int t) {
+  if (!have) return make_int2(0, -1);
+  if (kTree) return make_int2(0, u.base - 1);
+  const int pos = u.pos0 + t;
+  return make_int2(pos >= p.window ? pos - p.window + 1 : 0, pos);
+}
 
 // Bit c: whether row t of the unit sees token x + c.
 template <bool kTree>
@@ -299,6 +417,74 @@ __device__ __forceinline__ bool codes_finite(uint32_t codes) {
 }
 __device__ __forceinline__ uint32_t multiplier_bytes(uint32_t codes) {
   return codes_finite(codes) ? __vadd4(codes, 0x78787878u) : 0u;  // exponent field code + 120, as kv_dequant_multiplier
+}
+
+// Two values at once: a * b + c, and a + b.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The largest of 32 logits v * unit, in four chains.
+__device__ __forceinline__ float softmax_top(const uint32_t (&v)[32], float unit) {
+  float top[4];
+  if (unit >= 0.f) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(v[c]);
+#pragma unroll
+    for (int c = 4; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(v[c]));
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(v[c]);
+#pragma unroll
+  for (int c = 4; c < 32; ++c) top[c & 3] = fminf(top[c & 3], __uint_as_float(v[c]));
+  return fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * unit;
+}
+
+// The weights 2^(v * unit - ref) of 32 logits, in pairs as bf16, and their sum before that rounding. One kind of
+// operation after the other: exponentials that wait for each other's sums took twice the time.
+__device__ __forceinline__ float softmax_weights(uint32_t (&v)[32], float unit, float ref, uint32_t (&w)[16]) {
+  const uint64_t unit2 = pack2(unit, unit), ref2 = pack2(-ref, -ref);
+  float x[32];
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), unit2, ref2), x[c], x[c + 1]);
+  }
+#pragma unroll
+  for (int c = 0; c < 32; ++c) x[c] = exp2_approx(x[c]);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(x[c], x[c + 1]));
+    const __nv_bfloat162 e = __floats2bfloat162_rn(x[c], x[c + 1]);
+    w[c / 2] = *reinterpret_cast<const uint32_t*>(&e);
+  }
+  float a, b;
+  unpack2(add2(sum[0], sum[1]), a, b);
+  return a + b;
+}
+
+// Eight e4m3 dims to bf16, times the multiplier.
+__device__ __forceinline__ uint4 dequant8(const uint2& x, uint32_t mul) {
+  uint4 w;
+  kv_dequant4_signs(x.x, mul, w.x, w.y);
+  kv_dequant4_signs(x.y, mul, w.z, w.w);
+  return w;
 }
 
 // Bounded wait. A wait that takes two seconds marks the block dead and raises the device

@@ -31,7 +31,6 @@ constexpr int kLoaderWarps = 16;
 constexpr int kGroupWarps = kLoaderWarps / kStages;  // each stage has its own group of loader warps
 constexpr int kTokensPerWarp = kTile / kGroupWarps;
 static_assert(kTokensPerWarp == 8, "a loader warp's tokens are eight rows of the swizzle, within one page");
-constexpr int kEarly = 3;  // of a warp's tokens, those converted while the stage is still in use
 constexpr int kMmaWarp = 4 + kLoaderWarps;
 constexpr int kRopeWarp = kMmaWarp + 1;          // one per stage
 constexpr int kThreads = (kRopeWarp + kStages) * 32;
@@ -53,7 +52,8 @@ struct Shared {
   alignas(8) uint8_t poison[kStages][kGroupWarps];  // and not finite
   float xchg[2][128];
   float inv[kRows];                              // 1 / sum of each row
-  Unit unit;                                     // for the end: the roles' registers are all taken
+  Unit unit;
+  Place place;
 };
 
 constexpr int kSmemBytes = kQBytes + kStages * kStageBytes + kPieceBytes + 1024 + static_cast<int>(sizeof(Shared));
@@ -64,7 +64,8 @@ __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 2, %0;" 
 // The softmax warps and the matrix warp: tensor memory is there (and every row of Q copied).
 __device__ __forceinline__ void tmem_bar() { asm volatile("bar.sync 3, 160;" ::: "memory"); }
 
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The two warps with either half of a tile's tokens for the same 32 rows.
+__device__ __forceinline__ void row_bar(int which) { asm volatile("bar.sync %0, 64;" ::"r"(4 + which) : "memory"); }
 
 template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedParams p) {
@@ -75,16 +76,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
   uint8_t* p_s = k_s + kStages * kStageBytes;
   Shared& sh = *reinterpret_cast<Shared*>(p_s + kPieceBytes);
 
+  if (p.workers) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
+  bool started = false;
+  for (bool first = true;; first = false) {
+  const Unit u = fetch_unit<kTree, 1>(p, sh, blockIdx.x, first, true);
+  if (!u.any) break;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (p.capacity) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
-  Unit u;
-  if (!find_unit<kTree, 1>(p, blockIdx.x, u)) return;
   const int tiles = u.tiles;
   // query row r of the unit: head r % heads of token r / heads
   auto q_row_of = [&](int r) { return r / p.heads; };
 
   if (tiles == 0) {
-    if (u.parts > 1) {
+    if (u.part >= 0) {
       if (tid < kRows) p.ws_ml[static_cast<int64_t>(u.part) * kRows + tid] = make_float2(-INFINITY, 0.f);
     } else {
       for (int i = tid; i < u.rows * u.heads * (kKvLatent / 8); i += kThreads) {
@@ -94,10 +97,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       }
       if (p.lse && tid < u.rows * u.heads) p.lse[(u.row0 + tid / u.heads) * p.ld_lse + u.head0 + tid % u.heads] = -INFINITY;
     }
-    return;
+    __syncthreads();
+    continue;
   }
 
-  if (tid == 0) sh.unit = u;
   // Barriers and tensor memory are set up by the matrix warp; every role first does what needs neither.
   uint32_t tmem = 0;
   auto setup = [&]() {
@@ -149,13 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     };
     // eight dims in half h of the token with these multipliers
     auto word_of = [&](int j) { return __shfl_sync(0xFFFFFFFFu, mults, j); };
-    auto convert = [&](const uint2& x, uint32_t word, uint32_t h) {
-      const uint32_t mul = __byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)) * 0x00800080u;
-      uint4 w;
-      kv_dequant4_even_odd(x.x, mul, w.x, w.y);
-      kv_dequant4_even_odd(x.y, mul, w.z, w.w);
-      return w;
-    };
+    auto mul_of = [&](uint32_t word, uint32_t h) { return __byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)) * 0x00800080u; };
     const uint32_t unit = smem_u32(k_s) + group * kStageBytes + (lane >> 3) * kPieceBytes + r0 * 128 + 16 * (lane & 7);
 
     int next_block;
@@ -174,21 +171,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     for (int i = group; i < tiles; i += kStages) {
       mults = multiplier_bytes(next_codes);
       const uint32_t bad = __ballot_sync(0xFFFFFFFFu, mults == 0u) & now;
-      uint4 early[kEarly][2];
-#pragma unroll
-      for (int j = 0; j < kEarly; ++j) {
-        const uint32_t word = word_of(j);
-        early[j][0] = convert(raw[j][0], word, 0);
-        early[j][1] = convert(raw[j][1], word, 1);
-      }
       if (i >= kStages) wait_for(sh, &sh.o_done[group], ((i >> 1) - 1) & 1);
 #pragma unroll
       for (int j = 0; j < kTokensPerWarp; ++j) {
-        const uint32_t word = j < kEarly ? 0u : word_of(j);
+        const uint32_t word = word_of(j);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          st_shared16(unit + 4 * h * kPieceBytes + j * 128, j < kEarly ? early[j % kEarly][h] : convert(raw[j][h], word, h));
-        }
+        for (int h = 0; h < 2; ++h) st_shared16(unit + 4 * h * kPieceBytes + j * 128, dequant8(raw[j][h], mul_of(word, h)));
       }
       if (lane == 0) {
         // O of tile i - 2, waited for above, was issued once its softmax had read this place
@@ -275,6 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
+      if (started) {
+        // nobody waits any more: all warps have passed the last unit's end
+        for (uint64_t* bar = &sh.q_full; bar < reinterpret_cast<uint64_t*>(&sh.tmem); ++bar) mbar_inval(bar);
+      } else {
+        sh.dead = 0;
+      }
       mbar_init(&sh.q_full, 4);
       mbar_init(&sh.drained, 1);
       for (int i = 0; i < kStages; ++i) {
@@ -283,12 +277,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
         mbar_init(&sh.p_full[i], 4);
         mbar_init(&sh.o_done[i], 1);
       }
-      sh.dead = 0;
       fence_mbar_init();
     }
     __syncwarp();
-    tmem_alloc(&sh.tmem, kTmemCols);
-    tmem_relinquish();
+    if (!started) {
+      tmem_alloc(&sh.tmem, kTmemCols);
+      tmem_relinquish();
+    }
     tc_fence_before();
     tmem_bar();
     setup();
@@ -369,21 +364,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------------- softmax
-    // Q, sixteen rows a warp, rows past the unit's last one zero, all copies out at once. The latent dims
-    // are then put into the loaders' order, 0, 2, 1, 3 of every four, and as many of them as there are columns
-    // into tensor memory: S reads less of the shared memory that the loaders and O want too.
-    const uint32_t q_row = smem_u32(q_s) + 16 * warp * 128;
+    // Q, sixteen rows a warp, rows past the unit's last one zero, all copies out at once; then as many pieces as there
+    // are columns into tensor memory: S reads less of the shared memory that the loaders and O want too. Lane l < 16
+    // finds row l.
+    {
+      const int qr = 16 * warp + (lane & 15), qt = q_row_of(qr), qh = qr - qt * p.heads;
+      const uint8_t* src = qt < u.rows && qh < u.heads
+                               ? reinterpret_cast<const uint8_t*>(p.q + (u.row0 + qt) * p.ld_q + (u.head0 + qh) * p.ld_qh)
+                               : nullptr;
+      const uint32_t q_row = smem_u32(q_s) + 16 * warp * 128;
 #pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      const int r = 16 * warp + i, t = q_row_of(r), h = r - t * p.heads;
-      const bool have = t < u.rows && h < u.heads;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q + (have ? (u.row0 + t) * p.ld_q + (u.head0 + h) * p.ld_qh : 0));
-      const uint32_t at = q_row + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
-      copy16_if(at + (lane >> 3) * kPieceBytes, src + 16 * lane, have);
-      copy16_if(at + (4 + (lane >> 3)) * kPieceBytes, src + 512 + 16 * lane, have);
-      if (lane < 8) copy16_if(at + 8 * kPieceBytes, src + 1024 + 16 * lane, have);
+      for (int i = 0; i < 16; ++i) {
+        const uint8_t* row = shfl_ptr(src, i);
+        const bool have_row = row != nullptr;
+        const uint8_t* from = (have_row ? row : reinterpret_cast<const uint8_t*>(p.q)) + 16 * lane;
+        const uint32_t at = q_row + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
+        copy16_if(at + (lane >> 3) * kPieceBytes, from, have_row);
+        copy16_if(at + (4 + (lane >> 3)) * kPieceBytes, from + 512, have_row);
+        if (lane < 8) copy16_if(at + 8 * kPieceBytes, from + 1024, have_row);
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
     tmem_bar();
     tc_fence_after();
     tmem = sh.tmem;
@@ -391,32 +393,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     const int t = q_row_of(r), h = r - t * p.heads;
     const bool have = t < u.rows && h < u.heads;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    auto reorder = [](const uint4& v) {
-      return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
-                        __byte_perm(v.z, v.w, 0x7632));
-    };
     const uint32_t own_row = smem_u32(q_s) + r * 128;
-#pragma unroll 1
+#pragma unroll 2
     for (int x = 0; x < 8 * kQTmemPieces; x += 4) {
       uint32_t w[16];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const uint4 v = reorder(ld_shared16(own_row + (x >> 3) * kPieceBytes + ((((x + y) & 7) ^ (r & 7)) << 4)));
+        const uint4 v = ld_shared16(own_row + (x >> 3) * kPieceBytes + ((((x + y) & 7) ^ (r & 7)) << 4));
         w[4 * y] = v.x;
         w[4 * y + 1] = v.y;
         w[4 * y + 2] = v.z;
         w[4 * y + 3] = v.w;
       }
       tmem_st16(lanes + kQCols + 4 * x, w);
-    }
-    // of the latent pieces that stay in shared memory, each thread has half a row
-#pragma unroll
-    for (int c = kQTmemPieces; c < kKvLatent / 64; ++c) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t at = own_row + c * kPieceBytes + (((4 * half + x) ^ (r & 7)) << 4);
-        st_shared16(at, reorder(ld_shared16(at)));
-      }
     }
     tmem_wait_st();
     setup();
@@ -428,11 +417,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     };
     arrive(&sh.q_full);
 
+    const int2 all = all_seen<kTree>(p, u, have, t);
     float m = -INFINITY, l = 0.f;                     // maximum (log2 units) that P and O refer to; this half's sum
     bool poisoned = false;                            // the row sees a token that is not finite
     for (int i = 0; i < tiles; ++i) {
       const int st = i & 1;
-      uint32_t seen = have ? row_sees<kTree>(p, u, t, tile_start(u, i) + 32 * half) : 0u;
+      const int x = tile_start(u, i) + 32 * half;
+      uint32_t seen = 0xFFFFFFFFu;
+      if (x < all.x || x + 31 > all.y) seen = have ? row_sees<kTree>(p, u, t, x) : 0u;
       wait_for(sh, &sh.s_full[st], (i >> 1) & 1);
       wait_for(sh, &sh.k_full[st], (i >> 1) & 1);  // long complete: `there` is written
       tc_fence_after();
@@ -446,7 +438,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       // v * unit is the logit in log2 units: the raw products as they are where every token counts, or
       // scaled here with -inf for the others
       float unit = p.scale_log2;
-      float top = -INFINITY;
       if (seen != 0xFFFFFFFFu) {
         unit = 1.0f;
 #pragma unroll
@@ -454,17 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
           v[c] = (seen >> c) & 1u ? __float_as_uint(__uint_as_float(v[c]) * p.scale_log2) : 0xFF800000u;
         }
       }
-      if (unit >= 0.f) {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-      } else {
-        top = INFINITY;
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) top = fminf(top, fminf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-      }
-      top *= unit;
+      float top = softmax_top(v, unit);
       sh.xchg[st][tid] = top;
-      softmax_bar();
+      row_bar(warp & 1);
       top = fmaxf(top, sh.xchg[st][tid ^ 64]);
       // P and O keep an old reference until the maximum has risen by 2^40, so hardly a tile rescales O
       const bool rise = top > m + kRescaleStep || (m == -INFINITY && top > -INFINITY);
@@ -493,14 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       // token exactly. l sums them unrounded, so lse keeps its 32 bits.
       const float ref = m == -INFINITY ? 0.f : m;
       uint32_t w[16];
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const float e0 = exp2_approx(fmaf(__uint_as_float(v[c]), unit, -ref));
-        const float e1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), unit, -ref));
-        l += e0 + e1;
-        const __nv_bfloat162 e = __floats2bfloat162_rn(e0, e1);
-        w[c / 2] = *reinterpret_cast<const uint32_t*>(&e);
-      }
+      l += softmax_weights(v, unit, ref, w);
       const uint32_t p_row = smem_u32(p_s) + r * 128;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -509,12 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       arrive(&sh.p_full[st]);
     }
     if (poisoned) l = __int_as_float(0x7FC00000);
-    softmax_bar();
+    row_bar(warp & 1);
     sh.xchg[0][tid] = l;
-    softmax_bar();
+    row_bar(warp & 1);
     l += sh.xchg[0][tid ^ 64];
     if (half == 0) {
-      const bool split = u.parts > 1;
+      const bool split = u.part >= 0;
       sh.inv[r] = split ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
       if (split) {
         p.ws_ml[static_cast<int64_t>(u.part) * kRows + r] = make_float2(m, l);
@@ -539,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     epilogue_bar();
     tc_fence_after();
     const volatile Unit& e = sh.unit;
-    const bool split = e.parts > 1;
+    const bool split = e.part >= 0;
     tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
     if (warp >= 4) {
       const int quarter = warp & 3, r = (32 * quarter + lane) & 63, half = quarter >> 1;
@@ -549,12 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
         uint32_t o[32];
         tmem_ld_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c, o);
         tmem_wait_ld(o);
-        // A product has 256 dims, 128 to each lane half. Dims 1 and 2 of every four have changed places.
+        // A product has 256 dims, 128 to each lane half.
         const int dim = (c / 128) * 256 + half * 128 + (c % 128);
         if (split) {
           const uint32_t at = smem_u32(k_s) + r * kPitchF32 + dim * 4;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared16(at + 16 * j, make_uint4(o[4 * j], o[4 * j + 2], o[4 * j + 1], o[4 * j + 3]));
+          for (int j = 0; j < 8; ++j) st_shared16(at + 16 * j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
         } else {
           const uint32_t at = smem_u32(k_s) + r * kPitchBf16 + dim * 2;
 #pragma unroll
@@ -562,9 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
             uint32_t w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int c0 = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
-              const __nv_bfloat162 b =
-                  __floats2bfloat162_rn(__uint_as_float(o[c0]) * inv, __uint_as_float(o[c0 + 2]) * inv);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * x]) * inv,
+                                                             __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
               w[x] = *reinterpret_cast<const uint32_t*>(&b);
             }
             st_shared16(at + 16 * j, make_uint4(w[0], w[1], w[2], w[3]));
@@ -573,21 +548,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       }
     }
     epilogue_bar();
-    const int units = split ? kKvLatent / 4 : kKvLatent / 8, pitch = split ? kPitchF32 : kPitchBf16;  // of 16 bytes
+    // a warp stores a row at a time
     const int rows = e.rows * p.heads, row0 = e.row0, heads = e.heads, head0 = e.head0, part = e.part;
-    for (int i = tid; i < rows * units; i += kMmaWarp * 32) {
-      const int r = i / units, x = i % units, t = q_row_of(r), h = r - t * p.heads;
+    for (int r = warp; r < rows; r += kMmaWarp) {
+      const int t = q_row_of(r), h = r - t * p.heads;
       if (h >= heads) continue;
-      uint8_t* dst = split ? reinterpret_cast<uint8_t*>(p.ws_o + (static_cast<int64_t>(part) * kRows + r) * kKvLatent)
-                           : reinterpret_cast<uint8_t*>(p.out + (row0 + t) * p.ld_out + (head0 + h) * p.ld_oh);
-      *reinterpret_cast<uint4*>(dst + 16 * x) = ld_shared16(smem_u32(k_s) + r * pitch + 16 * x);
+      const uint32_t from = smem_u32(k_s) + 16 * lane;
+      if (split) {
+        float* dst = p.ws_o + (static_cast<int64_t>(part) * kRows + r) * kKvLatent + 4 * lane;
+#pragma unroll
+        for (int x = 0; x < kKvLatent / 128; ++x) {
+          *reinterpret_cast<uint4*>(dst + 128 * x) = ld_shared16(from + r * kPitchF32 + 512 * x);
+        }
+      } else {
+        __nv_bfloat16* dst = p.out + (row0 + t) * p.ld_out + (head0 + h) * p.ld_oh + 8 * lane;
+#pragma unroll
+        for (int x = 0; x < kKvLatent / 256; ++x) {
+          *reinterpret_cast<uint4*>(dst + 256 * x) = ld_shared16(from + r * kPitchBf16 + 512 * x);
+        }
+      }
     }
   }
   tc_fence_before();
   __syncwarp();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
+  started = true;
+  }
+  if (started && threadIdx.x / 32 == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
 }
 
 }  // namespace block

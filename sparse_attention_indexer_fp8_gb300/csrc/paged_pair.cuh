@@ -73,7 +73,8 @@ struct Shared {
   alignas(16) uint8_t there[kRing][kTile / 4]; // of four tokens each: low bits, the token is there; high, and not finite
   float xchg[2][2 * kBlockRows];
   float inv[kBlockRows];                         // 1 / sum of each row
-  Unit unit;                                     // for the end: the roles' registers are all taken
+  Unit unit;
+  Place place;
 };
 
 constexpr int kSmemBytes =
@@ -138,18 +139,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxWarps * 32) : "memory"); }
+// The two warps that share a row of tensor-memory lanes: either half of a tile's tokens for the same 32 rows.
+__device__ __forceinline__ void row_bar(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(4 + quarter) : "memory"); }
 
 // The softmax warps and the matrix warp: tensor memory is there.
 __device__ __forceinline__ void tmem_bar() { asm volatile("bar.sync 3, %0;" ::"n"(kSoftmaxWarps * 32 + 32) : "memory"); }
 
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 2, %0;" ::"n"(kMmaWarp * 32) : "memory"); }
-
-// A latent's sixteen-byte unit (eight dims) in the loaders' order: 0, 2, 1, 3 of every four.
-__device__ __forceinline__ uint4 reorder(const uint4& v) {
-  return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
-                    __byte_perm(v.z, v.w, 0x7632));
-}
 
 template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedParams p) {
@@ -161,18 +157,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
   uint8_t* p_s = v_s + kValueStages * kValueBytes;
   Shared& sh = *reinterpret_cast<Shared*>(p_s + kPBytes);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (p.workers) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
+  bool started = false;
+  for (bool first = true;; first = false) {
+  const Unit u = fetch_unit<kTree, kHalves>(p, sh, blockIdx.x / 2, first, cluster_rank() == 0);
+  if (!u.any) break;
+  const int tid = thread_number(), warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());
-  if (p.capacity) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
-  Unit u;
-  if (!find_unit<kTree, kHalves>(p, blockIdx.x / 2, u)) return;
   const int tiles = u.tiles;
   // row r of the block: head r % heads of token first_token + r / heads
   const int first_token = rank * (p.tokens / 2);
   const int64_t part_row = static_cast<int64_t>(u.part) * kRows + rank * kBlockRows;
 
   if (tiles == 0) {
-    if (u.parts > 1) {
+    if (u.part >= 0) {
       if (tid < kBlockRows) p.ws_ml[part_row + tid] = make_float2(-INFINITY, 0.f);
     } else {
       const int rows = max(min(u.rows - first_token, p.tokens / 2), 0) * u.heads;
@@ -186,10 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
         p.lse[(u.row0 + first_token + tid / u.heads) * p.ld_lse + u.head0 + tid % u.heads] = -INFINITY;
       }
     }
-    return;
+    __syncthreads();
+    continue;
   }
 
-  if (tid == 0) sh.unit = u;
   // Barriers and tensor memory are set up by the matrix warp; every role first does what needs neither. Both blocks'
   // barriers exist behind it, and Q is in its place.
   uint32_t tmem = 0;
@@ -250,12 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
         raw_other[k] = load8_if(other + kKvLatent * j + 8 * ((lane & 15) ^ (swizzle | j)), (there >> (4 + j)) & 1u);
       }
     };
-    auto convert = [&](const uint2& x, uint32_t mul) {
-      uint4 w;
-      kv_dequant4_even_odd(x.x, mul, w.x, w.y);
-      kv_dequant4_even_odd(x.y, mul, w.z, w.w);
-      return w;
-    };
     const uint32_t keys = smem_u32(k_s) + group * kKeyBytes + (lane >> 3) * kKeyPiece + r0 * 128 + 16 * (lane & 7);
     // the lanes that hold own tokens' value dims, and where those and the others' go
     const bool value_lane = (lane >> 4) == rank;
@@ -292,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
         uint4 w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          w[h] = convert(raw[j][h], __byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)) * 0x00800080u);
+          w[h] = dequant8(raw[j][h], __byte_perm(word, 0u, 0x4440u + 2 * h + (lane >> 4)) * 0x00800080u);
           st_shared16(keys + 4 * h * kKeyPiece + j * 128, w[h]);
         }
         if (value_lane) st_shared16(own_values + v_off + j * 128, u.half ? w[1] : w[0]);
@@ -301,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
       for (int k = 0; k < 2; ++k) {
         const uint32_t word = __shfl_sync(0xFFFFFFFFu, mults, kPerWarp + 2 * k + (lane >> 4));
         st_shared16(other_values + v_off + 2 * k * 128,
-                    convert(raw_other[k], __byte_perm(word, 0u, 0x4440u + 2 * u.half + rank) * 0x00800080u));
+                    dequant8(raw_other[k], __byte_perm(word, 0u, 0x4440u + 2 * u.half + rank) * 0x00800080u));
       }
       if (lane == 0) {
         // S of tile i - 2 is complete; it was issued once the softmax of tile i - 4 had read this place
@@ -376,6 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
+      if (started) {
+        // nobody waits or arrives any more: all warps of both blocks have passed the last unit's end
+        for (uint64_t* bar = &sh.k_full[0]; bar < reinterpret_cast<uint64_t*>(&sh.tmem); ++bar) mbar_inval(bar);
+      } else {
+        sh.dead = 0;
+      }
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&sh.k_full[i], 2 * (kGroupWarps + 1));
         mbar_init(&sh.s_full[i], 1);
@@ -385,11 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
       mbar_init(&sh.p_full, 2 * kSoftmaxWarps);
       for (int i = 0; i < kRing; ++i) mbar_init(&sh.flags[i], kGroupWarps);
       mbar_init(&sh.drained, 1);
-      sh.dead = 0;
       fence_mbar_init();
     }
     __syncwarp();
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+    if (!started) asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
                  "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(&sh.tmem)), "r"(kTmemCols)
                  : "memory");
     tc_fence_before();
@@ -474,17 +471,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
     const int t = first_token + r / p.heads, h = r % p.heads;
     const bool have = r / p.heads < p.tokens / 2 && t < u.rows && h < u.heads;
     // Q, sixteen rows a warp, rows past the unit's last one zero, all copies out at once: the pieces for tensor memory
-    // into the keys' place for now. The latent dims are then put into the loaders' order.
-#pragma unroll 4
-    for (int x = 0; x < kBlockRows / kSoftmaxWarps; ++x) {
-      const int qr = kBlockRows / kSoftmaxWarps * warp + x, qt = qr / p.heads, qh = qr - qt * p.heads;
+    // into the keys' place for now. Lane l < 16 finds row l.
+    {
+      const int qr = kBlockRows / kSoftmaxWarps * warp + (lane & 15), qt = qr / p.heads, qh = qr - qt * p.heads;
       const bool in = qt < p.tokens / 2 && first_token + qt < u.rows && qh < u.heads;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(
-          p.q + (in ? (u.row0 + first_token + qt) * p.ld_q + (u.head0 + qh) * p.ld_qh : 0));
-      const uint32_t to = (lane >> 3) * kQPiece + qr * 128 + (((lane & 7) ^ (qr & 7)) << 4);
-      copy16_if(smem_u32(k_s) + to, src + 16 * lane, in);
-      copy16_if(smem_u32(q_s) + to, src + 512 + 16 * lane, in);
-      if (lane < 8) copy16_if(smem_u32(q_s) + 4 * kQPiece + to, src + 1024 + 16 * lane, in);
+      const uint8_t* src = in ? reinterpret_cast<const uint8_t*>(p.q + (u.row0 + first_token + qt) * p.ld_q + (u.head0 + qh) * p.ld_qh)
+                              : nullptr;
+      const uint32_t to = (lane >> 3) * kQPiece + kBlockRows / kSoftmaxWarps * warp * 128;
+#pragma unroll 4
+      for (int x = 0; x < kBlockRows / kSoftmaxWarps; ++x) {
+        const uint8_t* row = shfl_ptr(src, x);
+        const bool have_row = row != nullptr;
+        const uint8_t* from = (have_row ? row : reinterpret_cast<const uint8_t*>(p.q)) + 16 * lane;
+        const uint32_t at = to + x * 128 + (((lane & 7) ^ (x & 7)) << 4);
+        copy16_if(smem_u32(k_s) + at, from, have_row);
+        copy16_if(smem_u32(q_s) + at, from + 512, have_row);
+        if (lane < 8) copy16_if(smem_u32(q_s) + 4 * kQPiece + at, from + 1024, have_row);
+      }
     }
     static_assert(kQTmemPieces == 4, "half of the latent pieces");
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -492,30 +495,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
     tc_fence_after();
     tmem = sh.tmem;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    auto place = [&](int x) { return (x >> 3) * kQPiece + r * 128 + (((x & 7) ^ (r & 7)) << 4); };
-#pragma unroll 1
+#pragma unroll 2
     for (int x = 16 * half; x < 16 * half + 16; x += 4) {  // either thread of a row half of its units
       uint32_t w[16];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const uint4 v = reorder(ld_shared16(smem_u32(k_s) + place(x + y)));
+        const uint4 v = ld_shared16(smem_u32(k_s) + ((x + y) >> 3) * kQPiece + r * 128 + ((((x + y) & 7) ^ (r & 7)) << 4));
         w[4 * y] = v.x;
         w[4 * y + 1] = v.y;
         w[4 * y + 2] = v.z;
         w[4 * y + 3] = v.w;
       }
       tmem_st16(lanes + kQCol + 4 * x, w);
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const uint32_t at = smem_u32(q_s) + place(x + y);
-        st_shared16(at, reorder(ld_shared16(at)));
-      }
     }
     tmem_wait_st();
     fence_proxy_async_smem();
     const uint32_t s_free = first_block_addr(&sh.s_free[0]), p_full = first_block_addr(&sh.p_full);
     setup();
 
+    const int2 all = all_seen<kTree>(p, u, have, t);
     float m = -INFINITY, l = 0.f;                     // maximum (log2 units) that P and O refer to; this half's sum
     bool poisoned = false;                            // the row sees a token that is not finite
     int last = kValueStages - 1;                      // stage of the last tile's values
@@ -523,7 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
     for (int i = 0; i < tiles; ++i) {
       const int st = i & 1;
       const uint32_t par = (i >> 1) & 1;
-      uint32_t seen = have ? row_sees<kTree>(p, u, t, tile_start(u, i) + 32 * half) : 0u;
+      const int x = tile_start(u, i) + 32 * half;
+      uint32_t seen = 0xFFFFFFFFu;
+      if (x < all.x || x + 31 > all.y) seen = have ? row_sees<kTree>(p, u, t, x) : 0u;
       wait_for(sh, &sh.s_full[st], par);
       tc_fence_after();
       uint32_t v[32];
@@ -549,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
       // v * unit is the logit in log2 units: the raw products as they are where every token counts, or
       // scaled here with -inf for the others
       float unit = p.scale_log2;
-      float top = -INFINITY;
       if (seen != 0xFFFFFFFFu) {
         unit = 1.0f;
 #pragma unroll
@@ -557,17 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
           v[c] = (seen >> c) & 1u ? __float_as_uint(__uint_as_float(v[c]) * p.scale_log2) : 0xFF800000u;
         }
       }
-      if (unit >= 0.f) {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-      } else {
-        top = INFINITY;
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) top = fminf(top, fminf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-      }
-      top *= unit;
+      float top = softmax_top(v, unit);
       sh.xchg[i & 1][tid] = top;
-      softmax_bar();
+      row_bar(quarter);
       top = fmaxf(top, sh.xchg[i & 1][tid ^ kBlockRows]);
       // P and O keep an old reference until the maximum has risen by 2^40, so hardly a tile rescales O. (With 2^8 a tenth of
       // a warp's tiles did, for 1400 clocks, and each held up the other warps of both blocks.)
@@ -580,14 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
       // token exactly. l sums them unrounded, so lse keeps its 32 bits.
       const float ref = m == -INFINITY ? 0.f : m;
       uint32_t w[16];
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const float e0 = exp2_approx(fmaf(__uint_as_float(v[c]), unit, -ref));
-        const float e1 = exp2_approx(fmaf(__uint_as_float(v[c + 1]), unit, -ref));
-        l += e0 + e1;
-        const __nv_bfloat162 e = __floats2bfloat162_rn(e0, e1);
-        w[c / 2] = *reinterpret_cast<const uint32_t*>(&e);
-      }
+      l += softmax_weights(v, unit, ref, w);
       if (i > 0) {
         // O is complete up to the last tile (for a rescaling), and with it P is free
         wait_for(sh, &sh.o_done[last], last_par);
@@ -617,12 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
       if (++last == kValueStages) last = 0, last_par ^= 1;
     }
     if (poisoned) l = __int_as_float(0x7FC00000);
-    softmax_bar();
+    row_bar(quarter);
     sh.xchg[0][tid] = l;
-    softmax_bar();
+    row_bar(quarter);
     l += sh.xchg[0][tid ^ kBlockRows];
     if (half == 0) {
-      const bool split = u.parts > 1;
+      const bool split = u.part >= 0;
       sh.inv[r] = split ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
       if (split) {
         p.ws_ml[part_row + r] = make_float2(m, l);
@@ -645,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
     epilogue_bar();
     tc_fence_after();
     const volatile Unit& e = sh.unit;
-    const bool split = e.parts > 1;
+    const bool split = e.part >= 0;
     tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
     if (warp >= kFirstLoader) {
       const int quarter = warp & 3, r = 32 * quarter + lane;
@@ -655,11 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
         uint32_t o[32];
         tmem_ld_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c, o);
         tmem_wait_ld(o);
-        // dims 1 and 2 of every four have changed places
         if (split) {
           const uint32_t at = smem_u32(k_s) + r * kPitchF32 + c * 4;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared16(at + 16 * j, make_uint4(o[4 * j], o[4 * j + 2], o[4 * j + 1], o[4 * j + 3]));
+          for (int j = 0; j < 8; ++j) st_shared16(at + 16 * j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
         } else {
           const uint32_t at = smem_u32(k_s) + r * kPitchBf16 + c * 2;
 #pragma unroll
@@ -667,9 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
             uint32_t w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int c0 = 8 * j + 4 * (x >> 1) + (x & 1);  // dims 2 x, 2 x + 1 lie two columns apart
-              const __nv_bfloat162 b =
-                  __floats2bfloat162_rn(__uint_as_float(o[c0]) * inv, __uint_as_float(o[c0 + 2]) * inv);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * x]) * inv,
+                                                             __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
               w[x] = *reinterpret_cast<const uint32_t*>(&b);
             }
             st_shared16(at + 16 * j, make_uint4(w[0], w[1], w[2], w[3]));
@@ -678,25 +660,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pair_kernel(const PagedPara
       }
     }
     epilogue_bar();
-    const int units = split ? kDims / 4 : kDims / 8, pitch = split ? kPitchF32 : kPitchBf16;  // of 16 bytes
+    // a warp stores a row at a time
     const int first = static_cast<int>(cluster_rank()) * (p.tokens / 2);
     const int rows = max(min(e.rows - first, p.tokens / 2), 0) * p.heads, row0 = e.row0 + first;
     const int heads = e.heads, head0 = e.head0, dim0 = e.half * kDims;
     const int64_t part = static_cast<int64_t>(e.part) * kRows + cluster_rank() * kBlockRows;
-    for (int i = tid; i < rows * units; i += kMmaWarp * 32) {
-      const int r = i / units, x = i % units, t = r / p.heads, h = r - t * p.heads;
+    for (int r = warp; r < rows; r += kMmaWarp) {
+      const int t = r / p.heads, h = r - t * p.heads;
       if (h >= heads) continue;
-      uint8_t* dst = split ? reinterpret_cast<uint8_t*>(p.ws_o + (part + r) * kDims)
-                           : reinterpret_cast<uint8_t*>(p.out + (row0 + t) * p.ld_out + (head0 + h) * p.ld_oh + dim0);
-      *reinterpret_cast<uint4*>(dst + 16 * x) = ld_shared16(smem_u32(k_s) + r * pitch + 16 * x);
+      const uint32_t from = smem_u32(k_s) + 16 * lane;
+      if (split) {
+        float* dst = p.ws_o + (part + r) * kDims + 4 * lane;
+#pragma unroll
+        for (int x = 0; x < kDims / 128; ++x) {
+          *reinterpret_cast<uint4*>(dst + 128 * x) = ld_shared16(from + r * kPitchF32 + 512 * x);
+        }
+      } else {
+        *reinterpret_cast<uint4*>(p.out + (row0 + t) * p.ld_out + (head0 + h) * p.ld_oh + dim0 + 8 * lane) =
+            ld_shared16(from + r * kPitchBf16);
+      }
     }
   }
   tc_fence_before();
   __syncwarp();
-  // neither block ends while the other may still arrive in it or read its operands
+  // neither block goes on while the other may still arrive in it or read its operands
   cluster_sync();
   tc_fence_after();
-  if (warp == kMmaWarp) {
+  started = true;
+  }
+  if (started && threadIdx.x / 32 == kMmaWarp) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(kTmemCols) : "memory");
   }
 }
