@@ -3,21 +3,17 @@
 // tokens (idx_tree_attention).
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 
 #include "paged_attention.cuh"
 #include "paged_block.cuh"
-#include "paged_pair.cuh"
 
 namespace idx {
 namespace {
 
 // How a call's rows are cut into units, and the workers among whom they are shared out.
 struct Plan {
-  bool pairs;
   int head_blocks, heads, tokens, workers;
   int64_t units;
-  int64_t part_floats, part_rows;  // of a part: accumulators, maxima and sums
 };
 
 // Joins the parts of the units that the workers' shares cut: weights 2^(m_i - max m), a part without a visible token
@@ -28,13 +24,10 @@ constexpr int kJoinWarps = 8;   // of a block
 constexpr int kJoinBlocks = 2;  // of an SM
 constexpr int kMaxWorkers = kJoinWarps * 32;
 
-template <bool kPair>
 __global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocks) paged_join_kernel(const PagedParams p) {
-  constexpr int kHalves = kPair ? pair::kHalves : 1;
-  constexpr int kDims = kKvLatent / kHalves, kVecs = kDims / 128;
-  constexpr int kPartRows = kPair ? pair::kRows : block::kRows;
+  constexpr int kVecs = kKvLatent / 128;
   __shared__ int ends[kMaxWorkers];  // rows of the cut units up to and with each worker's
-  __shared__ float4 sums[kJoinWarps][kDims / 4];
+  __shared__ float4 sums[kJoinWarps][kKvLatent / 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // every part is complete and visible
   const int cuts = min(p.workers, kMaxWorkers);
@@ -75,17 +68,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocks) paged_join_kerne
       worker = lo;
       const int4* c = reinterpret_cast<const int4*>(p.ws_cuts + worker);
       const int4 c0 = __ldcg(c), c1 = __ldcg(c + 1);
-      cut = Cut{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, {0, 0}};
+      cut = Cut{c0.x, c0.y, c0.z, c0.w, c1.x, {0, 0, 0}};
       const int in = item - (lo > 0 ? ends[lo - 1] : 0);
       t = in / cut.heads;
       h = in - t * cut.heads;
       r = t * p.heads + h;
-      if (kPair) {
-        const int own = p.tokens / 2;
-        r = t / own * pair::kBlockRows + t % own * p.heads + h;
-      }
     }
-    auto place = [&](int i) { return static_cast<int64_t>(2 * (worker + i) + (i == 0 ? 1 : 0)) * kPartRows + r; };
+    auto place = [&](int i) { return static_cast<int64_t>(2 * (worker + i) + (i == 0 ? 1 : 0)) * block::kRows + r; };
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < cut.parts; i += 32) {
       const float2 x = __ldcg(p.ws_ml + place(i));
@@ -111,7 +100,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocks) paged_join_kerne
         x[j] = make_float2(-INFINITY, 0.f);
         if (i >= cut.parts) continue;
         x[j] = __ldcg(p.ws_ml + place(i));
-        const float4* o = reinterpret_cast<const float4*>(p.ws_o + place(i) * kDims) + lane;
+        const float4* o = reinterpret_cast<const float4*>(p.ws_o + place(i) * kKvLatent) + lane;
 #pragma unroll
         for (int c = 0; c < kVecs; ++c) v[j][c] = __ldcg(o + 32 * c);
       }
@@ -148,7 +137,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocks) paged_join_kerne
     if (!have) continue;
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const int64_t q = cut.row0 + t;
-    __nv_bfloat16* dst = p.out + q * p.ld_out + (cut.head0 + h) * p.ld_oh + cut.half * kDims + 4 * lane;
+    __nv_bfloat16* dst = p.out + q * p.ld_out + (cut.head0 + h) * p.ld_oh + 4 * lane;
 #pragma unroll
     for (int c = 0; c < kVecs; ++c) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
@@ -156,64 +145,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocks) paged_join_kerne
       *reinterpret_cast<uint2*>(dst + 128 * c) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
-    if (p.lse && lane == 0 && cut.half == 0) {
+    if (p.lse && lane == 0) {
       p.lse[q * p.ld_lse + cut.head0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
   }
 }
 
-cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, unsigned blocks, cudaStream_t stream) {
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = 2;
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(pair::kThreads);
-  cfg.dynamicSmemBytes = pair::kSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-
-// Pairs that the current device runs at once; 0 when it cannot be queried.
-int device_pairs() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  static int cache[64] = {0};
-  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
-  auto* kernel = pair::paged_pair_kernel<false>;
-  int n = 0;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pair_config(attr, 2, nullptr);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pair::kSmemBytes) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  if (dev >= 0 && dev < 64) cache[dev] = n;
-  return n;
-}
-
 Plan plan_of(int32_t T, int32_t B, int32_t H) {
   Plan plan{};
-  const char* env = getenv("IDX_PAIR");
-  plan.pairs = env ? atoi(env) : static_cast<int64_t>(T) * H >= 256 * static_cast<int64_t>(B);
-  const int rows = plan.pairs ? pair::kBlockRows : block::kRows;
-  plan.head_blocks = (H + rows - 1) / rows;
+  plan.head_blocks = (H + block::kRows - 1) / block::kRows;
   plan.heads = (H + plan.head_blocks - 1) / plan.head_blocks;
-  plan.tokens = rows / plan.heads * (plan.pairs ? 2 : 1);
-  const int each = plan.head_blocks * (plan.pairs ? pair::kHalves : 1);  // units of a group of tokens
-  plan.units = (T / plan.tokens + static_cast<int64_t>(B)) * each;
-  plan.workers = B <= kMaxSharedRequests ? std::min(plan.pairs ? device_pairs() : device_sm_count(), kMaxWorkers) : 0;
-  plan.part_rows = plan.pairs ? pair::kRows : block::kRows;
-  plan.part_floats = plan.part_rows * (plan.pairs ? pair::kDims : kKvLatent);
+  plan.tokens = block::kRows / plan.heads;
+  plan.units = (T / plan.tokens + static_cast<int64_t>(B)) * plan.head_blocks;
+  plan.workers = B <= kMaxSharedRequests ? std::min(device_sm_count(), kMaxWorkers) : 0;
   return plan;
 }
 
 int64_t plan_bytes(const Plan& plan) {
-  return plan.workers * (static_cast<int64_t>(sizeof(Cut)) + 2 * (plan.part_floats * 4 + plan.part_rows * 8));
+  return plan.workers * (static_cast<int64_t>(sizeof(Cut)) + 2 * block::kRows * (kKvLatent * 4 + 8));
+}
+
+// Whether sharing the work out can gain what finding the shares and the join cost (some 4 us). Windows are as long as
+// one another, so it can only where there are so few units that they are cut, and long enough for that; of whole contexts
+// the host does not know the lengths.
+bool worth_sharing(const PagedParams& p, const Plan& plan, bool tree) {
+  if (tree) return true;
+  const int64_t units = std::min<int64_t>(static_cast<int64_t>(p.T) * plan.head_blocks, plan.units);
+  const int64_t tokens = static_cast<int64_t>(p.window) + p.sinks + plan.tokens;
+  const int64_t tiles = std::min<int64_t>(tokens, static_cast<int64_t>(p.n_pages) * p.block_size) / kTile + 1;
+  return 2 * units <= plan.workers && tiles > 2 * kUnitTiles;
 }
 
 // What both calls check and launch; `p` holds what they were given.
@@ -246,37 +206,26 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
   p.head_blocks = plan.head_blocks;
   p.heads = plan.heads;
   p.tokens = plan.tokens;
-  p.workers = ws ? plan.workers : 0;
+  p.workers = ws && worth_sharing(p, plan, tree) ? plan.workers : 0;
+  if (ws && ws_bytes < static_cast<size_t>(plan_bytes(plan))) {
+    return fail(IDX_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %lld are needed", fn, ws_bytes,
+                static_cast<long long>(plan_bytes(plan)));
+  }
   if (p.workers) {
-    if (ws_bytes < static_cast<size_t>(plan_bytes(plan))) {
-      return fail(IDX_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %lld are needed", fn, ws_bytes,
-                  static_cast<long long>(plan_bytes(plan)));
-    }
     p.ws_cuts = static_cast<Cut*>(ws);
     p.ws_o = reinterpret_cast<float*>(p.ws_cuts + p.workers);
-    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + 2 * p.workers * plan.part_floats);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + 2 * static_cast<int64_t>(p.workers) * block::kRows * kKvLatent);
   }
   const unsigned units = static_cast<unsigned>(p.workers ? p.workers : plan.units);
-  cudaLaunchAttribute attr[1];
-  cudaError_t e;
-  if (plan.pairs) {
-    auto* kernel = tree ? pair::paged_pair_kernel<true> : pair::paged_pair_kernel<false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pair::kSmemBytes);
-    if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-    const cudaLaunchConfig_t cfg = pair_config(attr, 2 * units, stream);
-    e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedParams>(p));
-  } else {
-    auto* kernel = tree ? block::paged_block_kernel<true> : block::paged_block_kernel<false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block::kSmemBytes);
-    if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-    kernel<<<units, block::kThreads, block::kSmemBytes, stream>>>(p);
-    e = cudaSuccess;
-  }
+  auto* kernel = tree ? block::paged_block_kernel<true> : block::paged_block_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block::kSmemBytes);
+  if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
+  kernel<<<units, block::kThreads, block::kSmemBytes, stream>>>(p);
   if (e == cudaSuccess && p.workers > 1) {
     const idx_status_t launched = check_launch(fn);
     if (launched != IDX_OK) return launched;
     // launched while the parts run: its blocks wait at their first reads for the parts' end
-    auto* join = plan.pairs ? paged_join_kernel<true> : paged_join_kernel<false>;
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
@@ -285,7 +234,7 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join, static_cast<const PagedParams>(p));
+    e = cudaLaunchKernelEx(&cfg, paged_join_kernel, static_cast<const PagedParams>(p));
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

@@ -49,17 +49,17 @@ struct PagedParams {
   int page_shift;              // log2(block_size)
   int head_blocks, heads;      // groups of heads, and the heads of one
   int tokens;                  // query rows of a unit
-  int workers;                 // blocks (pairs) that share the work out evenly; 0: a block (pair) a unit
+  int workers;                 // blocks that share the work out evenly; 0: a block a unit
   struct Cut* ws_cuts;         // [workers]
-  float2* ws_ml;               // [2 workers, rows of a part]: maximum (log2 units) and sum
-  float* ws_o;                 // [2 workers, rows of a part, dims of a part]: accumulators
+  float2* ws_ml;               // [2 workers, 64 rows]: maximum (log2 units) and sum of a part
+  float* ws_o;                 // [2 workers, 64 rows, 512]: accumulators
 };
 
 // The unit that the end of a worker's share cuts, if the worker has its first part: for the join.
 struct alignas(16) Cut {
-  int row0, rows, head0, heads, half;
+  int row0, rows, head0, heads;
   int parts;  // 0: none
-  int unused[2];
+  int unused[3];
 };
 
 // A unit of work: consecutive query rows of one request with one group of heads, and a range of the tiles of the
@@ -67,7 +67,6 @@ struct alignas(16) Cut {
 struct Unit {
   int request, row0, rows;  // q rows [row0, row0 + rows)
   int head0, heads;
-  int half;                 // which half of the dims, where a unit is one of two
   int pos0;                 // position of the first row
   int base, ctx;            // tokens of the request before its new rows, and with them
   int lo, hi;               // tokens in [0, first) or [lo, hi] are seen by a row
@@ -134,15 +133,14 @@ __device__ __forceinline__ bool complete_unit(const PagedParams& p, int at, int 
   return true;
 }
 
-// Unit number `index` of the grid; false: there is none. All lanes get the same. `kHalves`: units that share their rows.
-template <bool kTree, int kHalves>
+// Unit number `index` of the grid; false: there is none. All lanes get the same.
+template <bool kTree>
 __device__ __forceinline__ bool find_unit(const PagedParams& p, int index, Unit& u) {
   const int lane = threadIdx.x & 31, U = p.tokens;
   // Groups of U rows of all requests have numbers: those of request b start at floor(cu_rows[b] / U) + b, which
   // leaves room for its last, part-filled one.
-  u.half = index % kHalves;
-  u.head0 = index / kHalves % p.head_blocks * p.heads;
-  const int g = index / kHalves / p.head_blocks;
+  const int g = index / p.head_blocks;
+  u.head0 = (index - g * p.head_blocks) * p.heads;
   int at, n, lo = 0, hi = p.B;  // the last b with a first group <= g, 32 candidates a round
   while (true) {
     const int step = (hi - lo + 31) / 32, b = lo + lane * step;
@@ -175,13 +173,14 @@ __device__ __forceinline__ bool find_unit(const PagedParams& p, int index, Unit&
 // All units of a call in one line, request after request, each as long as its tiles, and where there are more units than
 // workers, as what its start and end cost besides; every worker gets the same share of the line. Only the line's cuts
 // split a unit. It is computed by one warp from the lengths, which the host does not know.
-template <bool kTree, int kHalves>
+template <bool kTree>
 struct Line {
   static constexpr int kPer = kMaxSharedRequests / 32;  // requests of a lane: b = 32 k + lane
   int first[kPer], rows[kPer], ctxs[kPer], units[kPer], length[kPer];
-  int64_t start[kPer];  // of the request's units
-  int64_t total, share;
-  int extra;  // of a unit's length, the part that is not tiles
+  int start[kPer];   // of the request's units
+  int total, share;
+  int extra;         // of a unit's length, the part that is not tiles
+  int shift;         // log2 of the tiles that the line's lengths count
 
   __device__ __forceinline__ explicit Line(const PagedParams& p) {
     const int lane = threadIdx.x & 31, used = (p.B + 31) / 32;
@@ -195,7 +194,7 @@ struct Line {
         ctxs[k] = __ldg(p.ctx_lens + b);
       }
     }
-    int64_t sum = 0;
+    float tiles = 0.f;
     int longest = 1, all = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -203,55 +202,66 @@ struct Line {
       if (k >= used) continue;
       rows[k] -= first[k];
       if (rows[k] > 0) {
-        units[k] = (rows[k] + p.tokens - 1) / p.tokens * p.head_blocks * kHalves;
+        units[k] = (rows[k] + p.tokens - 1) / p.tokens * p.head_blocks;
         length[k] = most_tiles<kTree>(p, rows[k], max(ctxs[k], 0));
       }
       all += units[k];
-      sum += static_cast<int64_t>(units[k]) * length[k];
+      tiles += static_cast<float>(units[k]) * static_cast<float>(length[k]);
       longest = max(longest, length[k]);
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     all = __reduce_add_sync(0xFFFFFFFFu, all);
     extra = all > p.workers ? kUnitTiles : 0;
-    sum += static_cast<int64_t>(all) * extra;
+    tiles += static_cast<float>(all) * extra;
+    // lengths count more than one tile where their sum, or the workers' shares, would not fit into 32 bits
+    const float most = fmaxf(tiles, static_cast<float>(p.workers) * static_cast<float>(longest + extra));
+    for (shift = 0; ldexpf(most, -shift) + all > 0x1p30f; ++shift) {
+    }
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (k >= used) continue;
+      length[k] = (length[k] + extra + (1 << shift) - 1) >> shift;
+      sum += units[k] * length[k];
+    }
+    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+    longest = (longest + extra + (1 << shift) - 1) >> shift;
     // A share is the workers' part of the line, or where the 128 KB that every part stores and the join reads (0.04 us at
-    // 6.6 TB/s) cost as much as one more tile for each (1.6 us).
-    const float least = 0.5f + sqrtf(0.025f * static_cast<float>(sum));
-    share = static_cast<int64_t>(fmaxf(static_cast<float>(sum) / static_cast<float>(p.workers), least));
-    while (share * p.workers < sum) ++share;  // what the rounding took
+    // 6.6 TB/s) cost as much as one more tile for each (1.5 us).
+    share = max((sum + p.workers - 1) / p.workers, static_cast<int>(0.5f + sqrtf(0.025f * tiles)) >> shift);
     // With fewer units than workers, a share may begin in one unit and end in another, and has two starts and ends. Where
     // that costs more, units are lengthened to whole numbers of shares: of `per` tiles, the fewest with which all have room,
     // or all of the longest.
     int per = 0;
     if (all <= p.workers) {
-      per = min(static_cast<int>(share), longest);
+      per = min(share, longest);
       while (true) {
         if (per + kJoinTiles >= longest) per = longest;  // whole contexts cost less than parts and their join
-        int total_parts = 0;
+        int parts = 0;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-          if (k < used) total_parts += units[k] * ((length[k] + per - 1) / per);
+          if (k < used) parts += units[k] * ((length[k] + per - 1) / per);
         }
-        total_parts = __reduce_add_sync(0xFFFFFFFFu, total_parts);
-        if (total_parts <= p.workers || per == longest) break;
+        parts = __reduce_add_sync(0xFFFFFFFFu, parts);
+        if (parts <= p.workers || per == longest) break;
         per += max(per / 8, 1);
       }
       if (per > share + kUnitTiles) per = 0;
     }
     if (per) share = per;
-    int64_t before = 0;
+    int before = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       start[k] = 0;
       if (k >= used) continue;
-      length[k] = per ? (length[k] + per - 1) / per * per : length[k] + extra;
-      const int64_t mine = static_cast<int64_t>(units[k]) * length[k];
-      int64_t upto = mine;
+      if (per) length[k] = (length[k] + per - 1) / per * per;
+      const int mine = units[k] * length[k];
+      int upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
         if (lane >= d) upto += o;
       }
       start[k] = before + upto - mine;
@@ -260,18 +270,18 @@ struct Line {
     total = before;
   }
 
-  // The unit at `at` of the line: where it starts there, and its length. Sets the unit's request, ctx, half and heads;
+  // The unit at `at` of the line: where it starts there, and its length. Sets the unit's request, ctx and heads;
   // `row`, `n` and `from` are the request's first row, its rows, and the unit's first of them.
-  __device__ __forceinline__ int64_t unit_at(const PagedParams& p, int64_t at, Unit& u, int& len, int& row, int& n, int& from) const {
+  __device__ __forceinline__ int unit_at(const PagedParams& p, int at, Unit& u, int& len, int& row, int& n, int& from) const {
     const int lane = threadIdx.x & 31, used = (p.B + 31) / 32;
-    int64_t begin = 0;
+    int begin = 0;
     u.request = 0;
     len = 1;
     row = n = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (k >= used) continue;
-      const uint32_t who = __ballot_sync(0xFFFFFFFFu, at >= start[k] && at < start[k] + static_cast<int64_t>(units[k]) * length[k]);
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, at >= start[k] && at - start[k] < units[k] * length[k]);
       if (who) {
         const int src = __ffs(who) - 1;
         u.request = 32 * k + src;
@@ -282,77 +292,70 @@ struct Line {
         u.ctx = __shfl_sync(0xFFFFFFFFu, ctxs[k], src);
       }
     }
-    const int unit = static_cast<int>((at - begin) / len);
-    u.half = unit % kHalves;
-    u.head0 = unit / kHalves % p.head_blocks * p.heads;
-    from = unit / kHalves / p.head_blocks * p.tokens;
-    return begin + static_cast<int64_t>(unit) * len;
+    const int unit = (at - begin) / len, group = unit / p.head_blocks;
+    u.head0 = (unit - group * p.head_blocks) * p.heads;
+    from = group * p.tokens;
+    return begin + unit * len;
   }
 };
 
 // A worker's place on the line, and the end of its share; pos < 0 at first.
 struct Place {
-  int64_t pos, end;
+  int pos, end;
 };
 
 // The worker's next unit, or part of one, found by one warp. False: there is none left.
-template <bool kTree, int kHalves>
+template <bool kTree>
 __device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Place& place, Unit& u) {
-  int64_t pos = place.pos, end = place.end;
+  const bool at_first = place.pos < 0;
   if (p.workers == 0) {
     place.pos = 0;
-    return pos < 0 && find_unit<kTree, kHalves>(p, worker, u);
+    return at_first && find_unit<kTree>(p, worker, u);
   }
-  if (pos >= 0 && pos >= end) return false;
-  const Line<kTree, kHalves> line(p);
-  if (pos < 0) {
-    pos = worker * line.share;
-    place.end = end = min(pos + line.share, line.total);
-    place.pos = pos;
-    if (pos >= end) return false;
+  if (!at_first && place.pos >= place.end) return false;
+  const Line<kTree> line(p);
+  if (at_first) {
+    // the product is within 32 bits: as many shares of the line as there are workers cover it, and little more
+    place.pos = worker * line.share;
+    place.end = min(place.pos + line.share, line.total);
+    if (place.pos >= place.end) return false;
   }
+  const int pos = place.pos;
   int len, row, n, from;
-  const int64_t begin = line.unit_at(p, pos, u, len, row, n, from);
-  const int64_t stop = min(begin + len, end);
-  u.tile0 = max(static_cast<int>(pos - begin) - line.extra, 0);
-  u.tiles = max(static_cast<int>(stop - begin) - line.extra, 0) - u.tile0;
+  const int begin = line.unit_at(p, pos, u, len, row, n, from);
+  const int stop = min(begin + len, place.end);
+  u.tile0 = max(((pos - begin) << line.shift) - line.extra, 0);
+  u.tiles = max(((stop - begin) << line.shift) - line.extra, 0) - u.tile0;
   // A unit's first part is its worker's last, any other its worker's first.
   u.part = pos == begin && stop == begin + len ? -1 : pos == begin ? 2 * worker + 1 : 2 * worker;
-  u.parts = static_cast<int>((begin + len - 1) / line.share) - worker + 1;  // where this is the first
+  u.parts = (begin + len - 1) / line.share - worker + 1;  // where this is the first
   place.pos = stop;
   return complete_unit<kTree>(p, row, n, from, u);
 }
 
 // Called by all threads before each unit: the first warp finds it and all get it. `sh.unit` may be overwritten: everybody
 // has passed the end of the last unit.
-template <bool kTree, int kHalves, class S>
-__device__ __forceinline__ Unit fetch_unit(const PagedParams& p, S& sh, int worker, bool first, bool leads) {
+template <bool kTree, class S>
+__device__ __forceinline__ Unit fetch_unit(const PagedParams& p, S& sh, int worker, bool first) {
   if (threadIdx.x < 32) {
     Unit u;
     Place place = first ? Place{-1, 0} : sh.place;
-    const bool any = next_unit<kTree, kHalves>(p, worker, place, u);
+    const bool any = next_unit<kTree>(p, worker, place, u);
     u.any = any;
     __syncwarp();
     if (threadIdx.x == 0) {
       sh.unit = u;
       sh.place = place;
-      if (p.workers && leads) {
+      if (p.workers) {
         if (first) p.ws_cuts[worker].parts = 0;
         if (any && u.part == 2 * worker + 1) {
-          p.ws_cuts[worker] = Cut{u.row0, u.rows, u.head0, u.heads, u.half, u.parts, {0, 0}};
+          p.ws_cuts[worker] = Cut{u.row0, u.rows, u.head0, u.heads, u.parts, {0, 0, 0}};
         }
       }
     }
   }
   __syncthreads();
   return sh.unit;
-}
-
-// The thread's number, anew at each call: what is derived from it is not kept in registers from one unit to the next.
-__device__ __forceinline__ int thread_number() {
-  int t;
-  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
-  return t;
 }
 
 // First token of the part's tile i.

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
   if (p.workers) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
   bool started = false;
   for (bool first = true;; first = false) {
-  const Unit u = fetch_unit<kTree, 1>(p, sh, blockIdx.x, first, true);
+  const Unit u = fetch_unit<kTree>(p, sh, blockIdx.x, first);
   if (!u.any) break;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = u.tiles;
