@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       if (group + kStages < tiles) find(group + kStages, next_block);
       next_block = lookup(group + 2 * kStages);
     }
-    setup();
+    if (group >= tiles) setup();
     for (int i = group; i < tiles; i += kStages) {
       mults = multiplier_bytes(next_codes);
       const uint32_t bad = __ballot_sync(0xFFFFFFFFu, mults == 0u) & now;
@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
         sh.poison[group][lw] = static_cast<uint8_t>(bad);
       }
       fence_proxy_async_smem();
+      if (i == group) setup();  // the first tile is converted while Q is on its way
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[group]);
       if (i + kStages < tiles) {
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       prefetch(i, 1, entry(i, 1));
     }
     const uint32_t piece = smem_u32(k_s) + group * kStageBytes + (kPieces - 1) * kPieceBytes;
-    setup();
+    if (group >= tiles) setup();
     for (int i = group; i < tiles; i += kStages) {
       const uint8_t* rope[2];
 #pragma unroll
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
+      if (i == group) setup();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[group]);
 #pragma unroll
