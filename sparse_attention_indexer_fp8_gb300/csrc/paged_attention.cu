@@ -165,15 +165,14 @@ int64_t plan_bytes(const Plan& plan) {
   return plan.workers * (static_cast<int64_t>(sizeof(Cut)) + 2 * block::kRows * (kKvLatent * 4 + 8));
 }
 
-// Whether sharing the work out can gain what finding the shares and the join cost (some 4 us). Windows are as long as
-// one another, so it can only where there are so few units that they are cut, and long enough for that; of whole contexts
-// the host does not know the lengths.
+// Whether sharing the work out can gain what finding the shares and the join cost (some 4 us). Units of a few tiles
+// are not worth cutting. Windows are as long as one another, so it can gain only where there are so few units that they
+// are cut; of whole contexts the host does not know the lengths.
 bool worth_sharing(const PagedParams& p, const Plan& plan, bool tree) {
-  if (tree) return true;
-  const int64_t units = std::min<int64_t>(static_cast<int64_t>(p.T) * plan.head_blocks, plan.units);
-  const int64_t tokens = static_cast<int64_t>(p.window) + p.sinks + plan.tokens;
-  const int64_t tiles = std::min<int64_t>(tokens, static_cast<int64_t>(p.n_pages) * p.block_size) / kTile + 1;
-  return 2 * units <= plan.workers && tiles > 2 * kUnitTiles;
+  const int64_t tokens = static_cast<int64_t>(p.n_pages) * p.block_size;
+  const int64_t seen = tree ? tokens : std::min(tokens, static_cast<int64_t>(p.window) + p.sinks + plan.tokens);
+  if (seen / kTile < 2 * kUnitTiles) return false;
+  return tree || 2 * std::min<int64_t>(static_cast<int64_t>(p.T) * plan.head_blocks, plan.units) <= plan.workers;
 }
 
 // What both calls check and launch; `p` holds what they were given.

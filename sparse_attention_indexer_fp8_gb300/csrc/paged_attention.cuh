@@ -1,5 +1,5 @@
-// What the window and tree attention kernels share: the call's parameters, which rows
-// and tokens a block works on, and which of them see each other.
+// What the window and tree attention kernel works on: the call's parameters, how its work is cut into units and shared
+// out, which rows and tokens a unit has and which of them see each other.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -459,8 +459,7 @@ __device__ __forceinline__ float softmax_top(const uint32_t (&v)[32], float unit
   return fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * unit;
 }
 
-// The weights 2^(v * unit - ref) of 32 logits, in pairs as bf16, and their sum before that rounding. One kind of
-// operation after the other: exponentials that wait for each other's sums took twice the time.
+// The weights 2^(v * unit - ref) of 32 logits, in pairs as bf16, and their sum before that rounding.
 __device__ __forceinline__ float softmax_weights(uint32_t (&v)[32], float unit, float ref, uint32_t (&w)[16]) {
   const uint64_t unit2 = pack2(unit, unit), ref2 = pack2(-ref, -ref);
   float x[32];

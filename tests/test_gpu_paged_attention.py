@@ -415,3 +415,54 @@ def test_refusals_of_the_bindings():
     if n:
         with pytest.raises(idx.IdxError, match="workspace has"):
             c.window(10, 0, ws=torch.empty(n - 16, dtype=torch.uint8, device=DEV))
+
+
+def lengths(n, lo, hi, seed):
+    return [int(v) for v in np.random.default_rng(seed).integers(lo, hi + 1, n)]
+
+
+@pytest.mark.parametrize("H,counts,ctxs", [
+    (16, [9, 0, 20, 3] * 11, lengths(44, 20, 900, 1)),          # more units than the GPU has blocks: shares of several units
+    (3, [1] * 100, lengths(100, 1, 2500, 2)),                   # fewer, of lengths that no whole number of parts fits
+    (64, [2, 1, 3], [3000, 40, 9000]),                          # few: a context cut into many parts
+    (2, [1] * 160, lengths(160, 0, 700, 3)), (2, [1] * 161, lengths(161, 0, 700, 4)),  # the most requests that are shared, and more
+    (128, [1, 1], [1500, 1500]), (5, [64, 0, 0, 1], [800, 0, 900, 2000])])
+def test_shared_work(H, counts, ctxs):
+    """The same results with a workspace, where blocks take equal shares of ragged work, as the oracle has."""
+    ctxs = [max(c, n) for c, n in zip(ctxs, counts)]
+    c = Case(H, counts, ctxs, 64, seed=H, before=1, behind=1, extra_pages=20)
+    mask = random_mask(counts, 2, np.random.default_rng(H), 1, 1)
+    c.tree(mask, ws=c.workspace())
+    idx.idx_device_error()
+    c.check(c.tree_seen(mask))
+    c.tree(mask)
+    c.check(c.tree_seen(mask))
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+def test_long_context(bs):
+    """One row over 70 000 tokens, whole and cut: every token counts once, first and last among them."""
+    ctx, H = 70_001, 2
+    c = Case(H, [1], [ctx], bs, seed=2)
+    # all weights alike, values 1 at one dim each
+    c.q.zero_()
+    codes = torch.zeros(c.cache.shape[0], bs, 512, dtype=torch.uint8, device=DEV)
+    order = {int(blk): p for p, blk in enumerate(c.table[0])}
+    dims = np.random.default_rng(3).integers(0, 512, ctx)
+    host = np.zeros((c.cache.shape[0], bs, 512), dtype=np.uint8)
+    for blk, p in order.items():
+        n = min(bs, ctx - p * bs)
+        host[blk, np.arange(n), dims[p * bs:p * bs + n]] = 0x38  # 1.0
+    codes.copy_(torch.from_numpy(host))
+    c.cache[:, :512 * bs] = codes.view(-1, 512 * bs)
+    c.cache[:, 512 * bs:640 * bs] = 0
+    c.cache[:, 640 * bs:644 * bs] = 127
+    want = np.bincount(dims, minlength=512) / ctx
+    for ws in (None, c.workspace()):
+        c.out.fill_(7)
+        c.window(10 ** 9, 0, ws=ws)
+        idx.idx_device_error()
+        got = c.out.double().cpu().numpy()
+        # counts up to 200 of 70001 are exact in the accumulator; 1 / n, one product and the bf16 store round
+        assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -21) * want).all()
+        assert np.abs(c.lse.double().cpu().numpy() - np.log(ctx)).max() <= 2.0 ** -20 * np.log(ctx)
