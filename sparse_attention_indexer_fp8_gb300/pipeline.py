@@ -8,8 +8,9 @@ expansion, sparse logits, sparse top-k with remap, slot conversion), and
 ``DcpDecodeStep`` those of one rank of a context-parallel decode step (scoring
 of the rank's own shard, local top-k with scores, one exchange, merge).
 ``AttentionDecodeStep`` goes from a layer's projections to its attention output
-(both normalised inserts, q preparation, ``DecodeStep``, sparse attention). Buffers
-are allocated once at construction; ``run`` allocates nothing but the exchange's
+(both normalised inserts, q preparation, ``DecodeStep``, sparse attention).
+``TreeStep`` verifies trees of drafted tokens: tables and masks once a step, then a
+layer's insert and its attention over whole contexts. Buffers are allocated once at construction; ``run`` allocates nothing but the exchange's
 receive lists. ``kv="mxfp4"`` selects the MXFP4 indexer cache (the V4.1 format)
 for the cache fill and the decode and hierarchical steps.
 """
@@ -19,10 +20,11 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (idx_dcp_topk_merge, idx_expand_candidates, idx_k_norm_rope_quant_and_cache, idx_k_quant_and_cache,
+from . import (idx_build_tables, idx_dcp_topk_merge, idx_expand_candidates, idx_k_norm_rope_quant_and_cache, idx_k_quant_and_cache,
                idx_k_quant_and_cache_mxfp4, idx_kv_norm_rope_quant_and_cache, idx_paged_mqa_logits_decode,
-               idx_paged_mqa_logits_decode_mxfp4, idx_q_rope_quant, idx_req_to_global_slots, idx_sparse_attention,
-               idx_sparse_attention_workspace_bytes, idx_sparse_topk_remap, idx_topk, idx_workspace_bytes,
+               idx_paged_attention_workspace_bytes, idx_paged_mqa_logits_decode_mxfp4, idx_q_rope_quant, idx_req_to_global_slots, idx_sparse_attention,
+               idx_sparse_attention_workspace_bytes, idx_sparse_topk_remap, idx_topk, idx_tree_attention, idx_tree_mask,
+               idx_workspace_bytes,
                _heads, _mat, _vec)
 from . import workloads as W
 
@@ -254,6 +256,51 @@ class AttentionDecodeStep:
             # the lists of contexts shorter than topk end with -1: nothing past a context's length is looked at
             idx_sparse_attention(q, kv_cache, self.block_size, slots, self.out, self.softmax_scale, lse=self.lse,
                                  n_sel=ctx_lens, ws=self.ws, stream=stream)
+        return self.out
+
+
+class TreeStep:
+    """Verification of drafted trees over the attention cache, for up to ``requests`` requests and ``rows`` new tokens.
+
+    ``plan`` prepares a step from the requests' lengths and the nodes' parents, once for all layers: blocks and slots
+    of the new tokens, their positions (the request's length and the node's depth) and who sees whom. ``layer`` inserts
+    a layer's new tokens and attends to every request's earlier tokens and each node's ancestors. A prompt, or tokens
+    that an earlier step accepted, are nodes whose parent is the one before; the records of dropped nodes are
+    overwritten, and their blocks used again, by the next step over the same ``cached_lens``. Rows behind the last
+    node are padding. Neither call allocates anything.
+    """
+
+    def __init__(self, requests: int, rows: int, heads: int, words: int = 2, block_size: int = W.BLOCK_SIZE, device="cuda",
+                 softmax_scale: float = W.ATTN_HEAD_DIM ** -0.5, eps: float = 1e-6, interleaved: bool = False):
+        self.block_size, self.softmax_scale, self.eps, self.interleaved = block_size, softmax_scale, eps, interleaved
+
+        def ints(*shape, dtype=torch.int32):
+            return torch.zeros(shape, dtype=dtype, device=device)
+
+        self.ctx_lens, self.cu_rows = ints(requests), ints(requests + 1)
+        self.held_pages, self.free_end = ints(requests), ints(1)
+        self.row_positions, self.slots = ints(rows), ints(rows, dtype=torch.int64)
+        self.positions, self.mask = ints(rows), ints(rows, words)
+        self.out = torch.zeros((rows, heads, 512), dtype=torch.bfloat16, device=device)
+        self.lse = torch.zeros((rows, heads), dtype=torch.float32, device=device)
+        with torch.cuda.device(self.out.device):
+            nbytes = idx_paged_attention_workspace_bytes(rows, requests, heads)
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+    def plan(self, cached_lens, new_lens, parents, free_blocks, block_table, held_pages=None, free_start=None, stream=None):
+        """Lengths and ``held_pages`` int32 [requests], ``parents`` int32 [rows] (within the request, -1: none);
+        ``block_table`` is updated. See ``idx_build_tables`` and ``idx_tree_mask``."""
+        idx_build_tables(cached_lens, new_lens, free_blocks, block_table, self.block_size, self.ctx_lens, self.cu_rows,
+                         self.row_positions, self.slots, held_pages=held_pages, held_out=self.held_pages,
+                         free_start=free_start, free_end=self.free_end, stream=stream)
+        idx_tree_mask(parents, self.cu_rows, self.mask, base_lens=cached_lens, positions=self.positions, stream=stream)
+
+    def layer(self, kv, kv_weight, cos_sin, q, kv_cache, block_table, stream=None):
+        """``kv`` [rows, 576] is the attention projection, ``q`` [rows, heads, 576] the absorbed and rotated query."""
+        idx_kv_norm_rope_quant_and_cache(kv[:, :512], kv[:, 512:], kv_weight, self.eps, self.positions, cos_sin, self.slots,
+                                         kv_cache, self.block_size, interleaved=self.interleaved, stream=stream)
+        idx_tree_attention(q, kv_cache, self.block_size, block_table, self.cu_rows, self.ctx_lens, self.mask, self.out,
+                           self.softmax_scale, lse=self.lse, ws=self.ws, stream=stream)
         return self.out
 
 
