@@ -172,6 +172,9 @@ bool worth_sharing(const PagedParams& p, const Plan& plan, bool tree) {
   const int64_t tokens = static_cast<int64_t>(p.n_pages) * p.block_size;
   const int64_t seen = tree ? tokens : std::min(tokens, static_cast<int64_t>(p.window) + p.sinks + plan.tokens);
   if (seen / kTile < 2 * kUnitTiles) return false;
+  // the line's sums stay far within 32 bits
+  const int64_t tiles = std::min(tokens, static_cast<int64_t>(INT32_MAX)) / kTile + 1 + kUnitTiles;
+  if (tiles > (int64_t{1} << 29) / std::max<int64_t>(plan.units, plan.workers)) return false;
   return tree || 2 * std::min<int64_t>(static_cast<int64_t>(p.T) * plan.head_blocks, plan.units) <= plan.workers;
 }
 

@@ -180,7 +180,6 @@ struct Line {
   int start[kPer];   // of the request's units
   int total, share;
   int extra;         // of a unit's length, the part that is not tiles
-  int shift;         // log2 of the tiles that the line's lengths count
 
   __device__ __forceinline__ explicit Line(const PagedParams& p) {
     const int lane = threadIdx.x & 31, used = (p.B + 31) / 32;
@@ -194,8 +193,7 @@ struct Line {
         ctxs[k] = __ldg(p.ctx_lens + b);
       }
     }
-    float tiles = 0.f;
-    int longest = 1, all = 0;
+    int longest = 1, all = 0, sum = 0;  // the host lets no call in whose sums are near 32 bits
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       units[k] = length[k] = 0;
@@ -206,31 +204,19 @@ struct Line {
         length[k] = most_tiles<kTree>(p, rows[k], max(ctxs[k], 0));
       }
       all += units[k];
-      tiles += static_cast<float>(units[k]) * static_cast<float>(length[k]);
+      sum += units[k] * length[k];
       longest = max(longest, length[k]);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     all = __reduce_add_sync(0xFFFFFFFFu, all);
     extra = all > p.workers ? kUnitTiles : 0;
-    tiles += static_cast<float>(all) * extra;
-    // lengths count more than one tile where their sum, or the workers' shares, would not fit into 32 bits
-    const float most = fmaxf(tiles, static_cast<float>(p.workers) * static_cast<float>(longest + extra));
-    for (shift = 0; ldexpf(most, -shift) + all > 0x1p30f; ++shift) {
-    }
-    int sum = 0;
+    sum = __reduce_add_sync(0xFFFFFFFFu, sum) + all * extra;
+    longest += extra;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (k >= used) continue;
-      length[k] = (length[k] + extra + (1 << shift) - 1) >> shift;
-      sum += units[k] * length[k];
-    }
-    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-    longest = (longest + extra + (1 << shift) - 1) >> shift;
+    for (int k = 0; k < kPer; ++k) length[k] += extra;
     // A share is the workers' part of the line, or where the 128 KB that every part stores and the join reads (0.04 us at
     // 6.6 TB/s) cost as much as one more tile for each (1.5 us).
-    share = max((sum + p.workers - 1) / p.workers, static_cast<int>(0.5f + sqrtf(0.025f * tiles)) >> shift);
+    share = max((sum + p.workers - 1) / p.workers, static_cast<int>(0.5f + sqrtf(0.025f * static_cast<float>(sum))));
     // With fewer units than workers, a share may begin in one unit and end in another, and has two starts and ends. Where
     // that costs more, units are lengthened to whole numbers of shares: of `per` tiles, the fewest with which all have room,
     // or all of the longest.
@@ -273,7 +259,7 @@ struct Line {
   // The unit at `at` of the line: where it starts there, and its length. Sets the unit's request, ctx and heads;
   // `row`, `n` and `from` are the request's first row, its rows, and the unit's first of them.
   __device__ __forceinline__ int unit_at(const PagedParams& p, int at, Unit& u, int& len, int& row, int& n, int& from) const {
-    const int lane = threadIdx.x & 31, used = (p.B + 31) / 32;
+    const int used = (p.B + 31) / 32;
     int begin = 0;
     u.request = 0;
     len = 1;
@@ -315,7 +301,7 @@ __device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Plac
   if (!at_first && place.pos >= place.end) return false;
   const Line<kTree> line(p);
   if (at_first) {
-    // the product is within 32 bits: as many shares of the line as there are workers cover it, and little more
+    // as many shares as there are workers cover the line, and little more
     place.pos = worker * line.share;
     place.end = min(place.pos + line.share, line.total);
     if (place.pos >= place.end) return false;
@@ -324,8 +310,8 @@ __device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Plac
   int len, row, n, from;
   const int begin = line.unit_at(p, pos, u, len, row, n, from);
   const int stop = min(begin + len, place.end);
-  u.tile0 = max(((pos - begin) << line.shift) - line.extra, 0);
-  u.tiles = max(((stop - begin) << line.shift) - line.extra, 0) - u.tile0;
+  u.tile0 = max(pos - begin - line.extra, 0);
+  u.tiles = max(stop - begin - line.extra, 0) - u.tile0;
   // A unit's first part is its worker's last, any other its worker's first.
   u.part = pos == begin && stop == begin + len ? -1 : pos == begin ? 2 * worker + 1 : 2 * worker;
   u.parts = (begin + len - 1) / line.share - worker + 1;  // where this is the first
@@ -412,14 +398,11 @@ __device__ __forceinline__ uint32_t row_sees(const PagedParams& p, const Unit& u
   }
 }
 
-// One look at the codes of a token's four scales: a word of multiplier exponents, all zero for a token
-// that is not finite (kKvNanScaleCode). Multiplied by zero it leaves no trace in the products; the softmax makes the
-// rows that see it NaN by a flag, so that it cannot reach the others through 0 * NaN.
-__device__ __forceinline__ bool codes_finite(uint32_t codes) {
-  return __vcmpgtu4(codes, kKvMaxScaleCode * 0x01010101u) == 0u;
-}
+// Multiplier exponents of a token's four scales, code + 120 as in kv_dequant_multiplier; all zero for a token that is
+// not finite (kKvNanScaleCode). Multiplied by zero it leaves no trace in the products; the softmax makes the rows that
+// see it NaN by a flag, so that it cannot reach the others through 0 * NaN.
 __device__ __forceinline__ uint32_t multiplier_bytes(uint32_t codes) {
-  return codes_finite(codes) ? __vadd4(codes, 0x78787878u) : 0u;  // exponent field code + 120, as kv_dequant_multiplier
+  return __vcmpgtu4(codes, kKvMaxScaleCode * 0x01010101u) == 0u ? __vadd4(codes, 0x78787878u) : 0u;
 }
 
 // Two values at once: a * b + c, and a + b.

@@ -466,3 +466,18 @@ def test_long_context(bs):
         # counts up to 200 of 70001 are exact in the accumulator; 1 / n, one product and the bf16 store round
         assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -21) * want).all()
         assert np.abs(c.lse.double().cpu().numpy() - np.log(ctx)).max() <= 2.0 ** -20 * np.log(ctx)
+
+
+@pytest.mark.parametrize("bs,pages", [(128, 2 ** 24 + 3), (64, 2 ** 21)])
+def test_wide_table(bs, pages):
+    """Tables for more tokens than 31 bits count, and for so many that the call's work is not shared out."""
+    c = Case(3, [2, 1], [900, 2000], bs, seed=7)
+    have = c.block_table.shape[1]
+    c.block_table = torch.cat([c.block_table, torch.full((2, pages - have), -1, dtype=torch.int32, device=DEV)], dim=1)
+    mask = random_mask(c.counts, 1, np.random.default_rng(7))
+    c.tree(mask, ws=c.workspace())
+    idx.idx_device_error()
+    c.check(c.tree_seen(mask))
+    c.window(2 ** 31 - 1, 2 ** 31 - 1, ws=c.workspace())
+    idx.idx_device_error()
+    c.check(c.window_seen(2 ** 31 - 1, 2 ** 31 - 1))
