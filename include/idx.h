@@ -835,9 +835,11 @@ idx_status_t idx_tree_mask(const int32_t* parents, const int32_t* cu_rows, int32
  *                block is outside [0, num_blocks), is skipped and raises the device flag.
  *   cu_rows      int32 [B + 1], ascending, within [0, T];  ctx_lens int32 [B].
  *   window >= 1, sinks >= 0.
- *   ws           NULL, or idx_paged_attention_workspace_bytes(T, B, H) bytes, 16-byte aligned: with it the contexts
- *                of a few rows are split over the GPU's SMs and joined by a second launch. Its contents need no
- *                preparation and mean nothing after the call; calls that may overlap need one each.
+ *   ws           NULL, or idx_paged_attention_workspace_bytes(T, B, H) bytes, 16-byte aligned: with it the work of
+ *                up to 160 requests may be shared out evenly over the GPU's SMs, by the lengths on the device; rows
+ *                whose contexts that cuts are joined by a second launch. Its contents need no preparation and mean
+ *                nothing after the call; calls that may overlap need one each. The results depend on the lengths of
+ *                all requests in the last bits then, and are the same in every run.
  * Errors: as idx_sparse_attention, and IDX_ERR_INVALID_ARG for window < 1 or sinks < 0.
  */
 idx_status_t idx_window_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache,

@@ -522,7 +522,7 @@ def idx_tree_mask(parents, cu_rows, mask, base_lens=None, positions=None, stream
 
 
 def idx_paged_attention_workspace_bytes(rows: int, requests: int, heads: int) -> int:
-    """Bytes of the workspace with which the window and tree attention split these rows' contexts (0: they would not)."""
+    """Bytes of the workspace with which the window and tree attention share the work out evenly (0: they would not)."""
     fn = "idx_paged_attention_workspace_bytes"
     return library().idx_paged_attention_workspace_bytes(
         _int32(fn, "rows", rows), _int32(fn, "requests", requests), _int32(fn, "heads", heads))

@@ -17,7 +17,9 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // depend on the reference; with 2^31 tokens of values below 2^17, O stays below 2^88.
 constexpr float kRescaleStep = 40.0f;
 constexpr int kAhead = 4;                        // tiles between the L2 prefetch and the loads
-constexpr int kMaxSharedRequests = 160;          // of a call whose work is shared out evenly
+// Requests of a call whose work is shared out: a warp holds their lengths, five a lane. With ten a lane, the kernel's
+// registers fell out so that every call took 8-10 % longer.
+constexpr int kMaxSharedRequests = 160;
 constexpr int kUnitTiles = 6;                    // a unit's start and end, in tiles
 constexpr int kJoinTiles = 3;                    // a part's extra stores and the join, in tiles
 
@@ -128,7 +130,7 @@ __device__ __forceinline__ bool complete_unit(const PagedParams& p, int at, int 
   u.base = u.ctx - n;
   u.pos0 = u.base + start;
   const int all = seen_tiles<kTree>(p, start, start + u.rows - 1, u);
-  if (u.ctx > table_tokens(p) && threadIdx.x == 0) atomicOr(&g_paged_error, 1u);
+  if (u.ctx > table_tokens(p) && (threadIdx.x & 31) == 0) atomicOr(&g_paged_error, 1u);
   u.tiles = max(min(u.tiles, all - u.tile0), 0);
   return true;
 }
@@ -319,29 +321,21 @@ __device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Plac
   return complete_unit<kTree>(p, row, n, from, u);
 }
 
-// Called by all threads before each unit: the first warp finds it and all get it. `sh.unit` may be overwritten: everybody
-// has passed the end of the last unit.
-template <bool kTree, class S>
-__device__ __forceinline__ Unit fetch_unit(const PagedParams& p, S& sh, int worker, bool first) {
-  if (threadIdx.x < 32) {
-    Unit u;
-    Place place = first ? Place{-1, 0} : sh.place;
-    const bool any = next_unit<kTree>(p, worker, place, u);
-    u.any = any;
-    __syncwarp();
-    if (threadIdx.x == 0) {
-      sh.unit = u;
-      sh.place = place;
-      if (p.workers) {
-        if (first) p.ws_cuts[worker].parts = 0;
-        if (any && u.part == 2 * worker + 1) {
-          p.ws_cuts[worker] = Cut{u.row0, u.rows, u.head0, u.heads, u.parts, {0, 0, 0}};
-        }
-      }
+// One warp finds the worker's unit and leaves it in `unit`; `unit.any` is false after the last.
+template <bool kTree>
+__device__ __forceinline__ void find_next(const PagedParams& p, int worker, bool first, Place& place, Unit& unit) {
+  Unit u;
+  Place at = first ? Place{-1, 0} : place;
+  u.any = next_unit<kTree>(p, worker, at, u);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    unit = u;
+    place = at;
+    if (p.workers) {
+      if (first) p.ws_cuts[worker].parts = 0;
+      if (u.any && u.part == 2 * worker + 1) p.ws_cuts[worker] = Cut{u.row0, u.rows, u.head0, u.heads, u.parts, {0, 0, 0}};
     }
   }
-  __syncthreads();
-  return sh.unit;
 }
 
 // First token of the part's tile i.

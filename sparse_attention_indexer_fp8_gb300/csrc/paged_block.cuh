@@ -1,5 +1,5 @@
-// Window and tree attention of few rows a request: one block per unit of up to 64 query rows (a row is one
-// head of one token), all 512 dims of the values.
+// The kernel of window and tree attention: a block takes units of up to 64 query rows (a row is one head of one token)
+// and some of the tokens that they see, all 512 dims of the values.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -22,6 +22,16 @@ namespace block {
 // What differs: tokens lie in pages, so eight of a warp share one block and one address; rows of several
 // query tokens see different tokens, so each thread of the softmax has its own mask of a tile; and parts of a
 // context are found on the device from the lengths, which the host does not know.
+//
+// What bounds it: a tile takes some 2700 clocks (1.42 us), the products' 2176 among them: M = 64 has half of the tensor
+// cores' rate. With 64 rows, one copy of a token serves 64 * 2 * (576 + 512) operations, and shared memory is as near its
+// limit: 72 KB of keys stored and read, 64 KB of values, and 27 KB of Q read a tile are some 1900 clocks. The rest is the
+// chain of a stage (store 1450 clocks, S 1240, softmax 1370, O 850), of which two stages hide all but a fifth. A unit
+// starts in some 8000 clocks (lengths, table, first tokens and Q are four round trips) and ends in some 5000.
+// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 680 us (34 % of the bf16 rate); 64 trees of 4 to
+// 8 nodes, 64 heads, contexts of 4096 to 8192: 447 us (44 %); one tree of 8 nodes, 128 heads, 32768 tokens: 102 us (38 %).
+// Pairs of blocks on one product of M = 256 with half of the values' dims each (full rate, but S twice) took 699, 484
+// and 96 us, and lost more in units that are not full.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 64;                        // of a unit
 constexpr int kQBytes = kPieces * kPieceBytes;
@@ -52,7 +62,7 @@ struct Shared {
   alignas(8) uint8_t poison[kStages][kGroupWarps];  // and not finite
   float xchg[2][128];
   float inv[kRows];                              // 1 / sum of each row
-  Unit unit;
+  Unit units[2];                                 // this one and the next
   Place place;
 };
 
@@ -67,20 +77,12 @@ __device__ __forceinline__ void tmem_bar() { asm volatile("bar.sync 3, 160;" :::
 // The two warps with either half of a tile's tokens for the same 32 rows.
 __device__ __forceinline__ void row_bar(int which) { asm volatile("bar.sync %0, 64;" ::"r"(4 + which) : "memory"); }
 
+// All that a block does for a unit; `started`: barriers and tensor memory are there from an earlier one.
 template <bool kTree>
-__global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+__device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Shared& sh, int turn, const Unit& u, bool& started) {
   uint8_t* q_s = smem;
   uint8_t* k_s = q_s + kQBytes;
   uint8_t* p_s = k_s + kStages * kStageBytes;
-  Shared& sh = *reinterpret_cast<Shared*>(p_s + kPieceBytes);
-
-  if (p.workers) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
-  bool started = false;
-  for (bool first = true;; first = false) {
-  const Unit u = fetch_unit<kTree>(p, sh, blockIdx.x, first);
-  if (!u.any) break;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = u.tiles;
   // query row r of the unit: head r % heads of token r / heads
@@ -97,8 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       }
       if (p.lse && tid < u.rows * u.heads) p.lse[(u.row0 + tid / u.heads) * p.ld_lse + u.head0 + tid % u.heads] = -INFINITY;
     }
-    __syncthreads();
-    continue;
+    return;
   }
 
   // Barriers and tensor memory are set up by the matrix warp; every role first does what needs neither.
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
     }
     epilogue_bar();
     tc_fence_after();
-    const volatile Unit& e = sh.unit;
+    const volatile Unit& e = sh.units[turn];
     const bool split = e.part >= 0;
     tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
     if (warp >= 4) {
@@ -571,11 +572,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedPar
       }
     }
   }
-  tc_fence_before();
-  __syncwarp();
-  __syncthreads();
-  tc_fence_after();
   started = true;
+}
+
+template <bool kTree>
+__global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  Shared& sh = *reinterpret_cast<Shared*>(smem + kQBytes + kStages * kStageBytes + kPieceBytes);
+
+  if (p.workers) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
+  bool started = false;
+  for (int turn = 1, first = 1;; turn ^= 1, first = 0) {
+    if (!first) {
+      const Unit u = sh.units[turn];
+      if (!u.any) break;
+      run_unit<kTree>(p, smem, sh, turn, u, started);
+    }
+    // the last tiles' position dims are long copied: this warp finds the next unit while the others finish theirs
+    if (threadIdx.x / 32 == kThreads / 32 - 1) find_next<kTree>(p, blockIdx.x, first, sh.place, sh.units[turn ^ 1]);
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
   }
   if (started && threadIdx.x / 32 == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
 }

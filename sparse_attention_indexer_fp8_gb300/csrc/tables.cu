@@ -47,6 +47,10 @@ struct TableParams {
 // computes the sums of all requests by itself. Outputs may overwrite the lengths they come from, so no block
 // writes before all have read: one block needs its own barrier for that, several are one cluster. A slot
 // in a fresh page comes from free_blocks, not from the table, which another block writes.
+//
+// One block up to 2048 rows, 3.5 us for a decode step of 128 requests; a cluster of eight above. With a cluster
+// always, 892 rows take 4.5 us instead of 4.1, 1612 rows 4.7 instead of 5.0, 2420 rows 5.1 instead of one block's 6.2,
+// 44216 rows of 256 requests 9.7 instead of 39.2 (1.3 MB written there; the bisections' shared-memory reads bound it).
 // ---------------------------------------------------------------------------
 constexpr int kClusterBlocks = 8;  // the portable cluster size
 constexpr int kMaxTableThreads = 1024;
@@ -209,6 +213,7 @@ __global__ void __launch_bounds__(kMaxTableThreads) build_tables_kernel(const Ta
 // One block per request, one thread per node: it climbs from the node to the root through the parents in shared
 // memory. Ancestors have falling indices, so the words of a row are finished one after the other, from
 // its own down to word 0, and each is written once.
+// 1.8 us for 8 trees of 16 nodes, 2.7 us for 128 of 64: the launch, and the climb's dependent reads.
 // ---------------------------------------------------------------------------
 constexpr int kTreeThreads = 128;
 constexpr int kTreeNodes = 32 * IDX_TREE_MAX_WORDS;

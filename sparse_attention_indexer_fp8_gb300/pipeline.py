@@ -265,7 +265,8 @@ class TreeStep:
     ``plan`` prepares a step from the requests' lengths and the nodes' parents, once for all layers: blocks and slots
     of the new tokens, their positions (the request's length and the node's depth) and who sees whom. ``layer`` inserts
     a layer's new tokens and attends to every request's earlier tokens and each node's ancestors. A prompt, or tokens
-    that an earlier step accepted, are nodes whose parent is the one before; the records of dropped nodes are
+    that an earlier step accepted, are nodes whose parent is the one before (32 ``words`` nodes a request at most; longer
+    prompts go through ``idx_window_attention``); the records of dropped nodes are
     overwritten, and their blocks used again, by the next step over the same ``cached_lens``. Rows behind the last
     node are padding. Neither call allocates anything.
     """

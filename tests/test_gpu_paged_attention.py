@@ -426,7 +426,9 @@ def lengths(n, lo, hi, seed):
     (3, [1] * 100, lengths(100, 1, 2500, 2)),                   # fewer, of lengths that no whole number of parts fits
     (64, [2, 1, 3], [3000, 40, 9000]),                          # few: a context cut into many parts
     (2, [1] * 160, lengths(160, 0, 700, 3)), (2, [1] * 161, lengths(161, 0, 700, 4)),  # the most requests that are shared, and more
-    (128, [1, 1], [1500, 1500]), (5, [64, 0, 0, 1], [800, 0, 900, 2000])])
+    (128, [1, 1], [1500, 1500]), (5, [64, 0, 0, 1], [800, 0, 900, 2000]),
+    (2, [1] * 160, lengths(160, 0, 1300, 5)), (16, [37, 0, 50, 3] * 11, lengths(44, 60, 1300, 6)),
+    (64, [5, 0, 2] * 50, lengths(150, 0, 1300, 7))])
 def test_shared_work(H, counts, ctxs):
     """The same results with a workspace, where blocks take equal shares of ragged work, as the oracle has."""
     ctxs = [max(c, n) for c, n in zip(ctxs, counts)]
@@ -481,3 +483,25 @@ def test_wide_table(bs, pages):
     c.window(2 ** 31 - 1, 2 ** 31 - 1, ws=c.workspace())
     idx.idx_device_error()
     c.check(c.window_seen(2 ** 31 - 1, 2 ** 31 - 1))
+
+
+def test_two_streams():
+    """Calls on two streams at once, each with its own workspace, give what they give alone."""
+    cases = [Case(64, [5, 0, 2, 8] * 4, lengths(16, 100, 4000, 8), 64, seed=8), Case(128, [1, 3], [9000, 40], 16, seed=9)]
+    masks = [random_mask(c.counts, 1, np.random.default_rng(1)) for c in cases]
+    ws = [c.workspace() for c in cases]
+    want = []
+    for c, m, w in zip(cases, masks, ws):
+        c.tree(m, ws=w)
+        want.append((c.out.clone(), c.lse.clone()))
+        c.out.fill_(7)
+    lens = [(i32(c.cu), i32(c.ctxs)) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, m, w, st, (cu, ctx) in zip(cases, masks, ws, streams, lens):
+            idx.idx_tree_attention(c.q, c.cache, c.bs, c.block_table, cu, ctx, m, c.out, SCALE, lse=c.lse, ws=w, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    for c, (out, lse) in zip(cases, want):
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    idx.idx_device_error()
