@@ -166,20 +166,31 @@ int64_t plan_bytes(const Plan& plan) {
   return plan.workers * (static_cast<int64_t>(sizeof(Cut)) + 2 * block::kRows * (kKvLatent * 4 + 8));
 }
 
-// Whether sharing the work out can gain what it costs: finding the shares, the parts' stores and the join (some 6 us), and
-// a start and an end more for a block. The host knows of the lengths only how much the table or the window has room for.
-// Few units are cut: 8 requests of 4 rows and 16 heads take 16.6 us shared and 19.1 us plain with 8 tiles, 15.3 and 13.2
-// with 4; 76 windows of 4096 tokens and 64 heads 68 and 104 us, 16 of 1024 21 and 33 us. Of more units only the uneven
-// ends are gained, and windows are as long as one another (128 of 4096 tokens: 120 and 111 us). 64 requests of 8 rows and
-// 64 heads take 446 and 505 us with 128 tiles at most, 148 and 146 with 32, 100 and 85 with 16.
-bool worth_sharing(const PagedParams& p, const Plan& plan, bool tree) {
+// How many tiles a row may see: the host knows only how much the table or the window has room for.
+int64_t most_tiles_of(const PagedParams& p, const Plan& plan, bool tree) {
   const int64_t tokens = std::min(static_cast<int64_t>(p.n_pages) * p.block_size, static_cast<int64_t>(INT32_MAX));
+  return (tree ? tokens : std::min(tokens, static_cast<int64_t>(p.window) + p.sinks + plan.tokens)) / kTile;
+}
+
+// Whether even shares can gain what they cost: the parts' stores, the join, and a start and an end more for a block (some
+// 6 us). Few units are cut: 8 requests of 4 rows and 16 heads take 16.6 us shared and 19.1 us plain with 8 tiles, 15.3 and
+// 13.2 with 4; 76 windows of 4096 tokens and 64 heads 69 and 104 us, 16 of 1024 21 and 33 us. Of more units only the uneven
+// ends are gained, and windows are as long as one another (128 of 4096 tokens: 120 and 107 us). 64 requests of 8 rows and
+// 64 heads take 447 and 506 us with 128 tiles at most, 148 and 146 with 32, 100 and 85 with 16.
+bool worth_cutting(const PagedParams& p, const Plan& plan, bool tree) {
   const int64_t units = std::min(static_cast<int64_t>(p.T) * plan.head_blocks, plan.units);
   const bool few = 2 * units <= plan.workers;
-  const int64_t tiles = (tree ? tokens : std::min(tokens, static_cast<int64_t>(p.window) + p.sinks + plan.tokens)) / kTile;
-  if (tiles < (few ? 8 : 32) || !(tree || few)) return false;
+  if (most_tiles_of(p, plan, tree) < (few ? 8 : 32) || !(tree || few)) return false;
   // the line's sums stay far within 32 bits
-  return tokens / kTile + 1 + kUnitTiles <= (int64_t{1} << 29) / std::max<int64_t>(units, plan.workers);
+  return most_tiles_of(p, plan, true) + 1 + kUnitTiles <= (int64_t{1} << 29) / std::max<int64_t>(units, plan.workers);
+}
+
+// Whether a block for each SM, which takes units in turn and finds the next while it finishes one, is faster than a block
+// for each unit: chunks of four prompts, 128 heads, a window of 1024 take 651 us, and 680 with a block each; 2048 rows of a
+// prompt 279 and 307 us. Long contexts are left to the order in which blocks become free: 64 trees of 8 nodes and 64 heads
+// with up to 128 tiles take 539 us in turn and 506 with a block each, with 16 tiles 84 and 86, with 8 tiles 53 and 58.
+bool worth_sharing(const PagedParams& p, const Plan& plan, bool tree) {
+  return plan.units > plan.workers && (!tree || most_tiles_of(p, plan, tree) < 32);
 }
 
 // What both calls check and launch; `p` holds what they were given.
@@ -212,12 +223,13 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
   p.head_blocks = plan.head_blocks;
   p.heads = plan.heads;
   p.tokens = plan.tokens;
-  p.workers = ws && worth_sharing(p, plan, tree) ? plan.workers : 0;
+  p.cut = ws && plan.workers && worth_cutting(p, plan, tree);
+  p.workers = p.cut || worth_sharing(p, plan, tree) ? plan.workers : 0;
   if (ws && ws_bytes < static_cast<size_t>(plan_bytes(plan))) {
     return fail(IDX_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %lld are needed", fn, ws_bytes,
                 static_cast<long long>(plan_bytes(plan)));
   }
-  if (p.workers) {
+  if (p.cut) {
     p.ws_cuts = static_cast<Cut*>(ws);
     p.ws_o = reinterpret_cast<float*>(p.ws_cuts + p.workers);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + 2 * static_cast<int64_t>(p.workers) * block::kRows * kKvLatent);
@@ -227,7 +239,7 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block::kSmemBytes);
   if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
   kernel<<<units, block::kThreads, block::kSmemBytes, stream>>>(p);
-  if (e == cudaSuccess && p.workers > 1) {
+  if (e == cudaSuccess && p.cut && p.workers > 1) {
     const idx_status_t launched = check_launch(fn);
     if (launched != IDX_OK) return launched;
     // launched while the parts run: its blocks wait at their first reads for the parts' end

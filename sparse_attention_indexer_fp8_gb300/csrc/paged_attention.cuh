@@ -51,7 +51,8 @@ struct PagedParams {
   int page_shift;              // log2(block_size)
   int head_blocks, heads;      // groups of heads, and the heads of one
   int tokens;                  // query rows of a unit
-  int workers;                 // blocks that share the work out evenly; 0: a block a unit
+  int workers;                 // blocks that share the units; 0: a block a unit
+  bool cut;                    // shares are even, and may begin and end within a unit; else whole units in turn
   struct Cut* ws_cuts;         // [workers]
   float2* ws_ml;               // [2 workers, 64 rows]: maximum (log2 units) and sum of a part
   float* ws_o;                 // [2 workers, 64 rows, 512]: accumulators
@@ -172,9 +173,10 @@ __device__ __forceinline__ bool find_unit(const PagedParams& p, int index, Unit&
   return complete_unit<kTree>(p, at, n, (g - at / U - lo) * U, u);
 }
 
-// All units of a call in one line, request after request, each as long as its tiles, and where there are more units than
-// workers, as what its start and end cost besides; every worker gets the same share of the line. Only the line's cuts
-// split a unit. It is computed by one warp from the lengths, which the host does not know.
+// All units of a call in one line, request after request, computed by one warp from the lengths, which the host does not
+// know. Where shares are even, a unit is as long as its tiles, and where there are more units than workers, as what its
+// start and end cost besides; every worker gets the same share of the line, and only the line's cuts split a unit. Where
+// whole units are taken in turn, each is one long.
 template <bool kTree>
 struct Line {
   static constexpr int kPer = kMaxSharedRequests / 32;  // requests of a lane: b = 32 k + lane
@@ -203,7 +205,7 @@ struct Line {
       rows[k] -= first[k];
       if (rows[k] > 0) {
         units[k] = (rows[k] + p.tokens - 1) / p.tokens * p.head_blocks;
-        length[k] = most_tiles<kTree>(p, rows[k], max(ctxs[k], 0));
+        length[k] = p.cut ? most_tiles<kTree>(p, rows[k], max(ctxs[k], 0)) : 1;
       }
       all += units[k];
       sum += units[k] * length[k];
@@ -211,7 +213,7 @@ struct Line {
     }
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     all = __reduce_add_sync(0xFFFFFFFFu, all);
-    extra = all > p.workers ? kUnitTiles : 0;
+    extra = p.cut && all > p.workers ? kUnitTiles : 0;
     sum = __reduce_add_sync(0xFFFFFFFFu, sum) + all * extra;
     longest += extra;
 #pragma unroll
@@ -223,7 +225,7 @@ struct Line {
     // that costs more, units are lengthened to whole numbers of shares: of `per` tiles, the fewest with which all have room,
     // or all of the longest.
     int per = 0;
-    if (all <= p.workers) {
+    if (p.cut && all <= p.workers) {
       per = min(share, longest);
       while (true) {
         if (per + kJoinTiles >= longest) per = longest;  // whole contexts cost less than parts and their join
@@ -300,8 +302,19 @@ __device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Plac
     place.pos = 0;
     return at_first && find_unit<kTree>(p, worker, u);
   }
-  if (!at_first && place.pos >= place.end) return false;
+  if (p.cut && !at_first && place.pos >= place.end) return false;
   const Line<kTree> line(p);
+  int len, row, n, from;
+  if (!p.cut) {
+    place.pos = at_first ? worker : place.pos + p.workers;
+    if (place.pos >= line.total) return false;
+    // windows from the last rows on: of causal rows these see most, and what is long should not begin last
+    line.unit_at(p, kTree ? place.pos : line.total - 1 - place.pos, u, len, row, n, from);
+    u.tile0 = 0;
+    u.tiles = INT32_MAX;
+    u.part = -1;
+    return complete_unit<kTree>(p, row, n, from, u);
+  }
   if (at_first) {
     // as many shares as there are workers cover the line, and little more
     place.pos = worker * line.share;
@@ -309,7 +322,6 @@ __device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Plac
     if (place.pos >= place.end) return false;
   }
   const int pos = place.pos;
-  int len, row, n, from;
   const int begin = line.unit_at(p, pos, u, len, row, n, from);
   const int stop = min(begin + len, place.end);
   u.tile0 = max(pos - begin - line.extra, 0);
@@ -331,7 +343,7 @@ __device__ __forceinline__ void find_next(const PagedParams& p, int worker, bool
   if ((threadIdx.x & 31) == 0) {
     unit = u;
     place = at;
-    if (p.workers) {
+    if (p.cut) {
       if (first) p.ws_cuts[worker].parts = 0;
       if (u.any && u.part == 2 * worker + 1) p.ws_cuts[worker] = Cut{u.row0, u.rows, u.head0, u.heads, u.parts, {0, 0, 0}};
     }
