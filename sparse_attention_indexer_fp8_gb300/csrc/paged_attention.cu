@@ -234,11 +234,27 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
     p.ws_o = reinterpret_cast<float*>(p.ws_cuts + p.workers);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + 2 * static_cast<int64_t>(p.workers) * block::kRows * kKvLatent);
   }
+  // Q as a unit reads it, 64 dims of its heads and rows a copy, and the position dims of the cache's pages. Strides of one
+  // row, head or block may be anything.
+  CUtensorMap q_map, rope_map;
+  const uint64_t q_dims[3] = {kKvDim, static_cast<uint64_t>(p.H), static_cast<uint64_t>(p.T)};
+  const uint64_t q_strides[2] = {p.H > 1 ? 2 * static_cast<uint64_t>(p.ld_qh) : 2 * kKvDim,
+                                 p.T > 1 ? 2 * static_cast<uint64_t>(p.ld_q) : 2 * kKvDim};
+  const uint32_t q_box[3] = {64, static_cast<uint32_t>(plan.heads), static_cast<uint32_t>(plan.tokens)};
+  idx_status_t made = encode_tensor_map(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.q, q_dims, q_strides, q_box,
+                                        CU_TENSOR_MAP_SWIZZLE_128B);
+  if (made != IDX_OK) return made;
+  const uint64_t rope_dims[3] = {kKvRope, static_cast<uint64_t>(p.block_size), static_cast<uint64_t>(std::max(p.num_blocks, 1))};
+  const uint64_t rope_strides[2] = {2 * kKvRope, static_cast<uint64_t>(p.num_blocks > 1 ? p.block_stride : p.block_size * IDX_KV_TOKEN_BYTES)};
+  const uint32_t rope_box[3] = {kKvRope, static_cast<uint32_t>(block::copy_tokens_of(p.block_size)), 1};
+  made = encode_tensor_map(&rope_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.cache + p.block_size * kKvRopeAt, rope_dims,
+                           rope_strides, rope_box, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (made != IDX_OK) return made;
   const unsigned units = static_cast<unsigned>(p.workers ? p.workers : plan.units);
   auto* kernel = tree ? block::paged_block_kernel<true> : block::paged_block_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block::kSmemBytes);
   if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
-  kernel<<<units, block::kThreads, block::kSmemBytes, stream>>>(p);
+  kernel<<<units, block::kThreads, block::kSmemBytes, stream>>>(q_map, rope_map, p);
   if (e == cudaSuccess && p.cut && p.workers > 1) {
     const idx_status_t launched = check_launch(fn);
     if (launched != IDX_OK) return launched;

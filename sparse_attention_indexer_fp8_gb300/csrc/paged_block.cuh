@@ -51,7 +51,7 @@ constexpr int kTmemCols = 512;
 static_assert(kQCols + kQTmemPieces * 32 <= kTmemCols, "tensor memory of one block");
 
 struct Shared {
-  uint64_t q_full, drained;
+  uint64_t q_full, q_free, drained;              // Q is in place; S of the last tile is complete
   uint64_t k_full[kStages];                      // a stage's tokens are stored
   uint64_t s_full[kStages];                      // S of the tile is complete
   uint64_t p_full[kStages];                      // P is stored
@@ -60,6 +60,8 @@ struct Shared {
   volatile uint32_t dead;                        // a wait expired: no further wait blocks
   alignas(8) uint8_t there[kStages][kGroupWarps];   // bit j of byte w: token 8 w + j of the tile is there
   alignas(8) uint8_t poison[kStages][kGroupWarps];  // and not finite
+  alignas(8) uint64_t q_here;                    // Q of the next unit: these three live as long as the block
+  uint64_t rope_here[kStages];                   // a tile's position dims
   float xchg[2][128];
   float inv[kRows];                              // 1 / sum of each row
   Unit units[2];                                 // this one and the next
@@ -77,9 +79,25 @@ __device__ __forceinline__ void tmem_bar() { asm volatile("bar.sync 3, 160;" :::
 // The two warps with either half of a tile's tokens for the same 32 rows.
 __device__ __forceinline__ void row_bar(int which) { asm volatile("bar.sync %0, 64;" ::"r"(4 + which) : "memory"); }
 
+// Tokens of one copy of position dims: within a page and half a tile.
+__host__ __device__ constexpr int copy_tokens_of(int block_size) { return block_size < 32 ? block_size : 32; }
+
+// A copy that was asked for always arrives; should it not, the wait ends all the same, as every other.
+__device__ __forceinline__ void wait_copy(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(&g_paged_error, 2u);
+      return;
+    }
+  }
+}
+
 // All that a block does for a unit; `started`: barriers and tensor memory are there from an earlier one.
 template <bool kTree>
-__device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Shared& sh, int turn, const Unit& u, bool& started) {
+__device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap* rope_map, uint8_t* smem, Shared& sh, int turn,
+                                         const Unit& u, bool& started, uint32_t& copies) {
   uint8_t* q_s = smem;
   uint8_t* k_s = q_s + kQBytes;
   uint8_t* p_s = k_s + kStages * kStageBytes;
@@ -198,9 +216,10 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Sh
     }
   } else if (warp >= kRopeWarp) {
     // ---------------------------------------------------------------- position dims, and L2 prefetch
-    // Position dims are bf16 in the cache as in the tile: copied asynchronously, as soon as S of the tile
-    // before is complete. Lane l locates tokens l and 32 + l. The same warp reports missing pages, and brings the records
-    // of the tile kAhead further on into L2.
+    // Position dims are bf16 in the cache as in the tile: bulk copies of the tile's pages, as soon as S of the tile
+    // before is complete. Tokens that no row sees come along or leave what was there: their scores are not read. Lane l
+    // locates tokens l and 32 + l. The same warp reports missing pages, and brings the records of the tile kAhead further on
+    // into L2.
     const int group = warp - kRopeWarp;
     auto entry = [&](int tile, int h) { return tile < tiles ? entry_of(p, u, tile_start(u, tile) + 32 * h + lane) : -1; };
     // 32 tokens: each lane's own position dims and codes, and 8 x 4 lines of latents an instruction
@@ -227,35 +246,46 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Sh
       here[h] = entry(group, h);
       ahead[h] = entry(group + kAhead, h);
     }
-    for (int i = group; i < kAhead && i < tiles; i += kStages) {
-      prefetch(i, 0, entry(i, 0));
-      prefetch(i, 1, entry(i, 1));
-    }
     const uint32_t piece = smem_u32(k_s) + group * kStageBytes + (kPieces - 1) * kPieceBytes;
+    const int copy_tokens = copy_tokens_of(p.block_size);
     if (group >= tiles) setup();
     for (int i = group; i < tiles; i += kStages) {
-      const uint8_t* rope[2];
+      // a page, or 32 tokens of one, are a copy, made by the first lane with a token in it
+      int block[2];
+      uint32_t first[2];
+      int copied = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int j = tile_start(u, i) + 32 * h + lane;
-        const bool mine = is_block(p, here[h]);
-        rope[h] = mine ? p.cache + here[h] * p.block_stride + p.block_size * kKvRopeAt +
-                             (j & (p.block_size - 1)) * (2 * kKvRope)
-                       : nullptr;
+        block[h] = here[h];
+        const bool mine = is_block(p, block[h]);
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, mine), page = copy_tokens == 32 ? 0xFFFFFFFFu : lane < 16 ? 0xFFFFu : 0xFFFF0000u;
+        first[h] = __ballot_sync(0xFFFFFFFFu, mine && lane == __ffs(have & page) - 1);
+        copied += __popc(first[h]);
         if (!mine && unit_sees(u, j)) atomicOr(&g_paged_error, 1u);
         here[h] = entry(i + kStages, h);
       }
       // only S reads position dims, so their piece is free long before the stage is
       if (i >= kStages) wait_for(sh, &sh.s_full[group], ((i >> 1) - 1) & 1);
+      if (copied) {
+        if (lane == 0) mbar_arrive_expect_tx(&sh.rope_here[group], copied * copy_tokens * (2 * kKvRope));
+        __syncwarp();
 #pragma unroll
-      for (int c = 0; c < kTile / 4; ++c) {
-        const int t = 4 * c + (lane >> 3), x = lane & 7;
-        const uint8_t* from = shfl_ptr(rope[c / 8], t & 31);
-        copy16_if(piece + t * 128 + ((x ^ (t & 7)) << 4), from ? from + 16 * x : p.cache, from != nullptr);
+        for (int h = 0; h < 2; ++h) {
+          if ((first[h] >> lane) & 1u) {
+            const int at = 32 * h + (lane & ~(copy_tokens - 1));  // in the tile
+            tma_load_3d(piece + at * 128, rope_map, &sh.rope_here[group], 0, (tile_start(u, i) + at) & (p.block_size - 1), block[h]);
+          }
+        }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      if (i == group) setup();
+      if (i == group) {
+        for (int k = group + kStages; k < kAhead && k < tiles; k += kStages) {  // the first tile's are on their way
+          prefetch(k, 0, entry(k, 0));
+          prefetch(k, 1, entry(k, 1));
+        }
+        setup();
+      }
+      if (copied) wait_copy(&sh.rope_here[group], copies++ & 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[group]);
 #pragma unroll
@@ -273,6 +303,7 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Sh
         sh.dead = 0;
       }
       mbar_init(&sh.q_full, 4);
+      mbar_init(&sh.q_free, 1);
       mbar_init(&sh.drained, 1);
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&sh.k_full[i], kGroupWarps + 1);
@@ -344,7 +375,7 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Sh
           }
         }
         commit_if(&sh.s_full[st], lead);
-        ++s_next;
+        if (++s_next == total) commit_if(&sh.q_free, lead);
         idle = 0;
         continue;
       }
@@ -367,28 +398,11 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Sh
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------------- softmax
-    // Q, sixteen rows a warp, rows past the unit's last one zero, all copies out at once; then as many pieces as there
-    // are columns into tensor memory: S reads less of the shared memory that the loaders and O want too. Lane l < 16
-    // finds row l.
-    {
-      const int qr = 16 * warp + (lane & 15), qt = q_row_of(qr), qh = qr - qt * p.heads;
-      const uint8_t* src = qt < u.rows && qh < u.heads
-                               ? reinterpret_cast<const uint8_t*>(p.q + (u.row0 + qt) * p.ld_q + (u.head0 + qh) * p.ld_qh)
-                               : nullptr;
-      const uint32_t q_row = smem_u32(q_s) + 16 * warp * 128;
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const uint8_t* row = shfl_ptr(src, i);
-        const bool have_row = row != nullptr;
-        const uint8_t* from = (have_row ? row : reinterpret_cast<const uint8_t*>(p.q)) + 16 * lane;
-        const uint32_t at = q_row + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
-        copy16_if(at + (lane >> 3) * kPieceBytes, from, have_row);
-        copy16_if(at + (4 + (lane >> 3)) * kPieceBytes, from + 512, have_row);
-        if (lane < 8) copy16_if(at + 8 * kPieceBytes, from + 1024, have_row);
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fence_proxy_async_smem();
+    // Q was copied by the warp that found the unit; rows past its last one hold anything, and give results that nobody
+    // reads. As many pieces as there are columns go into tensor memory: S reads less of the shared memory that the loaders
+    // and O want too.
+    wait_copy(&sh.q_here, copies & 1);
+    ++copies;
     tmem_bar();
     tc_fence_after();
     tmem = sh.tmem;
@@ -575,22 +589,50 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, uint8_t* smem, Sh
   started = true;
 }
 
+// The next unit, found by one warp, and its Q, copied once S of the last tile has left the place.
 template <bool kTree>
-__global__ void __launch_bounds__(kThreads, 1) paged_block_kernel(const PagedParams p) {
+__device__ __forceinline__ void prepare_unit(const PagedParams& p, const CUtensorMap* q_map, uint8_t* smem, Shared& sh, int turn,
+                                             bool first, bool busy) {
+  Unit& next = sh.units[turn];
+  find_next<kTree>(p, blockIdx.x, first, sh.place, next);
+  __syncwarp();
+  if (!next.any || next.tiles == 0) return;
+  if (busy) wait_for(sh, &sh.q_free, 0);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) mbar_arrive_expect_tx(&sh.q_here, kPieces * p.heads * p.tokens * 128);
+  __syncwarp();
+  if (lane < kPieces) tma_load_3d(smem_u32(smem) + lane * kPieceBytes, q_map, &sh.q_here, 64 * lane, next.head0, next.row0);
+}
+
+template <bool kTree>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_block_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap rope_map, const PagedParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   Shared& sh = *reinterpret_cast<Shared*>(smem + kQBytes + kStages * kStageBytes + kPieceBytes);
 
-  if (p.workers) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
-  bool started = false;
+  if (p.cut) asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up meanwhile
+  const bool finder = threadIdx.x / 32 == kThreads / 32 - 1;
+  if (finder && (threadIdx.x & 31) == 0) {
+    tma_prefetch_map(&q_map);
+    tma_prefetch_map(&rope_map);
+    mbar_init(&sh.q_here, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.rope_here[i], 1);
+    fence_mbar_init();
+  }
+  bool started = false;   // barriers and tensor memory are there
+  uint32_t copies = 0;    // that the warp has waited for: Q, or a stage's position dims
   for (int turn = 1, first = 1;; turn ^= 1, first = 0) {
+    bool busy = false;
     if (!first) {
       const Unit u = sh.units[turn];
       if (!u.any) break;
-      run_unit<kTree>(p, smem, sh, turn, u, started);
+      busy = u.tiles > 0;
+      run_unit<kTree>(p, &rope_map, smem, sh, turn, u, started, copies);
     }
-    // the last tiles' position dims are long copied: this warp finds the next unit while the others finish theirs
-    if (threadIdx.x / 32 == kThreads / 32 - 1) find_next<kTree>(p, blockIdx.x, first, sh.place, sh.units[turn ^ 1]);
+    // the last tiles' position dims are copied: this warp finds the next unit while the others finish theirs
+    if (finder) prepare_unit<kTree>(p, &q_map, smem, sh, turn ^ 1, first, busy);
+    fence_proxy_async_smem();  // the stages held results, and take copies again
     tc_fence_before();
     __syncwarp();
     __syncthreads();
