@@ -13,8 +13,8 @@ namespace block {
 //   P = exp2(S * scale - m)    the running maximum m of each row in registers
 //   O += P V    64 rows x 512 dims, 4 steps of K = 16 over the 64 tokens, two halves of N = 256
 // with tcgen05.mma.ws (M = 64) in bf16 x bf16 -> fp32, the form and the roles of the sparse attention: warps 4-19
-// load and dequantise the tokens' latents, warps 21-22 copy their position dims and prefetch, warp 20 issues the
-// matrix instructions, warps 0-3 load Q and do the softmax; all but 20-22 store the result. Keys and values are one
+// load and dequantise the tokens' latents, warps 21-22 copy their position dims and prefetch (22 also finds the next unit and
+// copies its Q), warp 20 issues the matrix instructions, warps 0-3 do the softmax; all but 20-22 store the result. Keys and values are one
 // copy in shared memory: a token is a row of nine 128-byte swizzled pieces (64 dims each), read along the dims as the
 // K-major B operand of S and along the tokens as the N-major one of O. Two groups of eight loader warps own a stage
 // each, and hold the next tile in registers.
@@ -23,15 +23,18 @@ namespace block {
 // query tokens see different tokens, so each thread of the softmax has its own mask of a tile; and parts of a
 // context are found on the device from the lengths, which the host does not know.
 //
-// What bounds it: a tile takes some 2700 clocks (1.42 us), the products' 2176 among them: M = 64 has half of the tensor
-// cores' rate. With 64 rows, one copy of a token serves 64 * 2 * (576 + 512) operations, and shared memory is as near its
-// limit: 72 KB of keys stored and read, 64 KB of values, and 27 KB of Q read a tile are some 1900 clocks. The rest is the
-// chain of a stage (store 1450 clocks, S 1240, softmax 1370, O 850), of which two stages hide all but a fifth. A unit
-// starts in some 8000 clocks (lengths, table, first tokens and Q are four round trips) and ends in some 5000.
-// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 680 us (34 % of the bf16 rate); 64 trees of 4 to
+// What bounds it: a tile takes some 2750 clocks (1.43 us), the products' 2176 among them: M = 64 has half of the tensor
+// cores' rate. Shared memory is nearer its limit: 1408 accesses of 128 bytes by the tensor core (72 KB of keys, 64 of values,
+// 24 of Q, P twice) and 1140 by the warps (72 KB of keys stored, P, and waits of either for the other) are 2550 a tile. With
+// 64 rows one copy of a token serves no more. The chain of a stage (store 2000 clocks, S 1200, softmax 1300, O 850, and the
+// other stage's S between) takes what two tiles take. A block's first unit starts in some 8000 clocks (lengths, table, first
+// tokens and Q are four round trips), a later one in 4300, and a unit ends in some 5000.
+// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 645 us (36 % of the bf16 rate); 64 trees of 4 to
 // 8 nodes, 64 heads, contexts of 4096 to 8192: 447 us (44 %); one tree of 8 nodes, 128 heads, 32768 tokens: 102 us (38 %).
 // Pairs of blocks on one product of M = 256 with half of the values' dims each (full rate, but S twice) took 699, 484
-// and 96 us, and lost more in units that are not full.
+// and 96 us, and lost more in units that are not full. Copies of Q and position dims by the threads took 651 us for the
+// chunks (a 16-byte copy is an access for every 32 bytes), S and O in halves that overlap the stores 665, results stored by
+// bulk copies 651.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 64;                        // of a unit
 constexpr int kQBytes = kPieces * kPieceBytes;
@@ -259,7 +262,8 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap
         const int j = tile_start(u, i) + 32 * h + lane;
         block[h] = here[h];
         const bool mine = is_block(p, block[h]);
-        const uint32_t have = __ballot_sync(0xFFFFFFFFu, mine), page = copy_tokens == 32 ? 0xFFFFFFFFu : lane < 16 ? 0xFFFFu : 0xFFFF0000u;
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, mine);
+        const uint32_t page = copy_tokens == 32 ? 0xFFFFFFFFu : lane < 16 ? 0xFFFFu : 0xFFFF0000u;
         first[h] = __ballot_sync(0xFFFFFFFFu, mine && lane == __ffs(have & page) - 1);
         copied += __popc(first[h]);
         if (!mine && unit_sees(u, j)) atomicOr(&g_paged_error, 1u);
@@ -274,7 +278,8 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap
         for (int h = 0; h < 2; ++h) {
           if ((first[h] >> lane) & 1u) {
             const int at = 32 * h + (lane & ~(copy_tokens - 1));  // in the tile
-            tma_load_3d(piece + at * 128, rope_map, &sh.rope_here[group], 0, (tile_start(u, i) + at) & (p.block_size - 1), block[h]);
+            tma_load_3d(piece + at * 128, rope_map, &sh.rope_here[group], 0, (tile_start(u, i) + at) & (p.block_size - 1),
+                      block[h]);
           }
         }
       }

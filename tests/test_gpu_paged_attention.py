@@ -505,3 +505,17 @@ def test_two_streams():
     for c, (out, lse) in zip(cases, want):
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
     idx.idx_device_error()
+
+
+def test_extents_of_one():
+    """One row, one head, one block: their strides are never used, whatever they are."""
+    c = Case(1, [1], [50], 64, seed=10)
+    block = int(c.table[0, 0])
+    c.cache, c.table = c.cache[block:block + 1], c.table * 0
+    c.block_table = i32(c.table)
+    q, out = c.q.as_strided((1, 1, 576), (24, 40, 1)), c.out.as_strided((1, 1, 512), (8, 16, 1))
+    cache = c.cache.as_strided((1, c.cache.shape[1]), (3, 1))
+    idx.idx_window_attention(q, cache, 64, c.block_table.as_strided((1, 1), (5, 1)), i32(c.cu), i32(c.ctxs), out, SCALE, 30,
+                             lse=c.lse.as_strided((1, 1), (9, 7)))
+    idx.idx_device_error()
+    c.check(c.window_seen(30, 0))
