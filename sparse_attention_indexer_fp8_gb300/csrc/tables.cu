@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kMaxTableThreads) build_tables_kernel(const Ta
     start = 0;
     bad |= 1u;
   }
-  int64_t carry[3] = {0, 0, 0};  // new rows, fresh blocks, context lengths of the requests before this round's
+  int64_t carry[3] = {0, 0, 0};  // new rows, fresh blocks, context lengths of the requests before this pass's
   for (int base = 0; base < p.B; base += blockDim.x) {
     const int b = base + tid;
     int64_t v[3] = {0, 0, 0};
