@@ -186,7 +186,7 @@ bool worth_cutting(const PagedParams& p, const Plan& plan, bool tree) {
 }
 
 // Whether a block for each SM, which takes units in turn and finds the next while it finishes one, is faster than a block
-// for each unit: chunks of four prompts, 128 heads, a window of 1024 take 645 us, and 680 with a block each; four prompts of
+// for each unit: chunks of four prompts, 128 heads, a window of 1024 take 626 us, and some 5 % more with a block each; four prompts of
 // 512 rows 266 and 307 us. Long contexts are left to the order in which blocks become free: 64 trees of 8 nodes and 64
 // heads with up to 128 tiles take 539 us in turn and 506 with a block each, with 16 tiles 83 and 86, with 8 tiles 51 and 58.
 bool worth_sharing(const PagedParams& p, const Plan& plan, bool tree) {

@@ -67,20 +67,36 @@ struct alignas(16) Cut {
 
 // A unit of work: consecutive query rows of one request with one group of heads, and a range of the tiles of the
 // tokens that they see together.
-struct Unit {
-  int request, row0, rows;  // q rows [row0, row0 + rows)
-  int head0, heads;
-  int pos0;                 // position of the first row
-  int base, ctx;            // tokens of the request before its new rows, and with them
+struct alignas(16) Unit {
+  int request;
   int lo, hi;               // tokens in [0, first) or [lo, hi] are seen by a row
   int first;
   int skip;                 // tiles from 0 that hold the first tokens; the others start at tile_lo
   int tile_lo;
   int tile0, tiles;         // this part's range
+  int row0, rows;           // q rows [row0, row0 + rows)
+  int head0, heads;
+  int pos0;                 // position of the first row
+  int base, ctx;            // tokens of the request before its new rows, and with them
   int part;                 // number of the part; -1: the unit is whole
   int parts;                // of the unit
   bool any;                 // false: there is no unit left
 };
+
+// Where a unit's tokens lie, out of shared memory: eight words that need not stay in registers.
+__device__ __forceinline__ Unit tokens_of(uint32_t unit) {
+  const uint4 a = ld_shared16(unit), b = ld_shared16(unit + 16);
+  Unit u;
+  u.request = static_cast<int>(a.x);
+  u.lo = static_cast<int>(a.y);
+  u.hi = static_cast<int>(a.z);
+  u.first = static_cast<int>(a.w);
+  u.skip = static_cast<int>(b.x);
+  u.tile_lo = static_cast<int>(b.y);
+  u.tile0 = static_cast<int>(b.z);
+  u.tiles = static_cast<int>(b.w);
+  return u;
+}
 
 __device__ __forceinline__ int row_at(const PagedParams& p, int b) {
   return min(max(__ldg(p.cu_rows + b), 0), p.T);

@@ -29,12 +29,12 @@ namespace block {
 // 64 rows one copy of a token serves no more. The chain of a stage (store 2000 clocks, S 1200, softmax 1300, O 850, and the
 // other stage's S between) takes what two tiles take. A block's first unit starts in some 8000 clocks (lengths, table, first
 // tokens and Q are four round trips), a later one in 4300, and a unit ends in some 5000.
-// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 645 us (36 % of the bf16 rate); 64 trees of 4 to
+// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 626 us (37 % of the bf16 rate); 64 trees of 4 to
 // 8 nodes, 64 heads, contexts of 4096 to 8192: 447 us (44 %); one tree of 8 nodes, 128 heads, 32768 tokens: 102 us (38 %).
 // Pairs of blocks on one product of M = 256 with half of the values' dims each (full rate, but S twice) took 699, 484
-// and 96 us, and lost more in units that are not full. Copies of Q and position dims by the threads took 651 us for the
-// chunks (a 16-byte copy is an access for every 32 bytes), S and O in halves that overlap the stores 665, results stored by
-// bulk copies 651.
+// and 96 us, and lost more in units that are not full. Copies of Q and position dims by the threads added 1 % to
+// the chunks (a 16-byte copy is an access for every 32 bytes), S and O in halves that overlap the stores 2 %, results stored
+// by bulk copies 1 %.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 64;                        // of a unit
 constexpr int kQBytes = kPieces * kPieceBytes;
@@ -147,8 +147,14 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap
     uint32_t there = 0;  // bit j: token j of the found tile is loaded
     const uint8_t* latent = nullptr;  // of the warp's first token
     // of a lane's own token, lane % 8; the warp's tokens that a row sees share one block
+    const uint32_t unit_at = smem_u32(&sh.units[turn]);
+    auto tokens = [&]() {
+      if constexpr (kTree) return u; else return tokens_of(unit_at);
+    };
     auto lookup = [&](int tile) {
-      return tile < tiles ? entry_of(p, u, tile_start(u, tile) + r0 + (lane & 7)) : -1;
+      if (tile >= tiles) return -1;
+      const Unit v = tokens();
+      return entry_of(p, v, tile_start(v, tile) + r0 + (lane & 7));
     };
     auto find = [&](int tile, int block) {  // the lane's token is in `block`
       const bool mine = is_block(p, block);
@@ -156,7 +162,7 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap
       const int blk = there ? __shfl_sync(0xFFFFFFFFu, block, __ffs(there) - 1) : 0;
       found_codes = 0;
       if (there) {
-        const int off = (tile_start(u, tile) + r0) & (p.block_size - 1);
+        const int off = (tile_start(tokens(), tile) + r0) & (p.block_size - 1);
         const uint8_t* base = p.cache + blk * p.block_stride;
         latent = base + off * kKvLatent;
         if (mine) {
@@ -165,11 +171,13 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap
       }
     };
     auto load = [&]() {
+      int own = lane;
+      asm volatile("" : "+r"(own));  // eight offsets would take eight registers through the loop
 #pragma unroll
       for (int j = 0; j < kTokensPerWarp; ++j) {
         const bool ok = (there >> j) & 1u;
-        raw[j][0] = load8_if(latent + kKvLatent * j + 8 * (lane ^ j), ok);  // r0 is a multiple of eight: row j of the swizzle
-        raw[j][1] = load8_if(latent + kKvLatent * j + 256 + 8 * (lane ^ j), ok);
+        raw[j][0] = load8_if(latent + kKvLatent * j + 8 * (own ^ j), ok);  // r0 is a multiple of eight: row j of the swizzle
+        raw[j][1] = load8_if(latent + kKvLatent * j + 256 + 8 * (own ^ j), ok);
       }
     };
     // eight dims in half h of the token with these multipliers
@@ -193,12 +201,21 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap
     for (int i = group; i < tiles; i += kStages) {
       mults = multiplier_bytes(next_codes);
       const uint32_t bad = __ballot_sync(0xFFFFFFFFu, mults == 0u) & now;
+      // The window form has registers to convert one of a warp's sixteen before the stage is free, with where the unit's
+      // tokens lie in shared memory: 626 us for the chunks above instead of 643. Two or more, or any in the tree form, spill
+      // (64 trees: 450 us instead of 446).
+      constexpr bool kAheadOne = !kTree;
+      uint4 ready;
+      if (kAheadOne) ready = dequant8(raw[0][0], mul_of(word_of(0), 0));
       if (i >= kStages) wait_for(sh, &sh.o_done[group], ((i >> 1) - 1) & 1);
+      if (kAheadOne) st_shared16(unit, ready);
 #pragma unroll
       for (int j = 0; j < kTokensPerWarp; ++j) {
         const uint32_t word = word_of(j);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) st_shared16(unit + 4 * h * kPieceBytes + j * 128, dequant8(raw[j][h], mul_of(word, h)));
+        for (int h = kAheadOne && j == 0 ? 1 : 0; h < 2; ++h) {
+          st_shared16(unit + 4 * h * kPieceBytes + j * 128, dequant8(raw[j][h], mul_of(word, h)));
+        }
       }
       if (lane == 0) {
         // O of tile i - 2, waited for above, was issued once its softmax had read this place
