@@ -13,9 +13,9 @@ namespace block {
 //   P = exp2(S * scale - m)    the running maximum m of each row in registers
 //   O += P V    64 rows x 512 dims, 4 steps of K = 16 over the 64 tokens, two halves of N = 256
 // with tcgen05.mma.ws (M = 64) in bf16 x bf16 -> fp32, the form and the roles of the sparse attention: warps 4-19
-// load and dequantise the tokens' latents, warps 21-22 copy their position dims and prefetch (22 also finds the next unit and
-// copies its Q), warp 20 issues the matrix instructions, warps 0-3 do the softmax; all but 20-22 store the result. Keys and values are one
-// copy in shared memory: a token is a row of nine 128-byte swizzled pieces (64 dims each), read along the dims as the
+// load and dequantise the tokens' latents, warps 21-22 copy their position dims and prefetch (22 also finds the next unit
+// and copies its Q), warp 20 issues the matrix instructions, warps 0-3 do the softmax; all but 20-22 store the result.
+// Keys and values are one copy in shared memory: a token is a row of nine 128-byte swizzled pieces (64 dims each), read along the dims as the
 // K-major B operand of S and along the tokens as the N-major one of O. Two groups of eight loader warps own a stage
 // each, and hold the next tile in registers.
 //
@@ -23,8 +23,8 @@ namespace block {
 // query tokens see different tokens, so each thread of the softmax has its own mask of a tile; and parts of a
 // context are found on the device from the lengths, which the host does not know.
 //
-// What bounds it: a tile takes some 2750 clocks (1.43 us), the products' 2176 among them: M = 64 has half of the tensor
-// cores' rate. Shared memory is nearer its limit: 1408 accesses of 128 bytes by the tensor core (72 KB of keys, 64 of values,
+// What bounds it: a tile takes some 3000 clocks (1.43 us where few blocks run, 1.54 us with all), the products' 2176 among
+// them: M = 64 has half of the tensor cores' rate. Shared memory is nearer its limit: 1408 accesses of 128 bytes by the tensor core (72 KB of keys, 64 of values,
 // 24 of Q, P twice) and 1140 by the warps (72 KB of keys stored, P, and waits of either for the other) are 2550 a tile. With
 // 64 rows one copy of a token serves no more. The chain of a stage (store 2000 clocks, S 1200, softmax 1300, O 850, and the
 // other stage's S between) takes what two tiles take. A block's first unit starts in some 8000 clocks (lengths, table, first
