@@ -840,7 +840,8 @@ idx_status_t idx_tree_mask(const int32_t* parents, const int32_t* cu_rows, int32
  *                whose contexts that cuts are joined by a second launch. Its contents need no preparation and mean
  *                nothing after the call; calls that may overlap need one each. The results depend on the lengths of
  *                all requests in the last bits then, and are the same in every run.
- * Errors: as idx_sparse_attention, and IDX_ERR_INVALID_ARG for window < 1 or sinks < 0.
+ * Errors: as idx_sparse_attention, IDX_ERR_INVALID_ARG for window < 1 or sinks < 0, and IDX_ERR_UNSUPPORTED for rows,
+ * heads of q or blocks 2^40 bytes apart or more.
  */
 idx_status_t idx_window_attention(const void* q, int64_t ld_q, int64_t ld_qh, const uint8_t* cache,
                                   int32_t num_blocks, int32_t block_size, int64_t block_stride_bytes,

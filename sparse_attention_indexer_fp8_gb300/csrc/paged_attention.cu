@@ -213,6 +213,11 @@ idx_status_t paged_attention(const char* fn, PagedParams& p, float softmax_scale
   if (!aligned(p.q, 16) || p.ld_q % 8 != 0 || p.ld_qh % 8 != 0 || !aligned(p.out, 16) || p.ld_out % 8 != 0 || p.ld_oh % 8 != 0) {
     return fail(IDX_ERR_UNSUPPORTED, "%s: q and out rows must be 16-byte aligned", fn);
   }
+  constexpr int64_t kMostBytes = int64_t{1} << 40;  // between two rows, heads or blocks: what a tensor map holds
+  if ((p.T > 1 && p.ld_q >= kMostBytes / 2) || (p.H > 1 && p.ld_qh >= kMostBytes / 2) ||
+      (p.num_blocks > 1 && p.block_stride >= kMostBytes)) {
+    return fail(IDX_ERR_UNSUPPORTED, "%s: a stride of 2^40 bytes or more", fn);
+  }
   if (ws && !aligned(ws, 16)) return fail(IDX_ERR_UNSUPPORTED, "%s: the workspace is not 16-byte aligned", fn);
   if (device_sm_count() <= 0) return fail(IDX_ERR_CUDA, "%s: cannot query the SM count", fn);
   const Plan plan = plan_of(p.T, p.B, p.H);

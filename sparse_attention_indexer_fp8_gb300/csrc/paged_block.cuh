@@ -12,29 +12,30 @@ namespace block {
 //   S = Q K^T   64 rows x 64 tokens, 36 steps of K = 16 over the 576 dims
 //   P = exp2(S * scale - m)    the running maximum m of each row in registers
 //   O += P V    64 rows x 512 dims, 4 steps of K = 16 over the 64 tokens, two halves of N = 256
-// with tcgen05.mma.ws (M = 64) in bf16 x bf16 -> fp32, the form and the roles of the sparse attention: warps 4-19
-// load and dequantise the tokens' latents, warps 21-22 copy their position dims and prefetch (22 also finds the next unit
-// and copies its Q), warp 20 issues the matrix instructions, warps 0-3 do the softmax; all but 20-22 store the result.
-// Keys and values are one copy in shared memory: a token is a row of nine 128-byte swizzled pieces (64 dims each), read along the dims as the
-// K-major B operand of S and along the tokens as the N-major one of O. Two groups of eight loader warps own a stage
-// each, and hold the next tile in registers.
+// with tcgen05.mma.ws (M = 64) in bf16 x bf16 -> fp32, the form and the roles of the sparse attention: warps 4-19 load
+// and dequantise the tokens' latents, warps 21-22 copy their position dims and prefetch (22 also finds the next unit and
+// copies its Q), warp 20 issues the matrix instructions, warps 0-3 do the softmax; all but 20-22 store the result. Keys
+// and values are one copy in shared memory: a token is a row of nine 128-byte swizzled pieces (64 dims each), read along
+// the dims as the K-major B operand of S and along the tokens as the N-major one of O. Two groups of eight loader warps
+// own a stage each, and hold the next tile in registers.
 //
-// What differs: tokens lie in pages, so eight of a warp share one block and one address; rows of several
-// query tokens see different tokens, so each thread of the softmax has its own mask of a tile; and parts of a
-// context are found on the device from the lengths, which the host does not know.
+// What differs: tokens lie in pages, so eight of a warp share one block and one address; rows of several query tokens
+// see different tokens, so each thread of the softmax has its own mask of a tile; and parts of a context are found on
+// the device from the lengths, which the host does not know.
 //
-// What bounds it: a tile takes some 3000 clocks (1.43 us where few blocks run, 1.54 us with all), the products' 2176 among
-// them: M = 64 has half of the tensor cores' rate. Shared memory is nearer its limit: 1408 accesses of 128 bytes by the tensor core (72 KB of keys, 64 of values,
-// 24 of Q, P twice) and 1140 by the warps (72 KB of keys stored, P, and waits of either for the other) are 2550 a tile. With
-// 64 rows one copy of a token serves no more. The chain of a stage (store 2000 clocks, S 1200, softmax 1300, O 850, and the
-// other stage's S between) takes what two tiles take. A block's first unit starts in some 8000 clocks (lengths, table, first
-// tokens and Q are four round trips), a later one in 4300, and a unit ends in some 5000.
-// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 626 us (37 % of the bf16 rate); 64 trees of 4 to
-// 8 nodes, 64 heads, contexts of 4096 to 8192: 447 us (44 %); one tree of 8 nodes, 128 heads, 32768 tokens: 102 us (38 %).
-// Pairs of blocks on one product of M = 256 with half of the values' dims each (full rate, but S twice) took 699, 484
-// and 96 us, and lost more in units that are not full. Copies of Q and position dims by the threads added 1 % to
-// the chunks (a 16-byte copy is an access for every 32 bytes), S and O in halves that overlap the stores 2 %, results stored
-// by bulk copies 1 %.
+// What bounds it: a tile takes some 3000 clocks (1.43 us where few blocks run, 1.54 us with all), the products' 2176
+// among them: M = 64 has half of the tensor cores' rate. Shared memory is nearer its limit: 1408 accesses of 128 bytes
+// by the tensor core (72 KB of keys, 64 of values, 24 of Q, P twice) and 1140 by the warps (72 KB of keys stored, P, and
+// waits of either for the other) are 2550 a tile. With 64 rows one copy of a token serves no more. The chain of a stage
+// (store 2000 clocks, S 1200, softmax 1300, O 850, and the other stage's S between) takes what two tiles take. A block's
+// first unit starts in some 8000 clocks (lengths, table, first tokens and Q are four round trips), a later one in 4300,
+// and a unit ends in some 5000.
+// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 626 us (37 % of the bf16 rate); 64 trees of 4
+// to 8 nodes, 64 heads, contexts of 4096 to 8192: 447 us (44 %); one tree of 8 nodes, 128 heads, 32768 tokens: 102 us
+// (38 %). Pairs of blocks on one product of M = 256 with half of the values' dims each (full rate, but S twice) took
+// 699, 484 and 96 us, and lost more in units that are not full. Copies of Q and position dims by the threads added 1 %
+// to the chunks (a 16-byte copy is an access for every 32 bytes), S and O in halves that overlap the stores 2 %, results
+// stored by bulk copies 1 %.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 64;                        // of a unit
 constexpr int kQBytes = kPieces * kPieceBytes;

@@ -76,6 +76,13 @@ def test_attention_refusals(lib, which, change, status):
     assert call(*_args(base, change)) == status
 
 
+@pytest.mark.parametrize("which", ["window", "tree"])
+@pytest.mark.parametrize("change", [{"ld_q": 1 << 39}, {"ld_qh": 1 << 39}, {"stride": 1 << 40}])
+def test_strides_beyond_a_tensor_map(lib, which, change):
+    call, base = (lib.idx_window_attention, WINDOW) if which == "window" else (lib.idx_tree_attention, TREE)
+    assert call(*_args(base, change)) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("change,status", [({"window": 0}, INVALID), ({"window": -5}, INVALID), ({"sinks": -1}, INVALID)])
 def test_window_refusals(lib, change, status):
     assert lib.idx_window_attention(*_args(WINDOW, change)) == status
