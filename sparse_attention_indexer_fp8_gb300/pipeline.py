@@ -17,6 +17,8 @@ for the cache fill and the decode and hierarchical steps.
 
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -35,6 +37,13 @@ def _workspace(op: str, rows: int, ld: int, k: int, device) -> torch.Tensor | No
     with torch.cuda.device(torch.device(device)):
         nbytes = idx_workspace_bytes(op, rows, ld, k)
     return torch.zeros((nbytes // 4,), dtype=torch.int32, device=device).view(rows, 1024) if nbytes else None
+
+
+def _stream_context(stream, device):
+    """Torch's operations on the stream that a call was given (None: they stay on the device's current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device))
 
 
 def _insert(kv: str):
@@ -279,6 +288,7 @@ class TreeStep:
             return torch.zeros(shape, dtype=dtype, device=device)
 
         self.ctx_lens, self.cu_rows = ints(requests), ints(requests + 1)
+        self.base_lens = ints(requests)
         self.held_pages, self.free_end = ints(requests), ints(1)
         self.row_positions, self.slots = ints(rows), ints(rows, dtype=torch.int64)
         self.positions, self.mask = ints(rows), ints(rows, words)
@@ -290,11 +300,18 @@ class TreeStep:
 
     def plan(self, cached_lens, new_lens, parents, free_blocks, block_table, held_pages=None, free_start=None, stream=None):
         """Lengths and ``held_pages`` int32 [requests], ``parents`` int32 [rows] (within the request, -1: none);
-        ``block_table`` is updated. See ``idx_build_tables`` and ``idx_tree_mask``."""
+        ``block_table`` is updated. ``cached_lens``, ``held_pages`` and ``free_start`` may be the step's own ``ctx_lens``,
+        ``held_pages`` and ``free_end``, which go on from step to step then. See ``idx_build_tables`` and ``idx_tree_mask``."""
+        base = cached_lens
+        if cached_lens.data_ptr() == self.ctx_lens.data_ptr():
+            # the tables advance it, and the nodes' positions count from what it was before
+            base = self.base_lens
+            with _stream_context(stream, self.ctx_lens.device):
+                base.copy_(cached_lens)
         idx_build_tables(cached_lens, new_lens, free_blocks, block_table, self.block_size, self.ctx_lens, self.cu_rows,
                          self.row_positions, self.slots, held_pages=held_pages, held_out=self.held_pages,
                          free_start=free_start, free_end=self.free_end, stream=stream)
-        idx_tree_mask(parents, self.cu_rows, self.mask, base_lens=cached_lens, positions=self.positions, stream=stream)
+        idx_tree_mask(parents, self.cu_rows, self.mask, base_lens=base, positions=self.positions, stream=stream)
 
     def layer(self, kv, kv_weight, cos_sin, q, kv_cache, block_table, stream=None):
         """``kv`` [rows, 576] is the attention projection, ``q`` [rows, heads, 576] the absorbed and rotated query."""

@@ -1,0 +1,70 @@
+"""Steps of drafted trees that carry their own lengths on, and what a step refuses, on the GPU."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_fp8_gb300 as idx
+from oracle import paged as P
+from sparse_attention_indexer_fp8_gb300.pipeline import TreeStep
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BS, PAGES = 16, 12
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    from sparse_attention_indexer_fp8_gb300.build import build_library
+
+    build_library()
+    idx.library()
+    yield
+    idx.idx_device_error()
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("how", ["eager", "stream", "raw stream", "graph"])
+def test_lengths_pages_and_blocks_carried_on_in_place(how):
+    """ctx_lens, held_pages and free_end of one step are the inputs of the next, in the step's own tensors."""
+    B, rows = 4, 40
+    rng = np.random.default_rng(3)
+    step = TreeStep(B, rows, 2, words=2, block_size=BS, device=DEV)
+    ids = rng.permutation(B * PAGES)
+    table, free = torch.full((B, PAGES), -1, dtype=torch.int32, device=DEV), i32(ids)
+    new, parents = i32([0] * B), i32([-1] * rows)
+    side = torch.cuda.Stream() if how != "eager" else torch.cuda.current_stream()
+    stream = {"stream": side, "raw stream": side.cuda_stream}.get(how)
+
+    def plan():
+        step.plan(step.ctx_lens, new, parents, free, table, held_pages=step.held_pages, free_start=step.free_end, stream=stream)
+
+    graph = None
+    if how == "graph":
+        with torch.cuda.stream(side):
+            plan()  # of no tokens: loads the kernels before the capture
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            plan()
+    host_table, ctx, held, at = np.full((B, PAGES), -1), np.zeros(B, dtype=np.int64), np.zeros(B, dtype=np.int64), 0
+    for counts in ([30, 0, 1, 8], [3, 5, 20, 12], [0, 0, 0, 0], [10, 1, 7, 16]):
+        trees = [[int(rng.integers(max(-1, i - 4), i)) for i in range(n)] for n in counts]
+        new.copy_(i32(counts))
+        parents.copy_(i32(sum(trees, []) + [9] * (rows - sum(counts))))
+        torch.cuda.synchronize()
+        graph.replay() if graph else plan()
+        torch.cuda.synchronize()
+        idx.idx_device_error()
+        want = P.build_tables(ctx, counts, ids, host_table, BS, rows, held, at)
+        n = sum(counts)
+        base = np.repeat(ctx, counts)
+        depth = [len(s) - 1 for t in trees for s in P.tree_sets(t)]
+        assert step.positions[:n].tolist() == [int(b) + d for b, d in zip(base, depth)]
+        assert step.row_positions.tolist() == want["positions"].tolist() and step.slots.tolist() == want["slots"].tolist()
+        assert np.array_equal(table.cpu().numpy(), want["table"])
+        host_table, ctx, held, at = want["table"], want["ctx_lens"], want["held"], want["free_end"]
+        assert step.ctx_lens.tolist() == ctx.tolist() and step.held_pages.tolist() == held.tolist() and step.free_end.item() == at

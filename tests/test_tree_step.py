@@ -1,0 +1,54 @@
+"""The step of drafted trees on the host: which tensors its calls get, and what it refuses (CPU only).
+
+The step's calls are replaced by records of themselves that do on the host what the test looks at, so no GPU is needed.
+"""
+
+import contextlib
+
+import pytest
+import torch
+
+from sparse_attention_indexer_fp8_gb300 import pipeline
+
+B, ROWS, H, BS, PAGES = 3, 12, 8, 16, 5
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """(name, base_lens as they are when the masks are made) of the calls, in order."""
+    made = []
+
+    def tables(cached, new, free, table, bs, ctx, cu, *a, **k):
+        made.append(("tables", None))
+        ctx.copy_(cached + new)  # as the header allows, also where ctx is cached
+
+    def masks(parents, cu, mask, base_lens=None, positions=None, stream=None):
+        made.append(("masks", base_lens.tolist()))
+
+    monkeypatch.setattr(pipeline, "idx_build_tables", tables)
+    monkeypatch.setattr(pipeline, "idx_tree_mask", masks)
+    monkeypatch.setattr(pipeline, "idx_kv_norm_rope_quant_and_cache", lambda *a, **k: made.append(("insert", None)))
+    monkeypatch.setattr(pipeline, "idx_tree_attention", lambda *a, **k: made.append(("attention", None)))
+    monkeypatch.setattr(pipeline, "idx_paged_attention_workspace_bytes", lambda *a: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    return made
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def plan_arguments(**change):
+    a = dict(cached_lens=i32(B), new_lens=i32(B) + 2, parents=i32(ROWS), free_blocks=i32(20), block_table=i32(B, PAGES))
+    a.update(change)
+    return a
+
+
+def test_lengths_that_the_step_advances_itself(calls):
+    """cached_lens may be the step's own ctx_lens: positions count from the lengths before the step."""
+    step = pipeline.TreeStep(B, ROWS, H, block_size=BS, device="cpu")
+    step.plan(**plan_arguments(cached_lens=torch.tensor([5, 0, 9], dtype=torch.int32)))
+    step.plan(**plan_arguments(cached_lens=step.ctx_lens))
+    step.plan(**plan_arguments(cached_lens=step.ctx_lens))
+    assert step.ctx_lens.tolist() == [11, 6, 15]
+    assert [c for c in calls if c[0] == "masks"] == [("masks", [5, 0, 9]), ("masks", [7, 2, 11]), ("masks", [9, 4, 13])]
