@@ -282,6 +282,14 @@ class TreeStep:
 
     def __init__(self, requests: int, rows: int, heads: int, words: int = 2, block_size: int = W.BLOCK_SIZE, device="cuda",
                  softmax_scale: float = W.ATTN_HEAD_DIM ** -0.5, eps: float = 1e-6, interleaved: bool = False):
+        # what the second call of ``plan`` or ``layer`` would refuse, when the first is enqueued already
+        for name, value, most in (("requests", requests, 8192), ("heads", heads, 1024), ("words", words, 32)):
+            if not (name == "words") <= value <= most:
+                raise ValueError(f"TreeStep: {name} {value}, at most {most} are taken")
+        if block_size not in (16, 32, 64, 128):
+            raise ValueError(f"TreeStep: block_size {block_size} is not one of 16, 32, 64, 128")
+        if not abs(softmax_scale) < 2.358e38:  # times log2(e) it is a binary32 number
+            raise ValueError(f"TreeStep: softmax_scale {softmax_scale}")
         self.block_size, self.softmax_scale, self.eps, self.interleaved = block_size, softmax_scale, eps, interleaved
 
         def ints(*shape, dtype=torch.int32):
@@ -302,6 +310,10 @@ class TreeStep:
         """Lengths and ``held_pages`` int32 [requests], ``parents`` int32 [rows] (within the request, -1: none);
         ``block_table`` is updated. ``cached_lens``, ``held_pages`` and ``free_start`` may be the step's own ``ctx_lens``,
         ``held_pages`` and ``free_end``, which go on from step to step then. See ``idx_build_tables`` and ``idx_tree_mask``."""
+        # the masks' arguments, before the tables count a block: after a refusal the same plan may be tried again
+        fn, dev = "TreeStep", self.out.get_device()
+        _vec(fn, "cached_lens", cached_lens, dev, torch.int32, self.ctx_lens.shape[0])
+        _vec(fn, "parents", parents, dev, torch.int32, self.positions.shape[0])
         base = cached_lens
         if cached_lens.data_ptr() == self.ctx_lens.data_ptr():
             # the tables advance it, and the nodes' positions count from what it was before
@@ -315,6 +327,12 @@ class TreeStep:
 
     def layer(self, kv, kv_weight, cos_sin, q, kv_cache, block_table, stream=None):
         """``kv`` [rows, 576] is the attention projection, ``q`` [rows, heads, 576] the absorbed and rotated query."""
+        # the attention's arguments, before the insert
+        fn, dev, (rows, heads, _) = "TreeStep", self.out.get_device(), self.out.shape
+        _mat(fn, "block_table", block_table, dev, torch.int32, self.ctx_lens.shape[0], None)
+        ptr, ld, ld_head = _heads(fn, "q", q, dev, rows, heads, W.ATTN_DIM)
+        if ptr % 16 or ld % 8 or ld_head % 8 or min(ld, ld_head) < W.ATTN_DIM:
+            raise ValueError(f"{fn}: q's rows and heads must begin at 16-byte boundaries and not overlap, its strides are {q.stride()}")
         idx_kv_norm_rope_quant_and_cache(kv[:, :512], kv[:, 512:], kv_weight, self.eps, self.positions, cos_sin, self.slots,
                                          kv_cache, self.block_size, interleaved=self.interleaved, stream=stream)
         idx_tree_attention(q, kv_cache, self.block_size, block_table, self.cu_rows, self.ctx_lens, self.mask, self.out,

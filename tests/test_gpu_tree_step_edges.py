@@ -68,3 +68,18 @@ def test_lengths_pages_and_blocks_carried_on_in_place(how):
         assert np.array_equal(table.cpu().numpy(), want["table"])
         host_table, ctx, held, at = want["table"], want["ctx_lens"], want["held"], want["free_end"]
         assert step.ctx_lens.tolist() == ctx.tolist() and step.held_pages.tolist() == held.tolist() and step.free_end.item() == at
+
+
+def test_a_refused_plan_takes_no_blocks():
+    """After a refusal the same step is planned again, with the step's own pages and start: every block counts once."""
+    B, rows = 2, 30
+    step = TreeStep(B, rows, 2, words=1, block_size=BS, device=DEV)
+    table, free = torch.full((B, PAGES), -1, dtype=torch.int32, device=DEV), torch.arange(50, dtype=torch.int32, device=DEV)
+    lens, parents = i32([20, 10]), i32([-1] * rows)
+    for bad in (parents[:-1], parents.long(), i32([-1] * 2 * rows)[::2]):
+        with pytest.raises(ValueError, match="parents"):
+            step.plan(step.ctx_lens, lens, bad, free, table, held_pages=step.held_pages, free_start=step.free_end)
+    step.plan(step.ctx_lens, lens, parents, free, table, held_pages=step.held_pages, free_start=step.free_end)
+    idx.idx_device_error()
+    assert step.ctx_lens.tolist() == [20, 10] and step.held_pages.tolist() == [2, 1] and step.free_end.item() == 3
+    assert table[:, :3].tolist() == [[0, 1, -1], [2, -1, -1]]
