@@ -826,7 +826,7 @@ idx_status_t idx_tree_mask(const int32_t* parents, const int32_t* cu_rows, int32
  *   s[h, j] = softmax_scale * sum_d q[t, h, d] * K_j[d]
  *   out[t, h] = sum_j exp(s[h, j]) V_j / sum_j exp(s[h, j]),   lse[t, h] = ln(sum_j exp(s[h, j])).
  * A row that sees no token (p < 0) gets out = 0 and lse = -inf; rows outside [cu_rows[0], cu_rows[B]) are left as
- * they were. Pages that no row sees are not looked up: their table entries and blocks may be anything. A token that
+ * they were. Pages that no row sees do not count: their table entries and blocks may be anything. A token that
  * a row does not see has no part in its result, whatever the record holds; one that reads as NaN (see
  * idx_kv_norm_rope_quant_and_cache) makes the results of the rows that see it NaN. Precision as idx_sparse_attention.
  *

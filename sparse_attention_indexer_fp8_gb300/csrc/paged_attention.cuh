@@ -135,6 +135,22 @@ __device__ __forceinline__ int most_tiles(const PagedParams& p, int n, int ctx) 
   return max(static_cast<int>(min(static_cast<int64_t>(all), near + (min(p.sinks, ctx) + kTile - 1) / kTile)), 1);
 }
 
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Whether one of `rows` masks, every `step`-th from `row` on, has a bit of nodes [from, to). Asked only where a page is
+// missing, to say whether that is an error; not inlined, so that it takes no registers from the loops around it.
+static __device__ __noinline__ bool nodes_seen(const int32_t* masks, int64_t ld_mask, int words, int row, int rows, int step,
+                                               int from, int to) {
+  for (; row < rows; row += step) {
+    for (int w = from >> 5; w < words && 32 * w < to; ++w) {
+      const uint32_t in = ~low_bits(from - 32 * w) & low_bits(to - 32 * w);
+      if (static_cast<uint32_t>(__ldg(masks + row * ld_mask + w)) & in) return true;
+    }
+  }
+  return false;
+}
+
 // Completes a unit of rows from `start` on, of a request whose n new rows begin at row `at`; its tiles are [u.tile0,
 // u.tile0 + u.tiles) as far as there are as many. False: it has no row.
 template <bool kTree>
@@ -147,7 +163,13 @@ __device__ __forceinline__ bool complete_unit(const PagedParams& p, int at, int 
   u.base = u.ctx - n;
   u.pos0 = u.base + start;
   const int all = seen_tiles<kTree>(p, start, start + u.rows - 1, u);
-  if (u.ctx > table_tokens(p) && (threadIdx.x & 31) == 0) atomicOr(&g_paged_error, 1u);
+  const int known = table_tokens(p);
+  if (u.ctx > known) {  // the last of a window's rows sees the last token, of nodes their masks tell
+    const int lane = threadIdx.x & 31;
+    const bool seen = !kTree || u.base > known ||
+                      nodes_seen(p.mask + u.row0 * p.ld_mask, p.ld_mask, p.words, lane, u.rows, 32, max(known - u.base, 0), n);
+    if (seen) atomicOr(&g_paged_error, 1u);
+  }
   u.tiles = max(min(u.tiles, all - u.tile0), 0);
   return true;
 }
@@ -385,9 +407,6 @@ __device__ __forceinline__ int entry_of(const PagedParams& p, const Unit& u, int
 __device__ __forceinline__ bool is_block(const PagedParams& p, int entry) {
   return static_cast<uint32_t>(entry) < static_cast<uint32_t>(p.num_blocks);
 }
-
-// The lowest n bits.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
 // Tokens [lo, hi] are all seen by row t of the unit; most tiles lie within.
 template <bool kTree>

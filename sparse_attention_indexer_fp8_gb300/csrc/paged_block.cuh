@@ -284,7 +284,13 @@ __device__ __forceinline__ void run_unit(const PagedParams& p, const CUtensorMap
         const uint32_t page = copy_tokens == 32 ? 0xFFFFFFFFu : lane < 16 ? 0xFFFFu : 0xFFFF0000u;
         first[h] = __ballot_sync(0xFFFFFFFFu, mine && lane == __ffs(have & page) - 1);
         copied += __popc(first[h]);
-        if (!mine && unit_sees(u, j)) atomicOr(&g_paged_error, 1u);
+        if (!mine && unit_sees(u, j)) {
+          const int node = j - u.base;
+          if (!kTree || node < 0 ||
+              nodes_seen(p.mask + u.row0 * p.ld_mask, p.ld_mask, p.words, 0, u.rows, 1, node, node + 1)) {
+            atomicOr(&g_paged_error, 1u);
+          }
+        }
         here[h] = entry(i + kStages, h);
       }
       // only S reads position dims, so their piece is free long before the stage is
