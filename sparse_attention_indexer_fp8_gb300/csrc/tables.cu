@@ -54,6 +54,9 @@ struct TableParams {
 // ---------------------------------------------------------------------------
 constexpr int kClusterBlocks = 8;  // the portable cluster size
 constexpr int kMaxTableThreads = 1024;
+constexpr size_t kTableSmemUnasked = 47 * 1024;  // with warp_sums, 48 KB are a block's without asking for more
+
+constexpr size_t table_smem_bytes(int requests) { return (4 * static_cast<size_t>(requests) + 2) * sizeof(int32_t); }
 
 // The last b in [0, n) with first[b] <= i, for first[0] <= i.
 __device__ __forceinline__ int last_at_most(const int32_t* first, int n, int i) {
@@ -315,10 +318,12 @@ extern "C" idx_status_t idx_build_tables(const int32_t* cached_lens, const int32
   const int most = std::max(B + 1, n_rows);
   const bool cluster = most > 2 * kMaxTableThreads;
   const int threads = std::min(kMaxTableThreads, (std::max(most, 64) + 31) / 32 * 32);
-  const size_t smem = (4 * static_cast<size_t>(B) + 2) * sizeof(int32_t);
+  const size_t smem = table_smem_bytes(B);
   auto* kernel = cluster ? build_tables_kernel<true> : build_tables_kernel<false>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (smem > kTableSmemUnasked) {
+    // of the most requests, whatever this call's: another thread's smaller call must not take back what this one needs
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(table_smem_bytes(IDX_TABLES_MAX_REQUESTS)));
     if (e != cudaSuccess) return fail(IDX_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
   }
   cudaLaunchAttribute attr[1];

@@ -1,0 +1,71 @@
+"""Step tables and tree masks at the edges: sums beyond 32 bits, request counts around what a block holds, calls at once."""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_fp8_gb300 as idx
+from oracle import paged as P
+from test_gpu_tables import call, i32, outputs, same
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    from sparse_attention_indexer_fp8_gb300.build import build_library
+
+    build_library()
+    idx.library()
+    yield
+    idx.idx_device_error()
+
+
+@pytest.mark.parametrize("B", [3023, 3024, 3050, 3071, 4500])
+@pytest.mark.parametrize("new", [1, 2])
+def test_request_counts_around_what_a_block_holds_without_asking(B, new):
+    """Sums of about 3000 requests reach the 48 KB of shared memory that a block has by default."""
+    rng = np.random.default_rng(B)
+    cached, bs = rng.integers(0, 50, B), 16
+    add = rng.integers(0, new + 1, B)
+    pages = 5
+    ids, table = rng.permutation(B * pages), rng.integers(0, B * pages, (B, pages))
+    rows = int(add.sum()) + 2
+    want = P.build_tables(cached, add, ids, table, bs, rows)
+    o, t = outputs(B, rows), i32(table)
+    call(o, i32(cached), i32(add), i32(ids), t, bs)
+    idx.idx_device_error()
+    same(o, t, want)
+
+
+def test_calls_of_two_threads():
+    """Calls of different sizes from two threads at once, each on its own stream: each is launched and right."""
+    failed = []
+
+    def work(B, seed):
+        try:
+            rng = np.random.default_rng(seed)
+            cached, add, bs, pages = rng.integers(0, 50, B), np.ones(B, dtype=np.int64), 16, 4
+            ids, table = rng.permutation(B * pages), rng.integers(0, B * pages, (B, pages))
+            want = P.build_tables(cached, add, ids, table, bs, B)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                o, t = outputs(B, B), i32(table)
+                args = i32(cached), i32(add), i32(ids), t, bs
+                for _ in range(500):
+                    call(o, *args)
+                stream.synchronize()
+                same(o, t, want)
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(B, s)) for s, B in enumerate((8192, 3500))]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not failed
+    idx.idx_device_error()
