@@ -56,7 +56,7 @@ constexpr int kClusterBlocks = 8;  // the portable cluster size
 constexpr int kMaxTableThreads = 1024;
 constexpr size_t kTableSmemUnasked = 47 * 1024;  // with warp_sums, 48 KB are a block's without asking for more
 
-constexpr size_t table_smem_bytes(int requests) { return (4 * static_cast<size_t>(requests) + 2) * sizeof(int32_t); }
+constexpr size_t table_smem_bytes(int requests) { return (5 * static_cast<size_t>(requests) + 2) * sizeof(int32_t); }
 
 // The last b in [0, n) with first[b] <= i, for first[0] <= i.
 __device__ __forceinline__ int last_at_most(const int32_t* first, int n, int i) {
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kMaxTableThreads) build_tables_kernel(const Ta
   int32_t* fresh_at = rows_at + p.B + 1;    // [B + 1] its first fresh block, counted from free_start
   int32_t* cached_s = fresh_at + p.B + 1;   // [B]
   int32_t* held_s = cached_s + p.B;         // [B]
+  int32_t* ctx_s = held_s + p.B;            // [B] kept apart: the sums may be held to 2^31 - 1
   __shared__ int64_t warp_sums[3][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int rank = kCluster ? static_cast<int>(blockIdx.x) : 0;
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kMaxTableThreads) build_tables_kernel(const Ta
       fresh_at[b] = to_int32(s[1] - v[1]);
       cached_s[b] = cached;
       held_s[b] = held;
+      ctx_s[b] = static_cast<int>(v[2]);
     }
     // cu_ctx is none of the inputs, so it is written at once
     if (rank == 0 && p.cu_ctx && b < p.B) {
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kMaxTableThreads) build_tables_kernel(const Ta
   for (int b = me; b <= p.B; b += step) {
     p.cu_rows[b] = rows_at[b];
     if (b == p.B) break;
-    p.ctx_lens[b] = cached_s[b] + (rows_at[b + 1] - rows_at[b]);
+    p.ctx_lens[b] = ctx_s[b];
     if (p.held_out) {
       const int need = fresh_at[b + 1] - fresh_at[b];
       p.held_out[b] = held_s[b] + min(need, max(available - fresh_at[b], 0));

@@ -69,3 +69,20 @@ def test_calls_of_two_threads():
         x.join()
     assert not failed
     idx.idx_device_error()
+
+
+@pytest.mark.parametrize("aliased", [False, True])
+def test_lengths_are_whole_where_the_sum_of_rows_is_held(aliased):
+    """Only sums are held to 2^31 - 1: every request's own length is its cached and its new tokens."""
+    cached, add = [1, 2, 3, 4], [2 ** 30, 2 ** 30, 2 ** 30, 5]
+    o, t = outputs(4, 3), torch.full((4, 1), 6, dtype=torch.int32, device=DEV)
+    lens = i32(cached)
+    if aliased:
+        o["ctx_lens"] = lens
+    call(o, lens, i32(add), i32([9]), t, 64, held=i32([1] * 4))
+    with pytest.raises(idx.IdxError, match="tables 0x0000000d"):
+        idx.idx_device_error()
+    assert o["ctx_lens"].tolist() == [c + a for c, a in zip(cached, add)]
+    assert o["cu_rows"].tolist() == [0, 2 ** 30, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]
+    assert o["cu_ctx"].tolist() == [0, 2 ** 30 + 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]
+    assert o["positions"].tolist() == [1, 2, 3] and o["slots"].tolist() == [6 * 64 + 1, 6 * 64 + 2, 6 * 64 + 3]
