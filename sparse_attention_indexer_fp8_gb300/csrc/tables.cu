@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kMaxTableThreads) build_tables_kernel(const Ta
   }
   for (uint32_t i = me; i < static_cast<uint32_t>(total_fresh); i += step) {
     const int f = static_cast<int>(i), b = last_at_most(fresh_at, p.B, f);
-    const int page = held_s[b] + f - fresh_at[b];
+    const int page = held_s[b] + (f - fresh_at[b]);
     p.table[b * p.ld_bt + page] = f < available ? __ldg(p.free_blocks + start + f) : -1;
   }
   const int mask = (1 << p.shift) - 1;
@@ -193,14 +193,14 @@ __global__ void __launch_bounds__(kMaxTableThreads) build_tables_kernel(const Ta
     int64_t slot = -1;
     if (r < total_rows) {
       req = last_at_most(rows_at, p.B, r);
-      pos = cached_s[req] + r - rows_at[req];
+      pos = cached_s[req] + (r - rows_at[req]);  // each sum on the way fits too
       ke = pos + 1;
       const int page = pos >> p.shift;
       int block = -1;
       if (page < held_s[req]) {
         block = p.table[req * p.ld_bt + page];
       } else if (page < p.n_pages) {
-        const int f = fresh_at[req] + page - held_s[req];
+        const int f = fresh_at[req] + (page - held_s[req]);
         if (f < available) block = __ldg(p.free_blocks + start + f);
       }
       if (block >= 0) slot = (static_cast<int64_t>(block) << p.shift) + (pos & mask);

@@ -86,3 +86,17 @@ def test_lengths_are_whole_where_the_sum_of_rows_is_held(aliased):
     assert o["cu_rows"].tolist() == [0, 2 ** 30, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]
     assert o["cu_ctx"].tolist() == [0, 2 ** 30 + 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]
     assert o["positions"].tolist() == [1, 2, 3] and o["slots"].tolist() == [6 * 64 + 1, 6 * 64 + 2, 6 * 64 + 3]
+
+
+def test_positions_near_the_end_of_32_bits():
+    """A late request's rows: neither its length nor the row's number alone is near 2^31, their sum is."""
+    B, n = 3, 40
+    cached, add = [0, 2 ** 31 - 41, 2 ** 31 - 21], [n, n, 20]
+    o, t = outputs(B, 2 * n + 25), torch.full((B, 3), 5, dtype=torch.int32, device=DEV)
+    call(o, i32(cached), i32(add), i32([1]), t, 128, held=i32([3] * B))
+    with pytest.raises(idx.IdxError, match="tables 0x00000005"):
+        idx.idx_device_error()
+    want = list(range(n)) + [2 ** 31 - 41 + i for i in range(n)] + [2 ** 31 - 21 + i for i in range(20)]
+    assert o["positions"].tolist() == want + [0] * 5
+    assert o["row_ke"].tolist() == [p + 1 for p in want] + [0] * 5
+    assert o["ctx_lens"].tolist() == [n, 2 ** 31 - 1, 2 ** 31 - 1]
