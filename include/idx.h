@@ -783,7 +783,7 @@ size_t idx_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t k);
  * length (its request counts as empty), a page count outside [0, n_pages] or more new tokens than n_rows (those
  * beyond are not written) raise the device flag. Sums beyond 2^31 - 1 are held to it.
  * Errors: IDX_ERR_INVALID_ARG for NULL pointers, negative sizes or a short stride; IDX_ERR_UNSUPPORTED for another
- * block_size or more than IDX_TABLES_MAX_REQUESTS requests.
+ * block_size, more than IDX_TABLES_MAX_REQUESTS requests, or 2^31 table entries (B * n_pages) or more.
  */
 #define IDX_TABLES_MAX_REQUESTS 8192
 idx_status_t idx_build_tables(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* held_pages,

@@ -290,6 +290,9 @@ extern "C" idx_status_t idx_build_tables(const int32_t* cached_lens, const int32
   if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) {
     return fail(IDX_ERR_UNSUPPORTED, "%s: block_size %d is not one of 16, 32, 64, 128", fn, block_size);
   }
+  if (static_cast<int64_t>(B) * n_pages > INT32_MAX) {  // fresh blocks of all requests are numbered in 32 bits
+    return fail(IDX_ERR_UNSUPPORTED, "%s: a table of %d x %d entries", fn, B, n_pages);
+  }
   if (ld_bt < n_pages) return fail(IDX_ERR_INVALID_ARG, "%s: ld_bt is smaller than n_pages", fn);
   if (!cu_rows || (B > 0 && (!cached_lens || !new_lens || !ctx_lens)) || (B > 0 && n_pages > 0 && !block_table) ||
       (n_free > 0 && !free_blocks) || (n_rows > 0 && (!positions || !slot_mapping))) {
