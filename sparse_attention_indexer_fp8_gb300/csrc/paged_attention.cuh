@@ -107,6 +107,9 @@ __device__ __forceinline__ int table_tokens(const PagedParams& p) {
   return static_cast<int>(min(static_cast<int64_t>(p.n_pages) << p.page_shift, static_cast<int64_t>(INT32_MAX)));
 }
 
+// Tiles of n tokens, of as many as 32 bits count.
+__device__ __forceinline__ int tiles_of(int n) { return n / kTile + (n % kTile > 0); }
+
 // Which tokens rows [first, last] of the unit's request see together, and the number of their tiles.
 template <bool kTree>
 __device__ __forceinline__ int seen_tiles(const PagedParams& p, int first, int last, Unit& u) {
@@ -121,7 +124,7 @@ __device__ __forceinline__ int seen_tiles(const PagedParams& p, int first, int l
   }
   u.hi = min(u.hi, table_tokens(p) - 1);
   u.tile_lo = u.lo / kTile;
-  u.skip = min((u.first + kTile - 1) / kTile, u.tile_lo);
+  u.skip = min(tiles_of(u.first), u.tile_lo);
   if (u.hi < 0) return u.skip = 0;
   return u.skip + max(u.hi / kTile - u.tile_lo + 1, 0);
 }
@@ -129,10 +132,10 @@ __device__ __forceinline__ int seen_tiles(const PagedParams& p, int first, int l
 // No unit of a request with n new rows has more tiles.
 template <bool kTree>
 __device__ __forceinline__ int most_tiles(const PagedParams& p, int n, int ctx) {
-  const int all = (min(ctx, table_tokens(p)) + kTile - 1) / kTile;
+  const int all = tiles_of(min(ctx, table_tokens(p)));
   if (kTree) return max(all, 1);
   const int64_t near = (static_cast<int64_t>(p.window) + min(p.tokens, n) - 2) / kTile + 2;
-  return max(static_cast<int>(min(static_cast<int64_t>(all), near + (min(p.sinks, ctx) + kTile - 1) / kTile)), 1);
+  return max(static_cast<int>(min(static_cast<int64_t>(all), near + tiles_of(min(p.sinks, ctx)))), 1);
 }
 
 // The lowest n bits.

@@ -73,3 +73,16 @@ def test_pages_of_nodes_that_no_row_sees_may_be_missing(H, with_ws):
     c.tree(i32(wide), ws=ws)
     flagged()
     c.check(c.tree_seen(i32(bits)))
+
+
+@pytest.mark.parametrize("with_ws", [False, True])
+@pytest.mark.parametrize("pages", [2, 40])
+def test_first_tokens_of_a_context_at_the_end_of_32_bits(pages, with_ws):
+    """Every token is one of the first, and the context is longer than its table: what the table has counts."""
+    c = Case(64, [1, 1], [64 * pages, 64 * pages], 64, seed=41)
+    have = list(c.ctxs)
+    c.ctxs = [2 ** 31 - 1, 64 * pages]
+    c.window(2 ** 31 - 1, 2 ** 31 - 1, ws=c.workspace() if with_ws else None)
+    flagged()
+    c.ctxs = have
+    c.check(lambda b, i: list(range(64 * pages)))
