@@ -229,7 +229,7 @@ tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict_
                  int32_t* __restrict__ positions) {
   __shared__ int16_t up[kTreeNodes];
   const int b = blockIdx.x;
-  const int first = max(__ldg(cu_rows + b), 0), end = min(__ldg(cu_rows + b + 1), n_rows);
+  const int first = min(max(__ldg(cu_rows + b), 0), n_rows), end = min(max(__ldg(cu_rows + b + 1), first), n_rows);
   const int n = end - first, known = min(n, 32 * words);
   const int base = base_lens ? __ldg(base_lens + b) : 0;
   bool bad = n > known;

@@ -100,3 +100,18 @@ def test_positions_near_the_end_of_32_bits():
     assert o["positions"].tolist() == want + [0] * 5
     assert o["row_ke"].tolist() == [p + 1 for p in want] + [0] * 5
     assert o["ctx_lens"].tolist() == [n, 2 ** 31 - 1, 2 ** 31 - 1]
+
+
+@pytest.mark.parametrize("cu,written", [
+    ([2 ** 31 - 1, -2 ** 31], []), ([-2 ** 31, 2 ** 31 - 1], list(range(6))), ([4, 1], []), ([7, 9], []), ([-5, -2], []), ([5, 5], []),
+    ([3, 2 ** 31 - 1], [3, 4, 5])])
+def test_tree_mask_rows_of_any_bounds(cu, written):
+    """Whatever cu_rows holds, only rows that there are are read and written."""
+    mask = torch.full((6, 1), -9, dtype=torch.int32, device=DEV)
+    pos = torch.full((6,), -9, dtype=torch.int32, device=DEV)
+    idx.idx_tree_mask(i32([-1] * 6), i32(cu), mask, positions=pos, base_lens=i32([3]))
+    idx.idx_device_error()
+    want = [-9] * 6
+    for i, r in enumerate(written):
+        want[r] = 1 << i
+    assert mask[:, 0].tolist() == want and pos.tolist() == [3 if r in written else -9 for r in range(6)]
