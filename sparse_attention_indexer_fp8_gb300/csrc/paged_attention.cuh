@@ -155,10 +155,11 @@ static __device__ __noinline__ bool nodes_seen(const int32_t* masks, int64_t ld_
 }
 
 // Completes a unit of rows from `start` on, of a request whose n new rows begin at row `at`; its tiles are [u.tile0,
-// u.tile0 + u.tiles) as far as there are as many. False: it has no row.
+// u.tile0 + u.tiles) as far as there are as many. False: it has no row, or, where cu_rows does not ascend, none of the
+// request's.
 template <bool kTree>
 __device__ __forceinline__ bool complete_unit(const PagedParams& p, int at, int n, int start, Unit& u) {
-  if (start >= n) return false;
+  if (start < 0 || start >= n) return false;
   u.row0 = at + start;
   u.rows = min(p.tokens, n - start);
   u.heads = min(p.heads, p.H - u.head0);
@@ -298,7 +299,7 @@ struct Line {
       start[k] = before + upto - mine;
       before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    total = before;
+    total = min(before, INT32_MAX / 2);  // as the host knows it of ranges that ascend; a worker steps beyond it
   }
 
   // The unit at `at` of the line: where it starts there, and its length. Sets the unit's request, ctx and heads;
@@ -369,7 +370,7 @@ __device__ __forceinline__ bool next_unit(const PagedParams& p, int worker, Plac
   u.tiles = max(stop - begin - line.extra, 0) - u.tile0;
   // A unit's first part is its worker's last, any other its worker's first.
   u.part = pos == begin && stop == begin + len ? -1 : pos == begin ? 2 * worker + 1 : 2 * worker;
-  u.parts = (begin + len - 1) / line.share - worker + 1;  // where this is the first
+  u.parts = min((begin + len - 1) / line.share, p.workers - 1) - worker + 1;  // where this is the first
   place.pos = stop;
   return complete_unit<kTree>(p, row, n, from, u);
 }

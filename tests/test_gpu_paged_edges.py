@@ -86,3 +86,35 @@ def test_first_tokens_of_a_context_at_the_end_of_32_bits(pages, with_ws):
     flagged()
     c.ctxs = have
     c.check(lambda b, i: list(range(64 * pages)))
+
+
+@pytest.mark.parametrize("op", ["window", "tree"])
+@pytest.mark.parametrize("H,counts,ctxs,cu", [
+    (128, [1] * 5, [900, 40, 300, 1000, 77], [0, 200, 260, 50, 60, 55]),       # shared out, or whole units in turn
+    (16, [1] * 5, [900, 40, 300, 1000, 77], [250, 0, 250, 10, 240, 3]),
+    (64, [1] * 170, [100] * 170, [(7 * b) % 251 for b in range(171)]),          # a block for each unit
+    (3, [1] * 3, [500, 500, 500], [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, -5])])
+def test_row_ranges_that_do_not_ascend_stay_inside(op, H, counts, ctxs, cu):
+    """Such a call's results mean nothing, but it ends, and touches none but the rows that some range names."""
+    c = Case(H, counts, ctxs, 64, seed=51, extra_pages=20)
+    T, rows = 270, 261
+    c.q = torch.randn(T, H, 576, device=DEV).bfloat16()
+    out, lse = torch.full((T, H, 512), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((T, H), 7.0, device=DEV)
+    mask = torch.full((T, 1), -1, dtype=torch.int32, device=DEV)[:rows]
+    n = idx.idx_paged_attention_workspace_bytes(rows, len(counts), H)
+    for ws in (None, torch.empty(n + 4096, dtype=torch.uint8, device=DEV)):
+        guard = None if ws is None else ws[n:].fill_(171)
+        part = None if ws is None else ws[:n]
+        if op == "window":
+            idx.idx_window_attention(c.q[:rows], c.cache, 64, c.block_table, i32(cu), i32(c.ctxs), out[:rows], 0.07, 2 ** 20, lse=lse[:rows], ws=part)
+        else:
+            idx.idx_tree_attention(c.q[:rows], c.cache, 64, c.block_table, i32(cu), i32(c.ctxs), mask, out[:rows], 0.07, lse=lse[:rows], ws=part)
+        idx.idx_device_error()
+        last = min(max(cu), rows)
+        assert (out[last:] == 7).all() and (lse[last:] == 7).all()
+        assert guard is None or (guard == 171).all()
+    # the next call is right
+    c = Case(H, counts, ctxs, 64, seed=52, extra_pages=20)
+    c.window(100, 3, ws=c.workspace())
+    idx.idx_device_error()
+    c.check(c.window_seen(100, 3))
