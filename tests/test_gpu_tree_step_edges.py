@@ -7,6 +7,7 @@ import torch
 import sparse_attention_indexer_fp8_gb300 as idx
 from oracle import paged as P
 from sparse_attention_indexer_fp8_gb300.pipeline import TreeStep
+from test_gpu_tree_step import Server
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -83,3 +84,41 @@ def test_a_refused_plan_takes_no_blocks():
     idx.idx_device_error()
     assert step.ctx_lens.tolist() == [20, 10] and step.held_pages.tolist() == [2, 1] and step.free_end.item() == 3
     assert table[:, :3].tolist() == [[0, 1, -1], [2, -1, -1]]
+
+
+@pytest.mark.parametrize("H,graph", [(16, False), (16, True), (128, True)])
+def test_a_step_over_contexts_that_are_cut(H, graph):
+    """Prompts long enough that the step's attention shares its work out, then drafted trees over them; captured, too."""
+    B, lens = 3, [900, 300, 1000]
+    s = Server(B, H, 16, sum(lens) + 5, 1200 // 16, seed=H)
+    s.step = TreeStep(B, s.rows, H, words=32, block_size=16, device=DEV)
+    s.cos_sin = torch.cat([s.cos_sin] * 3)
+    s.run([list(range(-1, n - 1)) for n in lens], s.random(sum(lens), 576))
+    held, end = s.step.held_pages.clone(), s.step.free_end.clone()
+    s.cached += lens
+    rows = 30
+    st = s.step = TreeStep(B, rows, H, words=1, block_size=16, device=DEV)
+    s.rows = rows
+    cached, new, parents = i32(s.cached), i32([0] * B), i32([0] * rows)
+    kv, q = s.random(rows, 576), 2 * s.random(rows, H, 576)
+
+    def run():
+        st.plan(cached, new, parents, s.free, s.table, held_pages=held, free_start=end)
+        st.layer(kv, s.weight, s.cos_sin, q, s.cache, s.table)
+
+    run()
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+    for counts in ([3, 0, 12], [10, 10, 10], [0, 1, 0], [1, 1, 1]):
+        trees = [[-1] * min(n, 1) + [int(s.rng.integers(-1, i)) for i in range(1, n)] for n in counts]
+        new.copy_(i32(counts))
+        parents.copy_(i32(sum(trees, []) + [0] * (rows - sum(counts))))
+        st.out.fill_(3)
+        st.ws.fill_(255)
+        g.replay() if graph else run()
+        idx.idx_device_error()
+        assert (st.ws != 255).any()  # every worker noted its cut
+        s.check(trees, q)
