@@ -494,7 +494,7 @@ def idx_build_tables(cached_lens, new_lens, free_blocks, block_table, block_size
           per_request("held_pages", held_pages), B, _vec(fn, "free_blocks", free_blocks, dev, i32, n_free),
           _int32(fn, "free_blocks' length", n_free),
           None if free_start is None else _vec(fn, "free_start", free_start, dev, i32, 1), bt, ld_bt,
-          block_table.shape[1], block_size, _vec(fn, "ctx_lens", ctx_lens, dev, i32, B),
+          block_table.shape[1], _int32(fn, "block_size", block_size), _vec(fn, "ctx_lens", ctx_lens, dev, i32, B),
           _vec(fn, "cu_rows", cu_rows, dev, i32, B + 1),
           None if cu_ctx is None else _vec(fn, "cu_ctx", cu_ctx, dev, i32, B + 1), per_request("held_out", held_out),
           None if free_end is None else _vec(fn, "free_end", free_end, dev, i32, 1),
