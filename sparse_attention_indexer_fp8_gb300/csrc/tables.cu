@@ -48,9 +48,11 @@ struct TableParams {
 // writes before all have read: one block needs its own barrier for that, several are one cluster. A slot
 // in a fresh page comes from free_blocks, not from the table, which another block writes.
 //
-// One block up to 2048 rows, 3.5 us for a decode step of 128 requests; a cluster of eight above. With a cluster
-// always, 892 rows take 4.5 us instead of 4.1, 1612 rows 4.7 instead of 5.0, 2420 rows 5.1 instead of one block's 6.2,
-// 44216 rows of 256 requests 9.7 instead of 39.2 (1.3 MB written there; the bisections' shared-memory reads bound it).
+// One block while every thread has one row and one request at most, 3.4 us for a decode step of 128 requests; a cluster of
+// eight above. One block and a cluster take, for 900 rows of 16 requests 3.9 and 4.3 us, for 1152 4.7 and 4.5, for 2048
+// 5.0 and 4.6; for 900 requests of a row 5.7 and 6.1 us, for 1152 8.3 and 7.9, for 2047 9.4 and 8.5; one request of 1152 to
+// 1408 rows alone is better off in one block (4.1 and 4.2 us). 44216 rows of 256 requests take 39.2 and 9.6 us (1.3 MB
+// written there; the bisections' shared-memory reads bound it).
 // ---------------------------------------------------------------------------
 constexpr int kClusterBlocks = 8;  // the portable cluster size
 constexpr int kMaxTableThreads = 1024;
@@ -320,8 +322,8 @@ extern "C" idx_status_t idx_build_tables(const int32_t* cached_lens, const int32
   p.row_to_req = row_to_req;
   p.row_ke = row_ke;
   p.n_rows = n_rows;
-  const int most = std::max(B + 1, n_rows);
-  const bool cluster = most > 2 * kMaxTableThreads;
+  const int most = std::max(B, n_rows);
+  const bool cluster = most > kMaxTableThreads;
   const int threads = std::min(kMaxTableThreads, (std::max(most, 64) + 31) / 32 * 32);
   const size_t smem = table_smem_bytes(B);
   auto* kernel = cluster ? build_tables_kernel<true> : build_tables_kernel<false>;
