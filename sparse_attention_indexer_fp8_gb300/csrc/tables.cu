@@ -324,7 +324,7 @@ extern "C" idx_status_t idx_build_tables(const int32_t* cached_lens, const int32
   p.n_rows = n_rows;
   const int most = std::max(B, n_rows);
   const bool cluster = most > kMaxTableThreads;
-  const int threads = std::min(kMaxTableThreads, (std::max(most, 64) + 31) / 32 * 32);
+  const int threads = (std::min(std::max(most, 64), kMaxTableThreads) + 31) / 32 * 32;
   const size_t smem = table_smem_bytes(B);
   auto* kernel = cluster ? build_tables_kernel<true> : build_tables_kernel<false>;
   if (smem > kTableSmemUnasked) {

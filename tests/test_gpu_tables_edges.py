@@ -115,3 +115,14 @@ def test_tree_mask_rows_of_any_bounds(cu, written):
     for i, r in enumerate(written):
         want[r] = 1 << i
     assert mask[:, 0].tolist() == want and pos.tolist() == [3 if r in written else -9 for r in range(6)]
+
+
+def test_the_most_rows():
+    """As many rows as 32 bits count, nearly all of them padding."""
+    rows = 2 ** 31 - 1
+    pos, slots = torch.full((rows,), 7, dtype=torch.int32, device=DEV), torch.full((rows,), 7, dtype=torch.int64, device=DEV)
+    t, ctx, cu = i32([[3]]), i32([0]), i32([0, 0])
+    idx.idx_build_tables(i32([10]), i32([4]), i32([5]), t, 16, ctx, cu, pos, slots)
+    idx.idx_device_error()
+    assert pos[:5].tolist() == [10, 11, 12, 13, 0] and slots[:5].tolist() == [58, 59, 60, 61, -1]
+    assert not pos[5:].any() and slots[5:].max().item() == -1 and slots[5:].min().item() == -1
