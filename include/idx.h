@@ -837,7 +837,9 @@ idx_status_t idx_tree_mask(const int32_t* parents, const int32_t* cu_rows, int32
  *   window >= 1, sinks >= 0.
  *   ws           NULL, or idx_paged_attention_workspace_bytes(T, B, H) bytes, 16-byte aligned: with it the work of
  *                up to 160 requests may be shared out evenly over the GPU's SMs, by the lengths on the device; rows
- *                whose contexts that cuts are joined by a second launch. Its contents need no preparation and mean
+ *                whose contexts that cuts are joined by a second launch. Every row of the block table counts, of
+ *                requests without rows too: with 161 no bytes are needed and no context is cut, so a padded batch of few live requests with long
+ *                contexts is better kept within 160. Its contents need no preparation and mean
  *                nothing after the call; calls that may overlap need one each. The results depend on the lengths of
  *                all requests in the last bits then, and are the same in every run.
  * Errors: as idx_sparse_attention, IDX_ERR_INVALID_ARG for window < 1 or sinks < 0, and IDX_ERR_UNSUPPORTED for rows,

@@ -176,7 +176,7 @@ int64_t most_tiles_of(const PagedParams& p, const Plan& plan, bool tree) {
 // 6 us). Few units are cut: 8 requests of 4 rows and 16 heads take 16.6 us shared and 19.1 us plain with 8 tiles, 15.3 and
 // 13.2 with 4; 76 windows of 4096 tokens and 64 heads 69 and 104 us, 16 of 1024 21 and 33 us. Of more units only the uneven
 // ends are gained, and windows are as long as one another (128 of 4096 tokens: 120 and 107 us). 64 requests of 8 rows and
-// 64 heads take 447 and 506 us with 128 tiles at most, 148 and 146 with 32, 100 and 85 with 16.
+// 64 heads take 443 and 505 us with 128 tiles at most, 148 and 146 with 32, 100 and 85 with 16.
 bool worth_cutting(const PagedParams& p, const Plan& plan, bool tree) {
   const int64_t units = std::min(static_cast<int64_t>(p.T) * plan.head_blocks, plan.units);
   const bool few = 2 * units <= plan.workers;
@@ -186,8 +186,8 @@ bool worth_cutting(const PagedParams& p, const Plan& plan, bool tree) {
 }
 
 // Whether a block for each SM, which takes units in turn and finds the next while it finishes one, is faster than a block
-// for each unit: chunks of four prompts, 128 heads, a window of 1024 take 626 us, and some 5 % more with a block each; four prompts of
-// 512 rows 266 and 307 us. Long contexts are left to the order in which blocks become free: 64 trees of 8 nodes and 64
+// for each unit: chunks of four prompts, 128 heads, a window of 1024 take 629 us, and some 5 % more with a block each;
+// four prompts of 512 rows 266 and 307 us. Long contexts are left to the order in which blocks become free: 64 trees of 8 nodes and 64
 // heads with up to 128 tiles take 539 us in turn and 506 with a block each, with 16 tiles 83 and 86, with 8 tiles 51 and 58.
 bool worth_sharing(const PagedParams& p, const Plan& plan, bool tree) {
   return plan.units > plan.workers && (!tree || most_tiles_of(p, plan, tree) < 32);

@@ -30,10 +30,10 @@ namespace block {
 // (store 2000 clocks, S 1200, softmax 1300, O 850, and the other stage's S between) takes what two tiles take. A block's
 // first unit starts in some 8000 clocks (lengths, table, first tokens and Q are four round trips), a later one in 4300,
 // and a unit ends in some 5000.
-// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 626 us (37 % of the bf16 rate); 64 trees of 4
-// to 8 nodes, 64 heads, contexts of 4096 to 8192: 447 us (44 %); one tree of 8 nodes, 128 heads, 32768 tokens: 102 us
-// (38 %). Pairs of blocks on one product of M = 256 with half of the values' dims each (full rate, but S twice) took
-// 699, 484 and 96 us, and lost more in units that are not full. Copies of Q and position dims by the threads added 1 %
+// Measured: four chunks of 256 to 512 rows, 128 heads, a window of 1024: 629 us (37 % of the bf16 rate); 64 trees of 4
+// to 8 nodes, 64 heads, contexts of 4096 to 8192: 443 us (44 %); one tree of 8 nodes, 128 heads, 32768 tokens: 103 us
+// (37 %). Pairs of blocks on one product of M = 256 with half of the values' dims each (full rate, but S twice) took
+// 703, 488 and 97 us, and lost more in units that are not full. Copies of Q and position dims by the threads added 1 %
 // to the chunks (a 16-byte copy is an access for every 32 bytes), S and O in halves that overlap the stores 2 %, results
 // stored by bulk copies 1 %.
 // ---------------------------------------------------------------------------

@@ -10,7 +10,8 @@ of the rank's own shard, local top-k with scores, one exchange, merge).
 ``AttentionDecodeStep`` goes from a layer's projections to its attention output
 (both normalised inserts, q preparation, ``DecodeStep``, sparse attention).
 ``TreeStep`` verifies trees of drafted tokens: tables and masks once a step, then a
-layer's insert and its attention over whole contexts. Buffers are allocated once at construction; ``run`` allocates nothing but the exchange's
+layer's insert and its attention over whole contexts. Buffers are allocated once
+at construction; ``run`` allocates nothing but the exchange's
 receive lists. ``kv="mxfp4"`` selects the MXFP4 indexer cache (the V4.1 format)
 for the cache fill and the decode and hierarchical steps.
 """
@@ -22,12 +23,11 @@ import contextlib
 import numpy as np
 import torch
 
-from . import (idx_build_tables, idx_dcp_topk_merge, idx_expand_candidates, idx_k_norm_rope_quant_and_cache, idx_k_quant_and_cache,
-               idx_k_quant_and_cache_mxfp4, idx_kv_norm_rope_quant_and_cache, idx_paged_mqa_logits_decode,
-               idx_paged_attention_workspace_bytes, idx_paged_mqa_logits_decode_mxfp4, idx_q_rope_quant, idx_req_to_global_slots, idx_sparse_attention,
-               idx_sparse_attention_workspace_bytes, idx_sparse_topk_remap, idx_topk, idx_tree_attention, idx_tree_mask,
-               idx_workspace_bytes,
-               _heads, _mat, _vec)
+from . import (idx_build_tables, idx_dcp_topk_merge, idx_expand_candidates, idx_k_norm_rope_quant_and_cache,
+               idx_k_quant_and_cache, idx_k_quant_and_cache_mxfp4, idx_kv_norm_rope_quant_and_cache,
+               idx_paged_attention_workspace_bytes, idx_paged_mqa_logits_decode, idx_paged_mqa_logits_decode_mxfp4,
+               idx_q_rope_quant, idx_req_to_global_slots, idx_sparse_attention, idx_sparse_attention_workspace_bytes,
+               idx_sparse_topk_remap, idx_topk, idx_tree_attention, idx_tree_mask, idx_workspace_bytes, _heads, _mat, _vec)
 from . import workloads as W
 
 
@@ -273,15 +273,21 @@ class TreeStep:
 
     ``plan`` prepares a step from the requests' lengths and the nodes' parents, once for all layers: blocks and slots
     of the new tokens, their positions (the request's length and the node's depth) and who sees whom. ``layer`` inserts
-    a layer's new tokens and attends to every request's earlier tokens and each node's ancestors. A prompt, or tokens
-    that an earlier step accepted, are nodes whose parent is the one before (32 ``words`` nodes a request at most; longer
-    prompts go through ``idx_window_attention``); the records of dropped nodes are
-    overwritten, and their blocks used again, by the next step over the same ``cached_lens``. Rows behind the last
-    node are padding. Neither call allocates anything.
+    a layer's new tokens and attends to every request's earlier tokens and each node's ancestors. A prompt is nodes whose
+    parent is the one before (32 ``words`` nodes a request at most; longer prompts go through ``idx_window_attention``).
+
+    Records lie in the order of the tree. Accepted nodes that are its first, each the child of the one before, are where the
+    sequence wants them: the next step's ``cached_lens`` count them. Any other accepted path is brought again by the next
+    step, as a chain before its tree, and costs as many rows once more. The records of dropped nodes are overwritten, and
+    their blocks used again, by the next step over the same ``cached_lens``. Rows behind the last node are padding.
+
+    Up to 160 ``requests``, those that sit a step out among them, the attention shares its work out evenly over the GPU;
+    with more, a step of few live requests with long contexts takes several times as long. Neither call allocates anything.
     """
 
-    def __init__(self, requests: int, rows: int, heads: int, words: int = 2, block_size: int = W.BLOCK_SIZE, device="cuda",
-                 softmax_scale: float = W.ATTN_HEAD_DIM ** -0.5, eps: float = 1e-6, interleaved: bool = False):
+    def __init__(self, requests: int, rows: int, heads: int, words: int = 2, block_size: int = W.BLOCK_SIZE,
+                 device="cuda", softmax_scale: float = W.ATTN_HEAD_DIM ** -0.5, eps: float = 1e-6,
+                 interleaved: bool = False):
         # what the second call of ``plan`` or ``layer`` would refuse, when the first is enqueued already
         for name, value, most in (("requests", requests, 8192), ("heads", heads, 1024), ("words", words, 32)):
             if not (name == "words") <= value <= most:
@@ -306,7 +312,8 @@ class TreeStep:
             nbytes = idx_paged_attention_workspace_bytes(rows, requests, heads)
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
-    def plan(self, cached_lens, new_lens, parents, free_blocks, block_table, held_pages=None, free_start=None, stream=None):
+    def plan(self, cached_lens, new_lens, parents, free_blocks, block_table, held_pages=None, free_start=None,
+             stream=None):
         """Lengths and ``held_pages`` int32 [requests], ``parents`` int32 [rows] (within the request, -1: none);
         ``block_table`` is updated. ``cached_lens``, ``held_pages`` and ``free_start`` may be the step's own ``ctx_lens``,
         ``held_pages`` and ``free_end``, which go on from step to step then. See ``idx_build_tables`` and ``idx_tree_mask``."""
@@ -332,7 +339,8 @@ class TreeStep:
         _mat(fn, "block_table", block_table, dev, torch.int32, self.ctx_lens.shape[0], None)
         ptr, ld, ld_head = _heads(fn, "q", q, dev, rows, heads, W.ATTN_DIM)
         if ptr % 16 or ld % 8 or ld_head % 8 or min(ld, ld_head) < W.ATTN_DIM:
-            raise ValueError(f"{fn}: q's rows and heads must begin at 16-byte boundaries and not overlap, its strides are {q.stride()}")
+            raise ValueError(f"{fn}: q's rows and heads must begin at 16-byte boundaries and not overlap, "
+                             f"its strides are {q.stride()}")
         idx_kv_norm_rope_quant_and_cache(kv[:, :512], kv[:, 512:], kv_weight, self.eps, self.positions, cos_sin, self.slots,
                                          kv_cache, self.block_size, interleaved=self.interleaved, stream=stream)
         idx_tree_attention(q, kv_cache, self.block_size, block_table, self.cu_rows, self.ctx_lens, self.mask, self.out,

@@ -122,3 +122,33 @@ def test_a_step_over_contexts_that_are_cut(H, graph):
         idx.idx_device_error()
         assert (st.ws != 255).any()  # every worker noted its cut
         s.check(trees, q)
+
+
+def test_an_accepted_chain_stays_where_it_is():
+    """Nodes accepted from the first on, each the child of the one before, are counted by the next step and not brought again."""
+    B, H, bs = 2, 16, 16
+    s = Server(B, H, bs, rows=80, pages=10, seed=21)
+    lens = [20, 7]
+    kv = s.random(sum(lens), 576)
+    s.run([list(range(-1, n - 1)) for n in lens], kv)
+    tokens = list(torch.split(kv, lens))
+    s.cached += lens
+    for keep in ((4, 1), (6, 0), (2, 5)):
+        # a chain of six and, for the second request, siblings behind it
+        trees = [list(range(-1, 5)), list(range(-1, 5)) + [2, 2, -1]]
+        kv = s.random(sum(len(t) for t in trees), 576)
+        q = s.run(trees, kv)
+        s.check(trees, q)
+        parts = torch.split(kv, [len(t) for t in trees])
+        for b in range(B):
+            tokens[b] = torch.cat([tokens[b], parts[b][:keep[b]]])
+            s.cached[b] += keep[b]
+    for b in range(B):
+        n = int(s.cached[b])
+        fresh = torch.zeros((10, s.cache.shape[1]), dtype=torch.uint8, device=DEV)
+        pos = torch.arange(n, dtype=torch.int32, device=DEV)
+        x = tokens[b].contiguous()
+        idx.idx_kv_norm_rope_quant_and_cache(x[:, :512], x[:, 512:], s.weight, 1e-6, pos, s.cos_sin, pos.long(), fresh, bs)
+        got = P.context(s.cache.cpu().numpy(), bs, s.table[b].tolist(), n)
+        assert np.array_equal(got, P.context(fresh.cpu().numpy(), bs, range(10), n))
+    idx.idx_device_error()
